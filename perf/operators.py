@@ -231,7 +231,8 @@ def _store_plain(codes, scale, x, start):
     if start > t0:      # earlier tokens of the first block
         old = codes[:, :, t0:start].float() * scale[:, :, b0, None, None]
         blk[:, :, 0, :start - t0] = old
-        s[:, :, 0] = torch.where(s[:, :, 0] > scale[:, :, b0], s[:, :, 0], scale[:, :, b0])
+        some = x[:, :, :t0 + BLOCK - start].float().abs().amax((-1, -2)) > 0
+        s[:, :, 0] = torch.where(some & (s[:, :, 0] > scale[:, :, b0]), s[:, :, 0], scale[:, :, b0])
     new = (blk / s[..., None, None]).to(torch.float8_e4m3fn).reshape(B, H, t1 - t0, d)
     codes[:, :, t0:start + n] = new[:, :, :start - t0 + n]
     scale[:, :, b0:b1] = s
@@ -345,7 +346,7 @@ def _exact_store(codes, scale, x, start):
         s[some] = 2.0 ** np.maximum(np.ceil(np.log2(top[some] / 448.0)), -126.0)
         if lo > blk * BLOCK:
             before = scale[:, :, blk].copy()
-            s = np.maximum(s, before)
+            s = np.where(some, np.maximum(s, before), before)
             old = codes[:, :, blk * BLOCK:lo] * before[:, :, None, None]
             codes[:, :, blk * BLOCK:lo] = _e4m3_grid(old / s[:, :, None, None])
         codes[:, :, lo:hi] = _e4m3_grid(piece / s[:, :, None, None])
