@@ -222,6 +222,121 @@ double npa_multidiffusion_useful_flops(int B, int heads, int H, int W, int d, in
 npa_status asg_guidance_combine(const void *eps, const void *eps_ref, const void *mask, void *out, int n_patches,
                                 int B, int C, int S, float w_t, npa_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The steps of a diffusion block around its self-attention: cross attention
+ * to an encoder's states (16-bit, or held in an 8-bit cache over the denoising
+ * steps) and the group norm in front of it. The pages leave these parts of
+ * the network as they are and have no passage on them; the definitions are
+ * stated at each declaration. Forward only, as everything here.
+ * ------------------------------------------------------------------------- */
+
+typedef enum { NPA_DTYPE_BF16 = 0, NPA_DTYPE_FP16 = 1, NPA_DTYPE_FP32 = 2 } npa_dtype;
+
+/* Strides, in elements, of a [B, heads, L, d] tensor whose d elements are
+ * contiguous. A projection's output [B, L, heads * d] is {L * heads * d, d,
+ * heads * d}. Each must be a multiple of 8 (NPA_ERR_MISALIGNED) and not
+ * negative, and the token stride at least d (NPA_ERR_INVALID_ARG); an input's
+ * batch or head stride may be 0 (every row reads the same states), an
+ * output's elements must not coincide. The stride of an axis with one entry
+ * is not read. A NULL pointer stands for a contiguous tensor. */
+typedef struct {
+    int64_t batch, head, token;
+} npa_strides;
+
+/* Cross attention forward:
+ *   o[b, h, i] = sum_j p_ij v[b, h', j],  p_ij = softmax_j(scale * q[b, h, i] . k[b, h', j]),
+ * over the keys j that batch row b keeps: j < kv_lens[b] and key_mask[b, j] !=
+ * 0; h' = h / (heads / kv_heads), so groups of query heads may share keys. A
+ * query without kept keys gets zeros. q, o: [B, heads, Lq, d]; k, v: [B,
+ * kv_heads, Lk, d], bfloat16 or float16 (`dtype`, all four alike), with the
+ * strides above; kv_lens: int32 [B] (device; values outside 0..Lk are
+ * clamped) or NULL; key_mask: one byte per key, [B, Lk] contiguous (device) or
+ * NULL. What k and v hold at keys that are not kept does not reach o, NaN and
+ * infinities included. scale > 0, or 0 for 1/sqrt(d). d is 64 or 128; Lq and
+ * Lk are any sizes >= 1.
+ * Arithmetic as for npa_attention_fwd; float16 inputs keep their probabilities
+ * in float16 for the P.V product.
+ * When the queries alone would leave multiprocessors idle, the key range is
+ * split over them: partial results go to `workspace` (caller-owned device
+ * memory, 16-byte aligned; npa_cross_attention_workspace_size() bytes for the
+ * planned split count, and a smaller or NULL workspace gives fewer or no
+ * splits) and a second kernel on the same stream merges them. Calls that
+ * overlap on the GPU need workspaces of their own. o and the workspace must
+ * not overlap each other or an input (address ranges, gaps between strided
+ * rows included). */
+npa_status npa_cross_attention_fwd(const void *q, const void *k, const void *v, void *o, npa_dtype dtype, int B,
+                                   int heads, int kv_heads, int Lq, int Lk, int d, const npa_strides *q_strides,
+                                   const npa_strides *k_strides, const npa_strides *v_strides,
+                                   const npa_strides *o_strides, const int32_t *kv_lens, const uint8_t *key_mask,
+                                   float scale, void *workspace, size_t workspace_bytes, npa_stream_t stream);
+
+/* Workspace bytes npa_cross_attention_fwd and npa_kv8_cross_attention_fwd use
+ * for their planned split count on the current device (0: none needed, or
+ * invalid arguments). */
+size_t npa_cross_attention_workspace_size(int B, int heads, int Lq, int Lk, int d);
+
+/* Keys and values held in 8 bits: e4m3 codes (1-4-3, largest 448) with one
+ * float32 scale for each block of 64 tokens of a head, value = code * scale.
+ * k, v: one byte per element, [B, kv_heads, capacity, d]; k_scale, v_scale:
+ * float32 [B, kv_heads, capacity / 64]; all contiguous device memory, 16-byte
+ * aligned; capacity is a multiple of 64. */
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int capacity;
+} npa_kv8_cache;
+
+/* Writes n_tokens keys and values, k, v: [B, kv_heads, n_tokens, d] (bfloat16
+ * or float16, strides as above), into the cache from token `start` on, or from
+ * starts[b] in batch row b (int32 [B], device; `start` is then not read, and
+ * tokens that would lie outside 0..capacity-1 are not written). Per block of
+ * 64 tokens and head the scale is the smallest power of two s >= 2^-126 with
+ * amax / s <= 448 (amax: largest finite magnitude among the block's written
+ * tokens; 1 when that is 0), and code = x / s rounded to the nearest e4m3
+ * number, ties to even; infinities become +-448, NaN stays NaN. When the first
+ * written token lies inside a block, the block's earlier tokens keep their
+ * values: its scale is the larger of the old one and the new tokens', and if
+ * it grows, the earlier codes are rounded again at it. Codes of tokens after
+ * the last written one are left as they were (in a block whose scale is set
+ * anew they then stand for other values). */
+npa_status npa_kv8_store(const void *k, const void *v, const npa_kv8_cache *cache, npa_dtype dtype, int B,
+                         int kv_heads, int d, int start, const int32_t *starts, int n_tokens,
+                         const npa_strides *k_strides, const npa_strides *v_strides, npa_stream_t stream);
+
+/* npa_cross_attention_fwd over the first Lk tokens of an 8-bit cache (Lk <=
+ * capacity); q and o are bfloat16. code * scale enters the products rounded
+ * to bfloat16, which is exact for the scales npa_kv8_store writes. Other
+ * arguments, results, workspace and errors as for npa_cross_attention_fwd. */
+npa_status npa_kv8_cross_attention_fwd(const void *q, const npa_kv8_cache *cache, void *o, int B, int heads,
+                                       int kv_heads, int Lq, int Lk, int d, const npa_strides *q_strides,
+                                       const npa_strides *o_strides, const int32_t *kv_lens, const uint8_t *key_mask,
+                                       float scale, void *workspace, size_t workspace_bytes, npa_stream_t stream);
+
+typedef enum { NPA_ACT_NONE = 0, NPA_ACT_SILU = 1 } npa_activation;
+
+/* Group norm with an activation, channels last:
+ *   y[b, n, c] = act((x[b, n, c] - mean[b, g]) / sqrt(var[b, g] + eps) * weight[c] + bias[c]),
+ * g = c / (C / groups), mean and (biased) variance over the N tokens and the
+ * C / groups channels of group g; act: none, or SiLU, z / (1 + e^-z). x, y:
+ * [B, N, C], C contiguous, batch and token strides in elements (token strides
+ * >= C; y's elements must not coincide); bfloat16, float16 or float32.
+ * weight, bias: [C], of x's type or float32 (`weight_dtype`), or NULL for 1
+ * and 0. groups divides C; C <= 4096. Statistics and arithmetic in float32.
+ * y may be x itself (same strides) but must not otherwise overlap an input.
+ * `workspace`: caller-owned device memory, 16-byte aligned, at least
+ * npa_group_norm_workspace_size() bytes, not overlapping any other buffer
+ * (NPA_ERR_INVALID_ARG when NULL or short); calls that overlap on the GPU need
+ * workspaces of their own. Pointers need their element's alignment only;
+ * 16-byte aligned rows (C and the strides multiples of 16 bytes) run fastest. */
+npa_status npa_group_norm_act(const void *x, const void *weight, const void *bias, void *y, npa_dtype dtype,
+                              npa_dtype weight_dtype, int B, int N, int C, int groups, int64_t x_batch_stride,
+                              int64_t x_token_stride, int64_t y_batch_stride, int64_t y_token_stride, float eps,
+                              npa_activation act, void *workspace, size_t workspace_bytes, npa_stream_t stream);
+
+/* Workspace bytes of npa_group_norm_act on the current device (0 for invalid
+ * arguments). */
+size_t npa_group_norm_workspace_size(npa_dtype dtype, int B, int N, int C, int groups);
+
 /* Workspace bytes npa_global_query_attention_fwd uses for its full split
  * count on the current device (0: no split needed, or invalid arguments). */
 size_t npa_global_query_workspace_size(int B, int heads, int H, int W, int d, int G);

@@ -371,3 +371,97 @@ def asg_guidance_combine(eps, eps_ref, mask, w_t: float) -> np.ndarray:
     if e.ndim != 4 or r.shape != e.shape[1:] or m.shape != (e.shape[0], e.shape[1], e.shape[3]):
         raise ValueError("shapes: eps [n, B, C, S], eps_ref [B, C, S], mask [n, B, S]")
     return e + float(w_t) * m[:, :, None, :] * (r[None] - e)
+
+
+# ---------------------------------------------------------------------------
+# The steps around the self-attention (no passage in the pages: the
+# definitions are those of the library's header)
+# ---------------------------------------------------------------------------
+
+def cross_attention(q, k, v, *, keep=None, scale: Optional[float] = None):
+    """softmax(scale * q k^T) v in float64, one query set, batch row and head
+    at a time. q: float64 [B, heads, Lq, d]; k, v: [B, kv_heads, Lk, d]; keep:
+    truth values [B, Lk] (None: all keys). A row without keys gives zeros;
+    unkept keys are never touched. Returns the output and, for error bounds,
+    sum_j p_ij |v_j|."""
+    q, k, v = (np.asarray(x, dtype=np.float64) for x in (q, k, v))
+    B, heads, Lq, d = q.shape
+    per = heads // k.shape[1]
+    c = 1.0 / np.sqrt(d) if scale is None else scale
+    out, mag = np.zeros(q.shape), np.zeros(q.shape)
+    for b in range(B):
+        pick = np.arange(k.shape[2]) if keep is None else np.flatnonzero(keep[b])
+        if pick.size == 0:
+            continue
+        for h in range(heads):
+            kk, vv = k[b, h // per, pick], v[b, h // per, pick]
+            z = (q[b, h] @ kk.T) * c
+            w = np.exp(z - z.max(axis=1, keepdims=True))
+            w /= w.sum(axis=1, keepdims=True)
+            out[b, h], mag[b, h] = w @ vv, w @ np.abs(vv)
+    return out, mag
+
+
+def e4m3_round(x) -> np.ndarray:
+    """float64 to the nearest e4m3 number (ties to even; 3 fraction bits, least
+    normal exponent -6, largest 448; beyond it +-448, NaN stays)."""
+    x = np.asarray(x, dtype=np.float64)
+    a = np.minimum(np.abs(x), 448.0)
+    _, e = np.frexp(np.where(np.isnan(a) | (a == 0), 1.0, a))    # a = m 2^e, 1/2 <= m < 1
+    step = np.ldexp(1.0, np.maximum(e - 1, -6) - 3)
+    return np.copysign(np.rint(a / step) * step, x)
+
+
+def kv8_scale(amax: float) -> float:
+    """Smallest power of two s >= 2^-126 with amax / s <= 448; 1 for 0."""
+    if amax == 0:
+        return 1.0
+    s = 2.0 ** -126
+    while amax / s > 448.0:
+        s *= 2.0
+    return s
+
+
+def kv8_store(codes, scale, x, start: int, block: int = 64) -> None:
+    """Writes x (float64 [heads, n, d]) into one batch row's cache in place:
+    codes (float64 values [heads, capacity, d]) and scale [heads, capacity /
+    block], from token ``start`` on; tokens outside the cache are dropped."""
+    heads, cap, _ = codes.shape
+    lo, hi = max(start, 0), min(start + x.shape[1], cap)
+    if lo >= hi:
+        return
+    for blk in range(lo // block, (hi - 1) // block + 1):
+        t0 = blk * block
+        a, b = max(lo, t0), min(hi, t0 + block)
+        for h in range(heads):
+            piece = x[h, a - start:b - start]
+            amax = float(np.max(np.abs(piece[np.isfinite(piece)]), initial=0.0))
+            if a > t0:
+                old = scale[h, blk]
+                s = max(old, kv8_scale(amax)) if amax > 0 else old
+                if s != old:
+                    codes[h, t0:a] = e4m3_round(codes[h, t0:a] * old / s)
+            else:
+                s = kv8_scale(amax)
+            codes[h, a:b] = e4m3_round(piece / s)
+            scale[h, blk] = s
+
+
+def group_norm(x, groups: int, weight=None, bias=None, eps: float = 1e-5, act: Optional[str] = None):
+    """Group norm of x (float64 [B, N, C]) over tokens and the channels of a
+    group, then the activation. Returns y and the bound terms (z, |mean| *
+    rstd * |w|): the value before the activation, and how an error of the mean
+    relative to itself shows in it."""
+    x = np.asarray(x, dtype=np.float64)
+    B, N, C = x.shape
+    g = x.reshape(B, N, groups, C // groups)
+    mean = g.mean(axis=(1, 3), keepdims=True)
+    rstd = 1.0 / np.sqrt(np.square(g - mean).mean(axis=(1, 3), keepdims=True) + eps)
+    w = np.ones(C) if weight is None else np.asarray(weight, dtype=np.float64)
+    b = np.zeros(C) if bias is None else np.asarray(bias, dtype=np.float64)
+    z = ((g - mean) * rstd).reshape(B, N, C) * w + b
+    lift = np.broadcast_to(np.abs(mean * rstd), g.shape).reshape(B, N, C) * np.abs(w)
+    if act == "silu":
+        with np.errstate(over="ignore"):
+            return z / (1.0 + np.exp(-z)), z, lift
+    return z, z, lift

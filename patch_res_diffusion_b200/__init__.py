@@ -23,14 +23,22 @@ a call fails, an exception is raised.
   mean over the windows that contain it.
 * ``asg_guidance_combine`` - asynchronous structure guidance (ASGDiffusion
   review, "core_discovery"): eps + w_t * M * (eps_ref - eps) per patch.
+* ``npa_cross_attention_fwd`` - cross attention of image tokens (or a few
+  latent queries) to an encoder's states of another length.
+* ``npa_kv8_store`` and ``npa_kv8_cross_attention_fwd`` - a key/value cache in
+  e4m3 with a power-of-two scale per 64 tokens and head, and the attention
+  over it.
+* ``npa_group_norm_act`` - group norm with an activation, channels last.
 
 The lower-case helpers (``npa_attention``, ``pcpp_attention``,
 ``pcpp_attention_stale``, ``global_query_attention``,
-``multidiffusion_attention``, ``asg_combine``) take torch CUDA tensors and
-allocate outputs and workspaces; the computation is the same C call.
+``multidiffusion_attention``, ``asg_combine``, ``cross_attention``,
+``kv8_store``, ``kv8_cross_attention``, ``group_norm``) take torch CUDA tensors
+and allocate outputs and workspaces; the computation is the same C call.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -45,6 +53,10 @@ __all__ = [
     "npa_multidiffusion_attention_fwd", "npa_multidiffusion_workspace_size", "npa_multidiffusion_useful_flops",
     "multidiffusion_attention", "asg_guidance_combine", "asg_combine", "EXPORTED_SYMBOLS", "DEBUG_LIB_PATH",
     "DEBUG_ONLY_SYMBOLS", "NPA_ERR_DEVICE_BOUNDS", "use_bounds_checking", "npa_debug_withhold_arrival_once",
+    "NPA_DTYPE_BF16", "NPA_DTYPE_FP16", "NPA_DTYPE_FP32", "NPA_ACT_NONE", "NPA_ACT_SILU", "KV8_BLOCK", "Kv8Cache",
+    "npa_cross_attention_fwd", "npa_cross_attention_workspace_size", "npa_kv8_store", "npa_kv8_cross_attention_fwd",
+    "npa_group_norm_act", "npa_group_norm_workspace_size", "cross_attention", "kv8_store", "kv8_cross_attention",
+    "group_norm",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnpa_b200.so")
@@ -58,12 +70,21 @@ NPA_ERR_CUDA = 4
 NPA_ERR_DEVICE_TIMEOUT = 5
 NPA_ERR_DEVICE_BOUNDS = 6
 
+NPA_DTYPE_BF16 = 0
+NPA_DTYPE_FP16 = 1
+NPA_DTYPE_FP32 = 2
+NPA_ACT_NONE = 0
+NPA_ACT_SILU = 1
+KV8_BLOCK = 64  # tokens of one head that share a scale of the 8-bit cache
+
 EXPORTED_SYMBOLS = (
     "npa_attention_fwd", "pcpp_attention_fwd", "pcpp_attention_fwd_stale", "pcpp_neighbor_rows", "npa_useful_flops",
     "pcpp_useful_flops", "npa_device_status", "npa_selftest_wait_timeout", "npa_status_string",
     "npa_global_query_attention_fwd", "npa_global_query_workspace_size",
     "npa_global_query_attention_fwd_noalloc", "npa_multidiffusion_attention_fwd",
     "npa_multidiffusion_workspace_size", "npa_multidiffusion_useful_flops", "asg_guidance_combine",
+    "npa_cross_attention_fwd", "npa_cross_attention_workspace_size", "npa_kv8_store", "npa_kv8_cross_attention_fwd",
+    "npa_group_norm_act", "npa_group_norm_workspace_size",
 )
 # exported by the bounds-checking build only
 DEBUG_ONLY_SYMBOLS = ("npa_debug_withhold_arrival_once",)
@@ -77,6 +98,15 @@ class NpaError(RuntimeError):
 
 class _GlobalKV(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_tokens", ctypes.c_int)]
+
+
+class _Strides(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("head", ctypes.c_int64), ("token", ctypes.c_int64)]
+
+
+class _Kv8Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("capacity", ctypes.c_int)]
 
 
 _LIB: Optional[ctypes.CDLL] = None
@@ -127,6 +157,19 @@ def _load(path: str) -> ctypes.CDLL:
         L.npa_multidiffusion_useful_flops.restype = d
         L.asg_guidance_combine.argtypes = [vp] * 4 + [i] * 4 + [ctypes.c_float, vp]
         L.asg_guidance_combine.restype = i
+        st, kv8, f = ctypes.POINTER(_Strides), ctypes.POINTER(_Kv8Cache), ctypes.c_float
+        L.npa_cross_attention_fwd.argtypes = [vp] * 4 + [i] * 7 + [st] * 4 + [vp, vp, f, vp, ctypes.c_size_t, vp]
+        L.npa_cross_attention_fwd.restype = i
+        L.npa_cross_attention_workspace_size.argtypes = [i] * 5
+        L.npa_cross_attention_workspace_size.restype = ctypes.c_size_t
+        L.npa_kv8_store.argtypes = [vp, vp, kv8] + [i] * 5 + [vp, i, st, st, vp]
+        L.npa_kv8_store.restype = i
+        L.npa_kv8_cross_attention_fwd.argtypes = [vp, kv8, vp] + [i] * 6 + [st, st, vp, vp, f, vp, ctypes.c_size_t, vp]
+        L.npa_kv8_cross_attention_fwd.restype = i
+        L.npa_group_norm_act.argtypes = [vp] * 4 + [i] * 6 + [ctypes.c_int64] * 4 + [f, i, vp, ctypes.c_size_t, vp]
+        L.npa_group_norm_act.restype = i
+        L.npa_group_norm_workspace_size.argtypes = [i] * 5
+        L.npa_group_norm_workspace_size.restype = ctypes.c_size_t
         L.npa_global_query_workspace_size.argtypes = [i] * 6
         L.npa_global_query_workspace_size.restype = ctypes.c_size_t
         L.pcpp_neighbor_rows.argtypes = [i, d]
@@ -251,6 +294,63 @@ def asg_guidance_combine(eps, eps_ref, mask, out, n_patches: int, B: int, C: int
     _check(lib().asg_guidance_combine(_ptr(eps), _ptr(eps_ref), _ptr(mask), _ptr(out), n_patches, B, C, S,
                                       float(w_t), _stream(stream)),
            "asg_guidance_combine")
+
+
+def _strides(s):
+    """None (contiguous) or (batch, head, token) strides in elements."""
+    return None if s is None else ctypes.byref(_Strides(*s))
+
+
+def npa_cross_attention_fwd(q, k, v, o, dtype: int, B: int, heads: int, kv_heads: int, Lq: int, Lk: int, d: int,
+                            q_strides=None, k_strides=None, v_strides=None, o_strides=None, kv_lens=None,
+                            key_mask=None, scale: float = 0.0, workspace=None, workspace_bytes: int = 0,
+                            stream=None) -> None:
+    """C ``npa_cross_attention_fwd``: q, o [B, heads, Lq, d], k, v [B, kv_heads, Lk, d]; strides are (batch, head,
+    token) in elements, None for contiguous."""
+    _check(lib().npa_cross_attention_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), dtype, B, heads, kv_heads, Lq, Lk, d,
+                                         _strides(q_strides), _strides(k_strides), _strides(v_strides),
+                                         _strides(o_strides), _ptr(kv_lens), _ptr(key_mask), scale, _ptr(workspace),
+                                         int(workspace_bytes), _stream(stream)),
+           "npa_cross_attention_fwd")
+
+
+def npa_cross_attention_workspace_size(B, heads, Lq, Lk, d) -> int:
+    return int(lib().npa_cross_attention_workspace_size(B, heads, Lq, Lk, d))
+
+
+def npa_kv8_store(k, v, cache_k, cache_v, k_scale, v_scale, capacity: int, dtype: int, B: int, kv_heads: int, d: int,
+                  start: int, n_tokens: int, starts=None, k_strides=None, v_strides=None, stream=None) -> None:
+    """C ``npa_kv8_store``: k, v [B, kv_heads, n_tokens, d] into the cache's codes and scales."""
+    c = _Kv8Cache(_ptr(cache_k), _ptr(cache_v), _ptr(k_scale), _ptr(v_scale), capacity)
+    _check(lib().npa_kv8_store(_ptr(k), _ptr(v), ctypes.byref(c), dtype, B, kv_heads, d, start, _ptr(starts),
+                               n_tokens, _strides(k_strides), _strides(v_strides), _stream(stream)),
+           "npa_kv8_store")
+
+
+def npa_kv8_cross_attention_fwd(q, cache_k, cache_v, k_scale, v_scale, capacity: int, o, B: int, heads: int,
+                                kv_heads: int, Lq: int, Lk: int, d: int, q_strides=None, o_strides=None, kv_lens=None,
+                                key_mask=None, scale: float = 0.0, workspace=None, workspace_bytes: int = 0,
+                                stream=None) -> None:
+    """C ``npa_kv8_cross_attention_fwd``: bf16 q, o over the first Lk tokens of an 8-bit cache."""
+    c = _Kv8Cache(_ptr(cache_k), _ptr(cache_v), _ptr(k_scale), _ptr(v_scale), capacity)
+    _check(lib().npa_kv8_cross_attention_fwd(_ptr(q), ctypes.byref(c), _ptr(o), B, heads, kv_heads, Lq, Lk, d,
+                                             _strides(q_strides), _strides(o_strides), _ptr(kv_lens), _ptr(key_mask),
+                                             scale, _ptr(workspace), int(workspace_bytes), _stream(stream)),
+           "npa_kv8_cross_attention_fwd")
+
+
+def npa_group_norm_act(x, weight, bias, y, dtype: int, weight_dtype: int, B: int, N: int, C: int, groups: int,
+                       x_batch_stride: int, x_token_stride: int, y_batch_stride: int, y_token_stride: int, eps: float,
+                       act: int, workspace, workspace_bytes: int, stream=None) -> None:
+    """C ``npa_group_norm_act``: x, y [B, N, C], statistics over the tokens and channels of a group."""
+    _check(lib().npa_group_norm_act(_ptr(x), _ptr(weight), _ptr(bias), _ptr(y), dtype, weight_dtype, B, N, C, groups,
+                                    x_batch_stride, x_token_stride, y_batch_stride, y_token_stride, eps, act,
+                                    _ptr(workspace), int(workspace_bytes), _stream(stream)),
+           "npa_group_norm_act")
+
+
+def npa_group_norm_workspace_size(dtype, B, N, C, groups) -> int:
+    return int(lib().npa_group_norm_workspace_size(dtype, B, N, C, groups))
 
 
 def npa_global_query_workspace_size(B, heads, H, W, d, G) -> int:
@@ -381,4 +481,236 @@ def asg_combine(eps, eps_ref, mask, w_t: float, out=None, stream=None):
     if out is None:
         out = eps.new_empty(eps.shape)
     asg_guidance_combine(eps, eps_ref, mask, out, n, B, C, S, w_t, stream)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# The steps around the self-attention
+# ---------------------------------------------------------------------------
+
+def _dtype_code(t, allowed) -> int:
+    import torch
+    code = {torch.bfloat16: NPA_DTYPE_BF16, torch.float16: NPA_DTYPE_FP16, torch.float32: NPA_DTYPE_FP32}.get(t.dtype)
+    if code not in allowed:
+        raise ValueError(f"unsupported dtype {t.dtype}")
+    return code
+
+
+def _same_device(*tensors):
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+    if dev.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got {dev}")
+    return dev
+
+
+@contextlib.contextmanager
+def _launch_on(dev, stream):
+    """Makes ``dev`` and, when given, ``stream`` current, so that outputs and
+    workspaces come from the stream that the call runs on; yields its handle."""
+    import torch
+    with contextlib.ExitStack() as stack:
+        if dev.index != torch.cuda.current_device():
+            stack.enter_context(torch.cuda.device(dev))
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=dev)
+            stack.enter_context(torch.cuda.stream(stream))
+        yield torch.cuda.current_stream().cuda_stream
+
+
+def _heads_view(name, t, B=None, heads=None, L=None, d=None):
+    """Checks a [B, heads, L, d] tensor and returns its (batch, head, token) strides."""
+    if t.dim() != 4:
+        raise ValueError(f"{name}: expected [B, heads, L, d], got {tuple(t.shape)}")
+    for got, want in zip(t.shape, (B, heads, L, d)):
+        if want is not None and got != want:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(B, heads, L, d)}")
+    s = t.stride()
+    if s[3] != 1 and t.shape[3] != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    return s[:3]
+
+
+def _kept_keys(kv_lens, key_mask, B, Lk):
+    import torch
+    if kv_lens is not None and (kv_lens.dtype != torch.int32 or tuple(kv_lens.shape) != (B,) or
+                                not kv_lens.is_contiguous()):
+        raise ValueError(f"kv_lens: expected a contiguous int32 tensor of {B} lengths")
+    if key_mask is not None and (key_mask.dtype not in (torch.bool, torch.uint8) or
+                                 tuple(key_mask.shape) != (B, Lk) or not key_mask.is_contiguous()):
+        raise ValueError(f"key_mask: expected a contiguous bool or uint8 tensor [{B}, {Lk}]")
+
+
+def _scale(scale) -> float:
+    if scale is None:
+        return 0.0
+    if not scale > 0:
+        raise ValueError(f"scale must be positive, got {scale}")
+    return float(scale)
+
+
+def _split_workspace(split, B, heads, Lq, Lk, d, dev):
+    import torch
+    nbytes = npa_cross_attention_workspace_size(B, heads, Lq, Lk, d) if split else 0
+    return (torch.empty(nbytes, dtype=torch.uint8, device=dev), nbytes) if nbytes else (None, 0)
+
+
+def cross_attention(q, k, v, kv_lens=None, key_mask=None, scale: Optional[float] = None, out=None, split: bool = True,
+                    stream=None):
+    """Cross attention on torch bf16 or fp16 CUDA tensors: q [B, heads, Lq, d],
+    k and v [B, kv_heads, Lk, d], any strides that are multiples of 8 elements
+    with the last axis contiguous (a projection's ``[B, L, heads, d]`` seen
+    through ``transpose(1, 2)``). Keys that ``kv_lens`` (int32 [B]) or
+    ``key_mask`` (bool or uint8 [B, Lk], true: attend) leave out are not read;
+    a row without keys gives zeros. ``scale`` defaults to 1/sqrt(d). With
+    ``split`` a workspace is allocated so that the key range of few queries can
+    be split across the GPU. Returns ``out`` (by default laid out like q)."""
+    import torch
+    qs = _heads_view("q", q)
+    B, heads, Lq, d = q.shape
+    ks = _heads_view("k", k, B, None, None, d)
+    kv_heads, Lk = k.shape[1], k.shape[2]
+    vs = _heads_view("v", v, B, kv_heads, Lk, d)
+    code = _dtype_code(q, (NPA_DTYPE_BF16, NPA_DTYPE_FP16))
+    _kept_keys(kv_lens, key_mask, B, Lk)
+    dev = _same_device(q, k, v, kv_lens, key_mask, out)
+    with _launch_on(dev, stream) as handle:
+        if out is None:
+            out = torch.empty_like(q)
+        if not q.dtype == k.dtype == v.dtype == out.dtype:
+            raise ValueError("q, k, v and out must have one dtype")
+        os_ = _heads_view("out", out, B, heads, Lq, d)
+        ws, nbytes = _split_workspace(split, B, heads, Lq, Lk, d, dev)
+        npa_cross_attention_fwd(q, k, v, out, code, B, heads, kv_heads, Lq, Lk, d, qs, ks, vs, os_, kv_lens, key_mask,
+                                _scale(scale), ws, nbytes, handle)
+    return out
+
+
+class Kv8Cache:
+    """Keys and values in 8 bits: e4m3 codes ``k``, ``v`` [B, kv_heads,
+    capacity, d] (``torch.float8_e4m3fn`` or uint8) and float32 scales
+    ``k_scale``, ``v_scale`` [B, kv_heads, capacity / 64], value = code *
+    scale. ``Kv8Cache.empty`` allocates one; ``kv8_store`` writes it."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale")
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        if k.dim() != 4 or k.shape != v.shape or k.shape[2] % KV8_BLOCK:
+            raise ValueError(f"expected codes [B, kv_heads, capacity, d] with capacity a multiple of {KV8_BLOCK}, "
+                             f"got {tuple(k.shape)} and {tuple(v.shape)}")
+        want = (k.shape[0], k.shape[1], k.shape[2] // KV8_BLOCK)
+        for t in (k_scale, v_scale):
+            if tuple(t.shape) != want or t.dtype != torch.float32:
+                raise ValueError(f"expected float32 scales {want}, got {t.dtype} {tuple(t.shape)}")
+        for t in (k, v):
+            if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+                raise ValueError(f"expected e4m3 or uint8 codes, got {t.dtype}")
+        if not all(t.is_contiguous() for t in (k, v, k_scale, v_scale)):
+            raise ValueError("a cache's tensors must be contiguous")
+        _same_device(k, v, k_scale, v_scale)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+
+    @classmethod
+    def empty(cls, B: int, kv_heads: int, capacity: int, d: int, device="cuda") -> "Kv8Cache":
+        """A cache of zeros for ``capacity`` tokens (rounded up to whole blocks)."""
+        import torch
+        capacity = -(-capacity // KV8_BLOCK) * KV8_BLOCK
+        codes = [torch.zeros(B, kv_heads, capacity, d, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+                 for _ in range(2)]
+        scales = [torch.ones(B, kv_heads, capacity // KV8_BLOCK, device=device) for _ in range(2)]
+        return cls(*codes, *scales)
+
+    @property
+    def capacity(self) -> int:
+        return int(self.k.shape[2])
+
+
+def kv8_store(cache: Kv8Cache, k, v, start: int = 0, starts=None, stream=None) -> None:
+    """Writes bf16 or fp16 k, v [B, kv_heads, n, d] (strides as for
+    ``cross_attention``) into the cache from token ``start`` on, or from
+    ``starts[b]`` (int32 [B]) in batch row b."""
+    import torch
+    B, kv_heads, capacity, d = cache.k.shape
+    ks = _heads_view("k", k, B, kv_heads, None, d)
+    n = k.shape[2]
+    vs = _heads_view("v", v, B, kv_heads, n, d)
+    code = _dtype_code(k, (NPA_DTYPE_BF16, NPA_DTYPE_FP16))
+    if v.dtype != k.dtype:
+        raise ValueError("k and v must have one dtype")
+    if starts is not None and (starts.dtype != torch.int32 or tuple(starts.shape) != (B,) or
+                               not starts.is_contiguous()):
+        raise ValueError(f"starts: expected a contiguous int32 tensor of {B} positions")
+    dev = _same_device(cache.k, k, v, starts)
+    with _launch_on(dev, stream) as handle:
+        npa_kv8_store(k, v, cache.k, cache.v, cache.k_scale, cache.v_scale, capacity, code, B, kv_heads, d, start, n,
+                      starts, ks, vs, handle)
+
+
+def kv8_cross_attention(q, cache: Kv8Cache, n_tokens: Optional[int] = None, kv_lens=None, key_mask=None,
+                        scale: Optional[float] = None, out=None, split: bool = True, stream=None):
+    """``cross_attention`` of bf16 q [B, heads, Lq, d] over the first
+    ``n_tokens`` (default: all) tokens of an 8-bit cache."""
+    import torch
+    cB, kv_heads, capacity, cd = cache.k.shape
+    qs = _heads_view("q", q, cB, None, None, cd)
+    B, heads, Lq, d = q.shape
+    Lk = capacity if n_tokens is None else int(n_tokens)
+    _dtype_code(q, (NPA_DTYPE_BF16,))
+    _kept_keys(kv_lens, key_mask, B, Lk)
+    dev = _same_device(q, cache.k, kv_lens, key_mask, out)
+    with _launch_on(dev, stream) as handle:
+        if out is None:
+            out = torch.empty_like(q)
+        if out.dtype != q.dtype:
+            raise ValueError("q and out must have one dtype")
+        os_ = _heads_view("out", out, B, heads, Lq, d)
+        ws, nbytes = _split_workspace(split, B, heads, Lq, Lk, d, dev)
+        npa_kv8_cross_attention_fwd(q, cache.k, cache.v, cache.k_scale, cache.v_scale, capacity, out, B, heads,
+                                    kv_heads, Lq, Lk, d, qs, os_, kv_lens, key_mask, _scale(scale), ws, nbytes, handle)
+    return out
+
+
+_ACTIVATIONS = {None: NPA_ACT_NONE, "none": NPA_ACT_NONE, "silu": NPA_ACT_SILU}
+
+
+def group_norm(x, groups: int, weight=None, bias=None, eps: float = 1e-5, act: Optional[str] = None, out=None,
+               stream=None):
+    """Group norm with an activation (None or "silu") on a torch bf16, fp16 or
+    fp32 CUDA tensor x [B, N, C], channels last and contiguous, batch and token
+    strides free; weight and bias [C] of x's dtype or float32. ``out=x`` works
+    in place. (A channels-last [B, C, H, W] tensor is ``x.permute(0, 2, 3,
+    1).flatten(1, 2)``.)"""
+    import torch
+    if x.dim() != 3:
+        raise ValueError(f"expected [B, N, C], got {tuple(x.shape)}")
+    if act not in _ACTIVATIONS:
+        raise ValueError(f"unknown activation {act!r}")
+    B, N, C = x.shape
+    code = _dtype_code(x, (NPA_DTYPE_BF16, NPA_DTYPE_FP16, NPA_DTYPE_FP32))
+    wcode = code
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is None:
+            continue
+        if tuple(t.shape) != (C,) or t.dtype not in (x.dtype, torch.float32) or not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous [{C}] tensor of {x.dtype} or float32")
+        wcode = _dtype_code(t, (code, NPA_DTYPE_FP32))
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise ValueError("weight and bias must have one dtype")
+    dev = _same_device(x, weight, bias, out)
+    with _launch_on(dev, stream) as handle:
+        if out is None:
+            out = torch.empty((B, N, C), dtype=x.dtype, device=dev)
+        if out.dtype != x.dtype or out.shape != x.shape:
+            raise ValueError("out must have x's shape and dtype")
+        for name, t in (("x", x), ("out", out)):
+            if C > 1 and t.stride(2) != 1:
+                raise ValueError(f"{name}: channels must be contiguous")
+        nbytes = npa_group_norm_workspace_size(code, B, N, C, groups)
+        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        npa_group_norm_act(x, weight, bias, out, code, wcode, B, N, C, groups, x.stride(0), x.stride(1),
+                           out.stride(0), out.stride(1), float(eps), _ACTIVATIONS[act], ws, nbytes, handle)
     return out

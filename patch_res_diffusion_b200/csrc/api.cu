@@ -14,6 +14,9 @@
 
 #include "npa.h"
 #include "asg_combine.cuh"
+#include "cross_attention.cuh"
+#include "group_norm.cuh"
+#include "kv8_store.cuh"
 #include "md_combine.cuh"
 #include "npa_fwd_kernel.cuh"
 
@@ -43,6 +46,8 @@ struct DeviceState {
     npa_status status = NPA_ERR_UNSUPPORTED;
     int sm_count = 0;
     int l2_bytes = 0;
+    bool xa_checked = false;  // the cross-attention kernels (on their first use)
+    npa_status xa_status = NPA_ERR_UNSUPPORTED;
 };
 DeviceState g_dev[kMaxDevices];
 
@@ -580,6 +585,338 @@ double useful_flops(int B, int heads, int d, const Geo &g, int G) {
     return 4.0 * d * (double)B * heads * pairs;
 }
 
+// ---------------------------------------------------------------------------
+// Cross attention, 16-bit keys or the 8-bit cache
+// ---------------------------------------------------------------------------
+template <int D, bool KV8, bool F16>
+bool prepare_xa_kernel() {
+    using C = npa::XaCfg<D, KV8>;
+    void (*kernel)(npa::XaParams) = npa::xa_fwd_kernel<D, KV8, F16>;
+    cudaFuncAttributes attr;
+    if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess || attr.numRegs != (int)C::kRegsLaunch) return false;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) == cudaSuccess;
+}
+
+// ensure_ready plus the cross-attention kernels' limits, once per device.
+npa_status ensure_xa_ready(int *sm_count) {
+    const npa_status st = ensure_ready(sm_count);
+    if (st != NPA_OK) return st;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return NPA_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceState &ds = g_dev[dev];
+    if (!ds.xa_checked) {
+        const bool ok = prepare_xa_kernel<64, false, false>() && prepare_xa_kernel<64, false, true>() &&
+                        prepare_xa_kernel<128, false, false>() && prepare_xa_kernel<128, false, true>() &&
+                        prepare_xa_kernel<64, true, false>() && prepare_xa_kernel<128, true, false>();
+        ds.xa_status = ok ? NPA_OK : NPA_ERR_UNSUPPORTED;
+        ds.xa_checked = true;
+    }
+    return ds.xa_status;
+}
+
+// A strided [B, heads, L, d] tensor of 16-bit elements (or 1-byte codes).
+struct View {
+    const void *ptr;
+    long long sb, sh, st;  // strides in elements
+    int B, heads, L, d, elem;
+    size_t span() const {  // bytes from the first element to the last
+        return (size_t)((B - 1) * sb + (heads - 1) * sh + (L - 1) * st + d) * elem;
+    }
+};
+
+// Strides given by the caller, or those of a contiguous tensor. Axes of one
+// entry get a contiguous tensor's stride (theirs is never used).
+npa_status make_view(View *v, const void *ptr, const npa_strides *s, int B, int heads, int L, int d, int elem,
+                     bool output) {
+    *v = View{ptr, (long long)heads * L * d, (long long)L * d, d, B, heads, L, d, elem};
+    if (s) {
+        if (s->batch < 0 || s->head < 0 || s->token < 0) return NPA_ERR_INVALID_ARG;
+        if (B > 1) v->sb = s->batch;
+        if (heads > 1) v->sh = s->head;
+        if (L > 1) v->st = s->token;
+    }
+    const int unit = 16 / elem;
+    if (v->sb % unit || v->sh % unit || v->st % unit) return NPA_ERR_MISALIGNED;
+    if (L > 1 && v->st < d) return NPA_ERR_INVALID_ARG;
+    // tensor-map limits (strides < 2^40 bytes), and spans that fit an address
+    const long long lim = (1LL << 40) / elem;
+    if (v->sb >= lim || v->sh >= lim || v->st >= lim) return NPA_ERR_UNSUPPORTED;
+    if ((double)v->sb * B + (double)v->sh * heads + (double)v->st * L >= (double)(1LL << 46)) return NPA_ERR_UNSUPPORTED;
+    if (output) {  // no two elements at one place
+        long long st[3] = {B > 1 ? v->sb : 0, heads > 1 ? v->sh : 0, L > 1 ? v->st : 0};
+        int n[3] = {B, heads, L};
+        for (int i = 0; i < 3; ++i)
+            for (int j = i + 1; j < 3; ++j)
+                if (st[j] < st[i]) std::swap(st[i], st[j]), std::swap(n[i], n[j]);
+        long long below = d;  // elements that the faster axes span
+        for (int i = 0; i < 3; ++i) {
+            if (n[i] == 1) continue;
+            if (st[i] < below) return NPA_ERR_INVALID_ARG;
+            below += (n[i] - 1) * st[i];
+        }
+    }
+    return NPA_OK;
+}
+
+// 4D map {d, L, heads, B}; an axis with stride 0 becomes one entry long (the
+// kernel multiplies its coordinate by 0).
+bool encode_view(CUtensorMap *m, const View &v, bool f16) {
+    const bool codes = v.elem == 1;
+    const cuuint64_t dims[4] = {(cuuint64_t)v.d, (cuuint64_t)v.L, (cuuint64_t)(v.sh ? v.heads : 1),
+                                (cuuint64_t)(v.sb ? v.B : 1)};
+    const cuuint64_t row = (cuuint64_t)v.d * v.elem;
+    const cuuint64_t strides[3] = {(cuuint64_t)v.st * v.elem, v.sh ? (cuuint64_t)v.sh * v.elem : row,
+                                   v.sb ? (cuuint64_t)v.sb * v.elem : row};
+    const cuuint32_t box[4] = {codes ? (cuuint32_t)v.d : 64u, 128, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return g_encode(m,
+                    codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                    : f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                          : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                    4, const_cast<void *>(v.ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Key-range splits: the count with the smallest predicted time, in key blocks
+// of one CTA, over the launch's waves. A unit costs about two blocks beyond
+// its own, and merging the splits about four.
+int plan_xa_splits(long long base_units, long long n_blocks, int sm_count) {
+    int best = 1;
+    double best_cost = 1e300;
+    for (int s = 1; s <= npa::kXaMaxSplits && s <= n_blocks; ++s) {
+        const long long waves = (base_units * s + sm_count - 1) / sm_count;
+        if (s > 1 && waves > 1 && base_units >= sm_count) break;
+        const double cost = (double)waves * ((n_blocks + s - 1) / s + 2) + (s > 1 ? 4 : 0);
+        if (cost < best_cost - 1e-9) {
+            best_cost = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
+size_t xa_split_bytes(int B, int heads, int Lq, int d) { return (size_t)B * heads * Lq * (d + 2) * sizeof(float); }
+
+struct XaCall {
+    View q, k, v, o;
+    const float *k_scale, *v_scale;  // null: 16-bit keys
+    int scale_blocks;
+    const int *kv_lens;
+    const unsigned char *key_mask;
+    float scale;
+    void *workspace;
+    size_t workspace_bytes;
+    bool f16;
+};
+
+// Sizes, scale and masks (before the views, which need the sizes).
+npa_status validate_xa_sizes(int B, int heads, int kv_heads, int Lq, int Lk, int d, float scale,
+                             const int32_t *kv_lens) {
+    if (B < 1 || heads < 1 || kv_heads < 1 || Lq < 1 || Lk < 1 || d < 1) return NPA_ERR_INVALID_ARG;
+    if (heads % kv_heads != 0 || !std::isfinite(scale) || scale < 0.f) return NPA_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return NPA_ERR_UNSUPPORTED;
+    if (reinterpret_cast<uintptr_t>(kv_lens) & 3u) return NPA_ERR_MISALIGNED;
+    const long long units = (long long)B * heads * (((long long)Lq + 255) / 256);
+    if ((long long)B * heads > INT_MAX / 64 || units > INT_MAX / 128 || Lq > INT_MAX - 256 || Lk > INT_MAX - 256)
+        return NPA_ERR_UNSUPPORTED;
+    return NPA_OK;
+}
+
+npa_status validate_xa_buffers(const XaCall &c) {
+    const int B = c.q.B, Lk = c.k.L;
+    if (!aligned16(c.q.ptr) || !aligned16(c.k.ptr) || !aligned16(c.v.ptr) || !aligned16(c.o.ptr) ||
+        (c.workspace && !aligned16(c.workspace)))
+        return NPA_ERR_MISALIGNED;
+    struct { const void *p; size_t n; } in[7] = {
+        {c.q.ptr, c.q.span()}, {c.k.ptr, c.k.span()}, {c.v.ptr, c.v.span()},
+        {c.kv_lens, (size_t)B * 4}, {c.key_mask, (size_t)B * Lk},
+        {c.k_scale, (size_t)B * c.k.heads * c.scale_blocks * 4}, {c.v_scale, (size_t)B * c.k.heads * c.scale_blocks * 4}};
+    for (const auto &x : in) {
+        if (!x.p) continue;
+        if (overlaps(c.o.ptr, c.o.span(), x.p, x.n)) return NPA_ERR_INVALID_ARG;
+        if (c.workspace && overlaps(c.workspace, c.workspace_bytes, x.p, x.n)) return NPA_ERR_INVALID_ARG;
+    }
+    if (c.workspace && overlaps(c.workspace, c.workspace_bytes, c.o.ptr, c.o.span())) return NPA_ERR_INVALID_ARG;
+    return NPA_OK;
+}
+
+npa_status launch_xa(const XaCall &c, npa_stream_t stream) {
+    int sm_count = 0;
+    const npa_status st = ensure_xa_ready(&sm_count);
+    if (st != NPA_OK) return st;
+    const int B = c.q.B, heads = c.q.heads, Lq = c.q.L, d = c.q.d, Lk = c.k.L;
+    npa::XaParams prm;
+    std::memset(&prm, 0, sizeof(prm));
+    prm.kv_lens = c.kv_lens;
+    prm.key_mask = c.key_mask;
+    prm.k_scale = c.k_scale;
+    prm.v_scale = c.v_scale;
+    prm.scale_blocks = c.scale_blocks;
+    prm.B = B;
+    prm.heads = heads;
+    prm.kv_heads = c.k.heads;
+    prm.group = heads / c.k.heads;
+    prm.Lq = Lq;
+    prm.Lk = Lk;
+    prm.q_b = c.q.sb != 0;
+    prm.q_h = c.q.sh != 0;
+    prm.k_b = c.k.sb != 0;
+    prm.k_h = c.k.sh != 0;
+    prm.v_b = c.v.sb != 0;
+    prm.v_h = c.v.sh != 0;
+    prm.n_qpairs = (Lq + 255) / 256;
+    const double scale = c.scale > 0.f ? (double)c.scale : 1.0 / std::sqrt((double)d);
+    prm.scale_log2 = (float)(1.4426950408889634 * scale);
+    prm.wait_limit_ns = kWaitLimitNs;
+    const long long base = (long long)B * heads * prm.n_qpairs;
+    // as many splits as planned and as the workspace holds (one needs none)
+    int splits = plan_xa_splits(base, ((long long)Lk + 127) / 128, sm_count);
+    const size_t per_split = xa_split_bytes(B, heads, Lq, d);
+    const size_t held = c.workspace ? c.workspace_bytes / per_split : 1;
+    if ((size_t)splits > held) splits = (int)held;
+    if (splits < 2) splits = 1;
+    prm.n_splits = splits;
+    const long long rows = (long long)B * heads * Lq;
+    if (splits > 1) {
+        prm.o_part = static_cast<float *>(c.workspace);
+        prm.ml = prm.o_part + (size_t)splits * rows * d;
+    }
+    prm.n_units = (int)(base * splits);
+    if (!encode_view(&prm.tm_q, c.q, c.f16) || !encode_view(&prm.tm_k, c.k, c.f16) ||
+        !encode_view(&prm.tm_v, c.v, c.f16) || !encode_view(&prm.tm_o, c.o, c.f16))
+        return NPA_ERR_CUDA;
+    const bool kv8 = c.k_scale != nullptr;
+    const void *kernel;
+    unsigned threads, smem;
+    auto pick = [&](const void *k, auto cfg) {
+        kernel = k;
+        threads = decltype(cfg)::kThreads;
+        smem = decltype(cfg)::kSmemBytes;
+    };
+    if (kv8 && d == 64)
+        pick((const void *)npa::xa_fwd_kernel<64, true, false>, npa::XaCfg<64, true>{});
+    else if (kv8)
+        pick((const void *)npa::xa_fwd_kernel<128, true, false>, npa::XaCfg<128, true>{});
+    else if (d == 64)
+        pick(c.f16 ? (const void *)npa::xa_fwd_kernel<64, false, true> : (const void *)npa::xa_fwd_kernel<64, false, false>,
+             npa::XaCfg<64, false>{});
+    else
+        pick(c.f16 ? (const void *)npa::xa_fwd_kernel<128, false, true>
+                   : (const void *)npa::xa_fwd_kernel<128, false, false>,
+             npa::XaCfg<128, false>{});
+    const unsigned grid = (unsigned)(prm.n_units < sm_count ? prm.n_units : sm_count);
+    void *args[1] = {&prm};
+    if (cudaLaunchKernel(kernel, dim3(grid), dim3(threads), args, smem, (cudaStream_t)stream) != cudaSuccess)
+        return NPA_ERR_CUDA;
+    if (splits > 1) {
+        npa::XaCombineParams cp{prm.o_part, prm.ml, const_cast<void *>(c.o.ptr), c.o.sb, c.o.sh, c.o.st, splits,
+                                (int)rows, heads, Lq};
+        void *cargs[1] = {&cp};
+        const void *ck = d == 64 ? (c.f16 ? (const void *)npa::xa_combine_kernel<64, true>
+                                          : (const void *)npa::xa_combine_kernel<64, false>)
+                                 : (c.f16 ? (const void *)npa::xa_combine_kernel<128, true>
+                                          : (const void *)npa::xa_combine_kernel<128, false>);
+        if (cudaLaunchKernel(ck, dim3((unsigned)((rows + 7) / 8)), dim3(256), cargs, 0, (cudaStream_t)stream) !=
+            cudaSuccess)
+            return NPA_ERR_CUDA;
+    }
+    return NPA_OK;
+}
+
+// A cache's own arguments.
+npa_status validate_kv8(const npa_kv8_cache *cache, int B, int kv_heads, int d) {
+    if (!cache || !cache->k || !cache->v || !cache->k_scale || !cache->v_scale) return NPA_ERR_INVALID_ARG;
+    if (B < 1 || kv_heads < 1 || d < 1 || cache->capacity < npa::kKv8Block || cache->capacity % npa::kKv8Block != 0)
+        return NPA_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return NPA_ERR_UNSUPPORTED;
+    if (!aligned16(cache->k) || !aligned16(cache->v) || !aligned16(cache->k_scale) || !aligned16(cache->v_scale))
+        return NPA_ERR_MISALIGNED;
+    if ((long long)B * kv_heads > INT_MAX / 64 || (double)B * kv_heads * cache->capacity * d >= (double)(1LL << 46))
+        return NPA_ERR_UNSUPPORTED;
+    return NPA_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Group norm
+// ---------------------------------------------------------------------------
+struct GnPlan {
+    int vec, cols, rows, threads;
+    int stat_tiles, stat_rows, apply_tiles, apply_rows;
+    size_t stat_smem, apply_smem, bytes;
+};
+
+// Tiles per batch row: enough blocks for `per_sm` on every multiprocessor, of
+// at least one batch of tokens per thread.
+void gn_tiles(int B, int N, int rows, int per_sm, int batch, int sm_count, int *tiles, int *tile_rows) {
+    long long t = ((long long)per_sm * sm_count + B - 1) / B;
+    const long long most = ((long long)N + (long long)rows * batch - 1) / ((long long)rows * batch);
+    if (t > most) t = most;
+    if (t < 1) t = 1;
+    long long r = (N + t - 1) / t;
+    r = (r + rows - 1) / rows * rows;
+    *tile_rows = (int)r;
+    *tiles = (int)((N + r - 1) / r);
+}
+
+GnPlan plan_gn(int B, int N, int C, int groups, int vec, int sm_count) {
+    GnPlan pl;
+    pl.vec = vec;
+    const int ncol = C / vec;
+    pl.cols = ncol < npa::kGnThreads ? ncol : npa::kGnThreads;
+    pl.rows = pl.cols < 256 ? 256 / pl.cols : 1;
+    if (pl.rows > N) pl.rows = N;
+    pl.threads = (pl.cols * pl.rows + 31) / 32 * 32;
+    gn_tiles(B, N, pl.rows, 4, npa::kGnBatch, sm_count, &pl.stat_tiles, &pl.stat_rows);
+    gn_tiles(B, N, pl.rows, 8, 4, sm_count, &pl.apply_tiles, &pl.apply_rows);
+    pl.stat_smem = ((size_t)2 * pl.rows * C + pl.rows) * sizeof(float);
+    pl.apply_smem = (size_t)2 * groups * sizeof(float);
+    pl.bytes = (size_t)B * groups * pl.stat_tiles * sizeof(float2);
+    return pl;
+}
+
+int gn_elem(npa_dtype t) { return t == NPA_DTYPE_FP32 ? 4 : 2; }
+bool gn_dtype(npa_dtype t) { return t == NPA_DTYPE_BF16 || t == NPA_DTYPE_FP16 || t == NPA_DTYPE_FP32; }
+
+// Tokens of C channels at these strides can be read 16 bytes at a time.
+bool gn_vectors(int C, npa_dtype dtype, const void *x, const void *y, const int64_t (&s)[4]) {
+    const int unit = 16 / gn_elem(dtype);
+    for (const int64_t t : s)
+        if (t % unit) return false;
+    return C % unit == 0 && aligned16(x) && aligned16(y);
+}
+
+template <typename T, int kVec>
+npa_status launch_gn(const npa::GnParams &prm, const GnPlan &pl, int B, npa_stream_t stream) {
+    npa::GnParams p = prm;
+    void *args[1] = {&p};
+    const void *stats = (const void *)npa::gn_stats_kernel<T, kVec>;
+    const void *apply = (const void *)npa::gn_apply_kernel<T, kVec>;
+    if (cudaLaunchKernel(stats, dim3(pl.stat_tiles, B), dim3(pl.threads), args, pl.stat_smem, (cudaStream_t)stream) !=
+        cudaSuccess)
+        return NPA_ERR_CUDA;
+    // the normalisation may start while the statistics finish; it waits for
+    // them on the device
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(pl.apply_tiles, B);
+    cfg.blockDim = dim3(pl.threads);
+    cfg.dynamicSmemBytes = pl.apply_smem;
+    cfg.stream = (cudaStream_t)stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, apply, args) == cudaSuccess ? NPA_OK : NPA_ERR_CUDA;
+}
+
+template <typename T>
+npa_status launch_gn_vec(const npa::GnParams &prm, const GnPlan &pl, int B, npa_stream_t stream) {
+    return pl.vec == 1 ? launch_gn<T, 1>(prm, pl, B, stream) : launch_gn<T, 16 / sizeof(T)>(prm, pl, B, stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -769,6 +1106,214 @@ npa_status asg_guidance_combine(const void *eps, const void *eps_ref, const void
     const cudaError_t e =
         cudaLaunchKernel((const void *)npa::asg_combine_kernel, dim3(grid), dim3(256), args, 0, (cudaStream_t)stream);
     return e == cudaSuccess ? NPA_OK : NPA_ERR_CUDA;
+}
+
+size_t npa_cross_attention_workspace_size(int B, int heads, int Lq, int Lk, int d) {
+    if (validate_xa_sizes(B, heads, heads, Lq, Lk, d, 0.f, nullptr) != NPA_OK) return 0;
+    int dev = 0, sm = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    const int s = plan_xa_splits((long long)B * heads * ((Lq + 255) / 256), ((long long)Lk + 127) / 128, sm);
+    return s > 1 ? (size_t)s * xa_split_bytes(B, heads, Lq, d) : 0;
+}
+
+npa_status npa_cross_attention_fwd(const void *q, const void *k, const void *v, void *o, npa_dtype dtype, int B,
+                                   int heads, int kv_heads, int Lq, int Lk, int d, const npa_strides *q_strides,
+                                   const npa_strides *k_strides, const npa_strides *v_strides,
+                                   const npa_strides *o_strides, const int32_t *kv_lens, const uint8_t *key_mask,
+                                   float scale, void *workspace, size_t workspace_bytes, npa_stream_t stream) {
+    if (!q || !k || !v || !o) return NPA_ERR_INVALID_ARG;
+    npa_status st = validate_xa_sizes(B, heads, kv_heads, Lq, Lk, d, scale, kv_lens);
+    if (st != NPA_OK) return st;
+    if (dtype != NPA_DTYPE_BF16 && dtype != NPA_DTYPE_FP16) return NPA_ERR_UNSUPPORTED;
+    XaCall c;
+    std::memset(&c, 0, sizeof(c));
+    if ((st = make_view(&c.q, q, q_strides, B, heads, Lq, d, 2, false)) != NPA_OK ||
+        (st = make_view(&c.k, k, k_strides, B, kv_heads, Lk, d, 2, false)) != NPA_OK ||
+        (st = make_view(&c.v, v, v_strides, B, kv_heads, Lk, d, 2, false)) != NPA_OK ||
+        (st = make_view(&c.o, o, o_strides, B, heads, Lq, d, 2, true)) != NPA_OK)
+        return st;
+    c.kv_lens = kv_lens;
+    c.key_mask = key_mask;
+    c.scale = scale;
+    c.workspace = workspace;
+    c.workspace_bytes = workspace_bytes;
+    c.f16 = dtype == NPA_DTYPE_FP16;
+    if ((st = validate_xa_buffers(c)) != NPA_OK) return st;
+    return launch_xa(c, stream);
+}
+
+npa_status npa_kv8_cross_attention_fwd(const void *q, const npa_kv8_cache *cache, void *o, int B, int heads,
+                                       int kv_heads, int Lq, int Lk, int d, const npa_strides *q_strides,
+                                       const npa_strides *o_strides, const int32_t *kv_lens, const uint8_t *key_mask,
+                                       float scale, void *workspace, size_t workspace_bytes, npa_stream_t stream) {
+    if (!q || !o) return NPA_ERR_INVALID_ARG;
+    npa_status st = validate_xa_sizes(B, heads, kv_heads, Lq, Lk, d, scale, kv_lens);
+    if (st != NPA_OK) return st;
+    if ((st = validate_kv8(cache, B, kv_heads, d)) != NPA_OK) return st;
+    if (Lk > cache->capacity) return NPA_ERR_INVALID_ARG;
+    XaCall c;
+    std::memset(&c, 0, sizeof(c));
+    npa_strides cs;
+    cs.token = d;
+    cs.head = (int64_t)cache->capacity * d;
+    cs.batch = cs.head * kv_heads;
+    if ((st = make_view(&c.q, q, q_strides, B, heads, Lq, d, 2, false)) != NPA_OK ||
+        (st = make_view(&c.k, cache->k, &cs, B, kv_heads, Lk, d, 1, false)) != NPA_OK ||
+        (st = make_view(&c.v, cache->v, &cs, B, kv_heads, Lk, d, 1, false)) != NPA_OK ||
+        (st = make_view(&c.o, o, o_strides, B, heads, Lq, d, 2, true)) != NPA_OK)
+        return st;
+    c.k_scale = cache->k_scale;
+    c.v_scale = cache->v_scale;
+    c.scale_blocks = cache->capacity / npa::kKv8Block;
+    c.kv_lens = kv_lens;
+    c.key_mask = key_mask;
+    c.scale = scale;
+    c.workspace = workspace;
+    c.workspace_bytes = workspace_bytes;
+    if ((st = validate_xa_buffers(c)) != NPA_OK) return st;
+    return launch_xa(c, stream);
+}
+
+npa_status npa_kv8_store(const void *k, const void *v, const npa_kv8_cache *cache, npa_dtype dtype, int B,
+                         int kv_heads, int d, int start, const int32_t *starts, int n_tokens,
+                         const npa_strides *k_strides, const npa_strides *v_strides, npa_stream_t stream) {
+    if (!k || !v) return NPA_ERR_INVALID_ARG;
+    npa_status st = validate_kv8(cache, B, kv_heads, d);
+    if (st != NPA_OK) return st;
+    if (n_tokens < 1 || (!starts && (start < 0 || (long long)start + n_tokens > cache->capacity)))
+        return NPA_ERR_INVALID_ARG;
+    if (dtype != NPA_DTYPE_BF16 && dtype != NPA_DTYPE_FP16) return NPA_ERR_UNSUPPORTED;
+    View kv[2];
+    if ((st = make_view(&kv[0], k, k_strides, B, kv_heads, n_tokens, d, 2, false)) != NPA_OK ||
+        (st = make_view(&kv[1], v, v_strides, B, kv_heads, n_tokens, d, 2, false)) != NPA_OK)
+        return st;
+    if (!aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(starts) & 3u)) return NPA_ERR_MISALIGNED;
+    // the four arrays of the cache and the inputs do not share memory
+    const size_t codes = (size_t)B * kv_heads * cache->capacity * d;
+    const size_t scales = (size_t)B * kv_heads * (cache->capacity / npa::kKv8Block) * 4;
+    struct { const void *p; size_t n; } a[7] = {{cache->k, codes}, {cache->v, codes}, {cache->k_scale, scales},
+        {cache->v_scale, scales}, {k, kv[0].span()}, {v, kv[1].span()}, {starts, (size_t)B * 4}};
+    for (int i = 0; i < 4; ++i)
+        for (int j = i + 1; j < 7; ++j)
+            if (a[j].p && overlaps(a[i].p, a[i].n, a[j].p, a[j].n)) return NPA_ERR_INVALID_ARG;
+    npa::Kv8StoreParams prm;
+    std::memset(&prm, 0, sizeof(prm));
+    for (int t = 0; t < 2; ++t) {
+        prm.x[t] = kv[t].ptr;
+        prm.sb[t] = kv[t].sb;
+        prm.sh[t] = kv[t].sh;
+        prm.st[t] = kv[t].st;
+    }
+    prm.codes[0] = static_cast<unsigned char *>(cache->k);
+    prm.codes[1] = static_cast<unsigned char *>(cache->v);
+    prm.scale[0] = cache->k_scale;
+    prm.scale[1] = cache->v_scale;
+    prm.starts = starts;
+    prm.start = start;
+    prm.n = n_tokens;
+    prm.capacity = cache->capacity;
+    prm.heads = kv_heads;
+    // blocks touched: counted from the first one's start, or, with starts on
+    // the device, one more than the tokens alone need
+    const long long span = starts ? (long long)n_tokens + npa::kKv8Block - 1 : start % npa::kKv8Block + (long long)n_tokens;
+    const long long nb = std::min<long long>((span + npa::kKv8Block - 1) / npa::kKv8Block, cache->capacity / npa::kKv8Block);
+    prm.n_blocks = (int)nb;
+    const long long grid = 2 * nb * B * kv_heads;
+    if (grid > INT_MAX) return NPA_ERR_UNSUPPORTED;
+    st = ensure_ready();
+    if (st != NPA_OK) return st;
+    const bool f16 = dtype == NPA_DTYPE_FP16;
+    const void *kernel = d == 64 ? (f16 ? (const void *)npa::kv8_store_kernel<64, true>
+                                        : (const void *)npa::kv8_store_kernel<64, false>)
+                                 : (f16 ? (const void *)npa::kv8_store_kernel<128, true>
+                                        : (const void *)npa::kv8_store_kernel<128, false>);
+    void *args[1] = {&prm};
+    return cudaLaunchKernel(kernel, dim3((unsigned)grid), dim3(128), args, 0, (cudaStream_t)stream) == cudaSuccess
+               ? NPA_OK
+               : NPA_ERR_CUDA;
+}
+
+size_t npa_group_norm_workspace_size(npa_dtype dtype, int B, int N, int C, int groups) {
+    if (!gn_dtype(dtype) || B < 1 || N < 1 || C < 1 || groups < 1 || C % groups || C > npa::kGnMaxChannels) return 0;
+    int dev = 0, sm = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    // whichever of the vector and the single-element form needs more
+    const int unit = 16 / gn_elem(dtype);
+    size_t n = plan_gn(B, N, C, groups, 1, sm).bytes;
+    if (C % unit == 0) n = std::max(n, plan_gn(B, N, C, groups, unit, sm).bytes);
+    return n;
+}
+
+npa_status npa_group_norm_act(const void *x, const void *weight, const void *bias, void *y, npa_dtype dtype,
+                              npa_dtype weight_dtype, int B, int N, int C, int groups, int64_t x_batch_stride,
+                              int64_t x_token_stride, int64_t y_batch_stride, int64_t y_token_stride, float eps,
+                              npa_activation act, void *workspace, size_t workspace_bytes, npa_stream_t stream) {
+    if (!x || !y || !workspace) return NPA_ERR_INVALID_ARG;
+    if (B < 1 || N < 1 || C < 1 || groups < 1 || C % groups != 0 || !std::isfinite(eps) || eps < 0.f)
+        return NPA_ERR_INVALID_ARG;
+    if (act != NPA_ACT_NONE && act != NPA_ACT_SILU) return NPA_ERR_INVALID_ARG;
+    if (!gn_dtype(dtype) || ((weight || bias) && weight_dtype != dtype && weight_dtype != NPA_DTYPE_FP32))
+        return NPA_ERR_UNSUPPORTED;
+    if (C > npa::kGnMaxChannels || B > 65535 || N > INT_MAX / 2) return NPA_ERR_UNSUPPORTED;
+    int64_t s[4] = {x_batch_stride, x_token_stride, y_batch_stride, y_token_stride};
+    for (const int64_t t : s)
+        if (t < 0 || t >= (1LL << 40)) return t < 0 ? NPA_ERR_INVALID_ARG : NPA_ERR_UNSUPPORTED;
+    // axes of one entry: their stride is never used
+    if (N == 1) s[1] = s[3] = C;
+    if (B == 1) s[0] = (int64_t)N * s[1], s[2] = (int64_t)N * s[3];
+    if (s[1] < C || s[3] < C) return NPA_ERR_INVALID_ARG;
+    if (B > 1 && N > 1 && s[2] < (N - 1) * s[3] + C && s[3] < (B - 1) * s[2] + C) return NPA_ERR_INVALID_ARG;
+    if (B > 1 && s[2] < C) return NPA_ERR_INVALID_ARG;
+    const int elem = gn_elem(dtype), welem = gn_elem(weight_dtype);
+    if ((reinterpret_cast<uintptr_t>(x) % elem) || (reinterpret_cast<uintptr_t>(y) % elem) || !aligned16(workspace) ||
+        (weight && reinterpret_cast<uintptr_t>(weight) % welem) || (bias && reinterpret_cast<uintptr_t>(bias) % welem))
+        return NPA_ERR_MISALIGNED;
+    const double ext = (double)B * std::max(s[0], s[2]) + (double)N * std::max(s[1], s[3]);
+    if (ext * elem >= (double)(1LL << 46)) return NPA_ERR_UNSUPPORTED;
+    const size_t xb = (size_t)((B - 1) * s[0] + (N - 1) * s[1] + C) * elem;
+    const size_t yb = (size_t)((B - 1) * s[2] + (N - 1) * s[3] + C) * elem;
+    // in place, or apart
+    const bool same = x == y && s[0] == s[2] && s[1] == s[3];
+    if (!same && overlaps(x, xb, y, yb)) return NPA_ERR_INVALID_ARG;
+    const size_t wb = (size_t)C * welem;
+    if ((weight && overlaps(y, yb, weight, wb)) || (bias && overlaps(y, yb, bias, wb))) return NPA_ERR_INVALID_ARG;
+    int sm_count = 0;
+    const npa_status st = ensure_ready(&sm_count);
+    if (st != NPA_OK) return st;
+    const GnPlan pl = plan_gn(B, N, C, groups, gn_vectors(C, dtype, x, y, s) ? 16 / elem : 1, sm_count);
+    if (workspace_bytes < pl.bytes) return NPA_ERR_INVALID_ARG;
+    if (overlaps(workspace, pl.bytes, x, xb) || overlaps(workspace, pl.bytes, y, yb) ||
+        (weight && overlaps(workspace, pl.bytes, weight, wb)) || (bias && overlaps(workspace, pl.bytes, bias, wb)))
+        return NPA_ERR_INVALID_ARG;
+    npa::GnParams prm;
+    std::memset(&prm, 0, sizeof(prm));
+    prm.x = x;
+    prm.y = y;
+    prm.w = weight;
+    prm.bias = bias;
+    prm.w_f32 = weight_dtype == NPA_DTYPE_FP32;
+    prm.xsb = s[0];
+    prm.xst = s[1];
+    prm.ysb = s[2];
+    prm.yst = s[3];
+    prm.N = N;
+    prm.G = groups;
+    prm.cpg = C / groups;
+    prm.cw = C;
+    prm.cols = pl.cols;
+    prm.rows = pl.rows;
+    prm.stat_tiles = pl.stat_tiles;
+    prm.stat_rows = pl.stat_rows;
+    prm.apply_tiles = pl.apply_tiles;
+    prm.apply_rows = pl.apply_rows;
+    prm.eps = eps;
+    prm.silu = act == NPA_ACT_SILU;
+    prm.part = static_cast<float2 *>(workspace);
+    if (dtype == NPA_DTYPE_BF16) return launch_gn_vec<__nv_bfloat16>(prm, pl, B, stream);
+    if (dtype == NPA_DTYPE_FP16) return launch_gn_vec<__half>(prm, pl, B, stream);
+    return launch_gn_vec<float>(prm, pl, B, stream);
 }
 
 int pcpp_neighbor_rows(int strip_rows, double p) { return neighbor_rows(strip_rows, p); }

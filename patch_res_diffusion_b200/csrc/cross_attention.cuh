@@ -1,0 +1,1003 @@
+// cross_attention.cuh - attention of Lq queries to an encoder's Lk keys and
+// values of another length (npa_cross_attention_fwd), and the same over a
+// cache held in e4m3 with a scale per 64 tokens and head
+// (npa_kv8_cross_attention_fwd).
+//
+//   o[b, h, i] = sum_j p_ij v[b, h', j],  p_ij = softmax_j(scale q[b, h, i] . k[b, h', j])
+//
+// over the keys j < kv_lens[b] with key_mask[b, j] != 0; h' = h / (heads /
+// kv_heads). A row without keys gives zeros. What it has to read and write is
+// q, o, k and v once; the exponentials (one per query and key) bind before the
+// products at d = 64, as in the self-attention kernel.
+//
+// A persistent CTA walks units of 256 query rows (two 128-row tiles, one
+// softmax warpgroup each) of one (batch, head), optionally over a part of the
+// key range. Warps:
+//   0-7    softmax and epilogue, tile 0 and 1 (TMEM lane = query row)
+//   8      TMA producer (query tiles; key and value blocks of 128 tokens)
+//   9, 10  MMA issuers: d = 64, the S products and the P.V products; d = 128,
+//          warp 9 issues both
+//   11     16-bit keys: clears the value rows of keys that are not kept
+//          (0 * NaN would reach the sums through the product otherwise)
+//   12-15  8-bit cache: converts code blocks to bf16 tiles in shared memory
+// TMEM, the aliasing of P at d = 128, the lazily moved softmax reference and
+// the turns on the exponential unit are those of npa_fwd_kernel.cuh.
+//
+// What differs from the self-attention kernel: every tensor is a 4D {d, L,
+// heads, B} map with the caller's strides (a projection's [B, L, heads * d]
+// needs no transposed copy); the last block's products and exponentials stop
+// at its last key (rounded up to 16 and 32); the output leaves through shared
+// memory as 128-byte rows with TMA stores, whose box the tensor map clips at
+// Lq; and Q is double buffered at d = 64, so that a short context (one block
+// per unit) streams queries and outputs at memory speed.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "npa_fwd_kernel.cuh"
+
+namespace npa {
+
+constexpr int kKv8Block = 64;  // tokens of one head that share a scale of the 8-bit cache
+constexpr int kXaMaxSplits = 64;  // key-range splits at most
+
+struct XaParams {
+    CUtensorMap tm_q;  // 4D {d, Lq, heads, B}, box {64, 128, 1, 1}, 128B swizzle
+    CUtensorMap tm_k;  // 4D {d, Lk, kv_heads, B}, box {64, 128, 1, 1}, 128B swizzle; codes: box {d, 128, 1, 1}, none
+    CUtensorMap tm_v;
+    CUtensorMap tm_o;  // as tm_q
+    const int *kv_lens;              // [B] or null: keys of batch row b (clamped to 0 .. Lk)
+    const unsigned char *key_mask;   // [B, Lk] or null: 0 = not attended
+    const float *k_scale, *v_scale;  // 8-bit cache: [B, kv_heads, scale_blocks]
+    int scale_blocks;
+    int B, heads, kv_heads, group, Lq, Lk;
+    int q_b, q_h, k_b, k_h, v_b, v_h;  // 1, or 0 along an axis that the tensor repeats (stride 0)
+    int n_qpairs;                      // ceil(Lq / 256)
+    int n_splits, n_units;
+    float scale_log2;
+    unsigned long long wait_limit_ns;
+    float *o_part;  // n_splits > 1: [n_splits][B * heads * Lq][d] unnormalised O
+    float *ml;      // n_splits > 1: [n_splits][B * heads * Lq][2] reference, row sum
+};
+
+template <int D, bool KV8>
+struct XaCfg {
+    static_assert(D == 64 || D == 128, "head dim");
+    static constexpr int kChunks = D / 64;
+    static constexpr int kChunkBytes = 128 * 128;  // 128 rows x 64 16-bit columns
+    static constexpr int kTileBytes = kChunks * kChunkBytes;
+    static constexpr int kCodeBytes = 128 * D;     // 128 rows of e4m3 codes
+    // Shared memory is what sets the depths: 224 KB in every shape.
+    static constexpr int kQStages = D == 64 ? 2 : 1;
+    static constexpr int kStages = KV8 ? (D == 64 ? 2 : 1) : (D == 64 ? 4 : 2);
+    static constexpr int kCodeStages = KV8 ? (D == 64 ? 4 : 2) : 0;
+    static constexpr int kThreads = KV8 ? 512 : 384;
+    static constexpr int kCtlWarp = 8;
+    static constexpr int kConvWarp = 12;
+    // Register split, as in KCfg; the 8-bit kernel's four warpgroups start
+    // with 128 each, and its converter takes its share from the softmax's.
+    static constexpr uint32_t kRegsLaunch = KV8 ? 128 : 168;
+    static constexpr uint32_t kRegsSoftmax = KV8 ? 184 : D == 64 ? 216 : 208;
+    static constexpr uint32_t kRegsCtl = KV8 ? 64 : D == 64 ? 72 : 88;
+    static constexpr uint32_t kRegsConv = 80;
+    static_assert(256 * kRegsSoftmax + 128 * kRegsCtl + (KV8 ? 128 * kRegsConv : 0) <= kThreads * kRegsLaunch,
+                  "register split");
+    static_assert(kThreads * kRegsLaunch <= 65536, "register file");
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffK = kQStages * 2 * kTileBytes;
+    static constexpr int kOffV = kOffK + kStages * kTileBytes;
+    static constexpr int kOffKC = kOffV + kStages * kTileBytes;
+    static constexpr int kOffVC = kOffKC + kCodeStages * kCodeBytes;
+    static constexpr int kOffO = kOffVC + kCodeStages * kCodeBytes;  // [2] 128 rows x 64 columns
+    static constexpr int kOffBar = kOffO + 2 * kChunkBytes;
+    static constexpr int bQFull = 0;                     // [kQStages] both tiles landed
+    static constexpr int bQEmpty = bQFull + kQStages;    // [kQStages] S products done (MMA commit)
+    static constexpr int bKFull = bQEmpty + kQStages;    // [kStages] key tile there (TMA, or 128 converter arrivals)
+    static constexpr int bKEmpty = bKFull + kStages;
+    static constexpr int bVFull = bKEmpty + kStages;
+    static constexpr int bVEmpty = bVFull + kStages;
+    static constexpr int bVReady = bVEmpty + kStages;    // [kStages] rows of unkept keys cleared
+    static constexpr int bKCFull = bVReady + kStages;    // [kCodeStages] code blocks landed
+    static constexpr int bKCEmpty = bKCFull + kCodeStages;
+    static constexpr int bVCFull = bKCEmpty + kCodeStages;
+    static constexpr int bVCEmpty = bVCFull + kCodeStages;
+    static constexpr int bSFull = bVCEmpty + kCodeStages;
+    static constexpr int bSFree = bSFull + 2;
+    static constexpr int bPFull = bSFree + 2;
+    static constexpr int bPFree = bPFull + 2;
+    static constexpr int bTurn = bPFree + 2;             // [2][4]
+    static constexpr int bEpi = bTurn + 8;               // [2] a softmax warpgroup's own barrier (128 arrivals)
+    static constexpr int bDrain = bEpi + 2;              // [2]
+    static constexpr int kNumBars = bDrain + 2;
+    static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+    static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+    static constexpr uint32_t kTmemCols = 512;
+    static constexpr bool kSeparateP = (D == 64);
+    static constexpr bool kUseTurn = (D == 64);
+    __device__ static constexpr uint32_t col_s(int q) { return uint32_t(q * 128); }
+    __device__ static constexpr uint32_t col_o(int q) { return uint32_t(256 + q * D); }
+    __device__ static constexpr uint32_t col_p(int q) { return kSeparateP ? uint32_t(256 + 2 * D + q * 64) : col_s(q); }
+};
+
+// ---------------------------------------------------------------------------
+// Units
+// ---------------------------------------------------------------------------
+struct XaUnit {
+    int b, h, kvh;
+    int row0;    // first query row
+    int nt;      // query tiles (1 or 2)
+    int len;     // keys of this batch row
+    int jb, je;  // key blocks [jb, je)
+    int split;
+};
+
+__device__ __forceinline__ XaUnit xa_unit(const XaParams &p, int unit) {
+    XaUnit u;
+    u.split = unit % p.n_splits;
+    const int r = unit / p.n_splits;
+    const int bh = r / p.n_qpairs;
+    u.row0 = (r - bh * p.n_qpairs) * 256;
+    u.b = bh / p.heads;
+    u.h = bh - u.b * p.heads;
+    u.kvh = u.h / p.group;
+    u.nt = p.Lq - u.row0 > 128 ? 2 : 1;
+    u.len = p.kv_lens ? min(max(__ldg(p.kv_lens + u.b), 0), p.Lk) : p.Lk;
+    const long long nblk = (u.len + 127) / 128;
+    u.jb = int(nblk * u.split / p.n_splits);
+    u.je = int(nblk * (u.split + 1) / p.n_splits);
+    return u;
+}
+
+__device__ __forceinline__ int xa_block_keys(const XaUnit &u, int j) { return min(128, u.len - j * 128); }
+
+// Which of block j's 128 keys are attended: bit i of w[c] is key 32 c + i.
+// Executed by a whole warp; every lane gets all words.
+__device__ __forceinline__ void xa_keep(const XaParams &p, const XaUnit &u, int j, int n, uint32_t (&w)[4]) {
+    if (p.key_mask) {
+        const unsigned char *m = p.key_mask + (size_t)u.b * p.Lk + (size_t)j * 128;
+        const int lane = threadIdx.x & 31;
+        bool k[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) k[c] = 32 * c + lane < n && __ldg(m + 32 * c + lane) != 0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) w[c] = __ballot_sync(0xffffffffu, k[c]);
+    } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int m = n - 32 * c;
+            w[c] = m >= 32 ? 0xffffffffu : m <= 0 ? 0u : (1u << m) - 1u;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Producer
+// ---------------------------------------------------------------------------
+template <int D, bool KV8>
+__device__ void xa_producer(const XaParams &p, uint8_t *smem, uint64_t *bars, volatile uint32_t *abort_flag) {
+    using C = XaCfg<D, KV8>;
+    constexpr int kRing = KV8 ? C::kCodeStages : C::kStages;
+    constexpr int kBytes = KV8 ? C::kCodeBytes : C::kTileBytes;
+    constexpr int kOffKr = KV8 ? C::kOffKC : C::kOffK, kOffVr = KV8 ? C::kOffVC : C::kOffV;
+    constexpr int bKF = KV8 ? C::bKCFull : C::bKFull, bKE = KV8 ? C::bKCEmpty : C::bKEmpty;
+    constexpr int bVF = KV8 ? C::bVCFull : C::bVFull, bVE = KV8 ? C::bVCEmpty : C::bVEmpty;
+    const uint64_t lim = p.wait_limit_ns;
+    sm100::tma_prefetch_desc(&p.tm_q);
+    sm100::tma_prefetch_desc(&p.tm_k);
+    sm100::tma_prefetch_desc(&p.tm_v);
+    sm100::tma_prefetch_desc(&p.tm_o);
+    int nk = 0, nv = 0, uq = 0;
+    bool ok = true;
+    for (int unit = blockIdx.x; ok && unit < p.n_units; unit += gridDim.x) {
+        const XaUnit u = xa_unit(p, unit);
+        if (u.je <= u.jb) continue;
+        const int qs = uq % C::kQStages, quse = uq / C::kQStages;
+        if (quse > 0 && !sm100::mbar_wait(&bars[C::bQEmpty + qs], (quse - 1) & 1, lim)) {
+            ok = false;
+            break;
+        }
+        sm100::mbar_arrive_expect_tx(&bars[C::bQFull + qs], u.nt * C::kTileBytes);
+        for (int t = 0; t < u.nt; ++t) {
+            const int r = bound_coord(u.row0 + t * 128, p.Lq);
+            uint8_t *dst = smem + C::kOffQ + (qs * 2 + t) * C::kTileBytes;
+#pragma unroll
+            for (int c = 0; c < C::kChunks; ++c)
+                sm100::tma_load_4d(dst + c * C::kChunkBytes, &p.tm_q, &bars[C::bQFull + qs], c * 64, r,
+                                   bound_coord(u.h, p.heads) * p.q_h, bound_coord(u.b, p.B) * p.q_b);
+        }
+        ++uq;
+        const int kh = bound_coord(u.kvh, p.kv_heads), kb = bound_coord(u.b, p.B);
+        for (int j = u.jb; j < u.je; ++j) {
+            if (*abort_flag) {
+                ok = false;
+                break;
+            }
+            const int s = nk % kRing, use = nk / kRing;
+            const int r = bound_coord(j * 128, p.Lk);
+            if (use > 0 && !sm100::mbar_wait(&bars[bKE + s], (use - 1) & 1, lim)) {
+                ok = false;
+                break;
+            }
+            sm100::mbar_arrive_expect_tx(&bars[bKF + s], kBytes);
+            if (KV8) {
+                sm100::tma_load_4d(smem + kOffKr + s * kBytes, &p.tm_k, &bars[bKF + s], 0, r, kh, kb);
+            } else {
+#pragma unroll
+                for (int c = 0; c < C::kChunks; ++c)
+                    sm100::tma_load_4d(smem + kOffKr + s * kBytes + c * C::kChunkBytes, &p.tm_k, &bars[bKF + s],
+                                       c * 64, r, kh * p.k_h, kb * p.k_b);
+            }
+            ++nk;
+            if (use > 0 && !sm100::mbar_wait(&bars[bVE + s], (use - 1) & 1, lim)) {
+                ok = false;
+                break;
+            }
+            sm100::mbar_arrive_expect_tx(&bars[bVF + s], kBytes);
+            if (KV8) {
+                sm100::tma_load_4d(smem + kOffVr + s * kBytes, &p.tm_v, &bars[bVF + s], 0, r, kh, kb);
+            } else {
+#pragma unroll
+                for (int c = 0; c < C::kChunks; ++c)
+                    sm100::tma_load_4d(smem + kOffVr + s * kBytes + c * C::kChunkBytes, &p.tm_v, &bars[bVF + s],
+                                       c * 64, r, kh * p.v_h, kb * p.v_b);
+            }
+            ++nv;
+        }
+    }
+    if (!ok) {
+        record_error(kErrDeviceTimeout);
+        *abort_flag = 1;
+    }
+    // every issued copy must have landed before the CTA may exit
+    for (int s = 0; s < C::kQStages; ++s)
+        if (uq > s) sm100::mbar_wait(&bars[C::bQFull + s], ((uq - 1 - s) / C::kQStages) & 1, lim);
+    for (int s = 0; s < kRing; ++s) {
+        if (nk > s) sm100::mbar_wait(&bars[bKF + s], ((nk - 1 - s) / kRing) & 1, lim);
+        if (nv > s) sm100::mbar_wait(&bars[bVF + s], ((nv - 1 - s) / kRing) & 1, lim);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// MMA issuers
+// ---------------------------------------------------------------------------
+// S_q[:, 0 .. n) = Q K^T for the block's n keys (n rounded up to 16).
+template <int D, bool F16>
+__device__ __forceinline__ void xa_issue_s(uint32_t d_tmem, uint64_t qdesc, uint64_t kdesc, int n) {
+    using C = XaCfg<D, false>;
+    constexpr uint32_t kId0 = F16 ? sm100::idesc_f16_f32(128, 0, false, false) : sm100::idesc_bf16_f32(128, 0, false, false);
+    const uint32_t id = kId0 | (uint32_t((n + 15) >> 4) << 18);  // N >> 3 at bit 17
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+        const uint64_t off = uint64_t(((kk >> 2) * C::kChunkBytes + (kk & 3) * 32) >> 4);
+        sm100::mma_ss(d_tmem, qdesc + off, kdesc + off, id, kk > 0 ? 1u : 0u);
+    }
+}
+
+// O_q (+)= P_q V over the block's n keys (n rounded up to 16; P is 0 and V is
+// finite past n).
+template <int D, bool F16>
+__device__ __forceinline__ void xa_issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint64_t vdesc, int n, bool accumulate) {
+    constexpr uint32_t kId = F16 ? sm100::idesc_f16_f32(128, D, false, true) : sm100::idesc_bf16_f32(128, D, false, true);
+    const int steps = (n + 15) >> 4;
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+        if (kk < steps)
+            sm100::mma_ts(o_tmem, p_tmem + kk * 8, vdesc + uint64_t((kk * 2048) >> 4), kId,
+                          (accumulate || kk > 0) ? 1u : 0u);
+}
+
+template <int D, bool KV8>
+struct XaDescs {
+    uint64_t q0, k0, v0;
+    static constexpr uint64_t tile = uint64_t(XaCfg<D, KV8>::kTileBytes >> 4);
+    __device__ explicit XaDescs(uint8_t *smem) {
+        using C = XaCfg<D, KV8>;
+        q0 = sm100::sdesc_sw128(sm100::smem_u32(smem + C::kOffQ), 16, 1024);
+        k0 = sm100::sdesc_sw128(sm100::smem_u32(smem + C::kOffK), 16, 1024);
+        v0 = sm100::sdesc_sw128(sm100::smem_u32(smem + C::kOffV), C::kChunkBytes, 1024);
+    }
+};
+
+// The barrier that says block values are ready for the products: the copy's
+// own, or the one of the warp that clears unkept rows.
+template <int D, bool KV8>
+__device__ __forceinline__ int xa_v_bar(const XaParams &p) {
+    using C = XaCfg<D, KV8>;
+    return !KV8 && (p.kv_lens || p.key_mask) ? C::bVReady : C::bVFull;
+}
+
+// d = 64: the S products.
+template <int D, bool KV8, bool F16>
+__device__ void xa_mma_s(const XaParams &p, uint8_t *smem, uint64_t *bars, uint32_t tmem,
+                         volatile uint32_t *abort_flag) {
+    using C = XaCfg<D, KV8>;
+    const uint64_t lim = p.wait_limit_ns;
+    const XaDescs<D, KV8> dd(smem);
+    int kv = 0, uq = 0, g[2] = {0, 0};
+    bool ok = true;
+    for (int unit = blockIdx.x; ok && unit < p.n_units; unit += gridDim.x) {
+        const XaUnit u = xa_unit(p, unit);
+        if (u.je <= u.jb) continue;
+        const int qs = uq % C::kQStages;
+        ok = sm100::mbar_wait(&bars[C::bQFull + qs], (uq / C::kQStages) & 1, lim);
+        ++uq;
+        for (int j = u.jb; ok && j < u.je; ++j, ++kv) {
+            if (*abort_flag) {
+                ok = false;
+                break;
+            }
+            const int s = kv % C::kStages, n = xa_block_keys(u, j);
+            ok = sm100::mbar_wait(&bars[C::bKFull + s], (kv / C::kStages) & 1, lim);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                if (!ok || q >= u.nt) continue;
+                if (g[q] > 0) ok = sm100::mbar_wait(&bars[C::bSFree + q], (g[q] - 1) & 1, lim);
+                if (!ok) continue;
+                sm100::tc_fence_after();
+                xa_issue_s<D, F16>(tmem + C::col_s(q), dd.q0 + (qs * 2 + q) * dd.tile, dd.k0 + s * dd.tile, n);
+                sm100::tc_commit(&bars[C::bSFull + q]);
+                ++g[q];
+            }
+            if (ok) sm100::tc_commit(&bars[C::bKEmpty + s]);
+        }
+        if (ok) sm100::tc_commit(&bars[C::bQEmpty + qs]);
+    }
+    if (!ok) {
+        record_error(kErrDeviceTimeout);
+        *abort_flag = 1;
+    }
+    sm100::tc_commit(&bars[C::bDrain]);
+    sm100::mbar_wait(&bars[C::bDrain], 0, lim);
+}
+
+// d = 64: the P.V products.
+template <int D, bool KV8, bool F16>
+__device__ void xa_mma_pv(const XaParams &p, uint8_t *smem, uint64_t *bars, uint32_t tmem,
+                          volatile uint32_t *abort_flag) {
+    using C = XaCfg<D, KV8>;
+    const uint64_t lim = p.wait_limit_ns;
+    const XaDescs<D, KV8> dd(smem);
+    const int bV = xa_v_bar<D, KV8>(p);
+    int kv = 0, g[2] = {0, 0};
+    bool ok = true;
+    for (int unit = blockIdx.x; ok && unit < p.n_units; unit += gridDim.x) {
+        const XaUnit u = xa_unit(p, unit);
+        for (int j = u.jb; ok && j < u.je; ++j, ++kv) {
+            if (*abort_flag) {
+                ok = false;
+                break;
+            }
+            const int s = kv % C::kStages, n = xa_block_keys(u, j);
+            ok = sm100::mbar_wait(&bars[bV + s], (kv / C::kStages) & 1, lim);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                if (!ok || q >= u.nt) continue;
+                ok = sm100::mbar_wait(&bars[C::bPFull + q], g[q] & 1, lim);
+                if (!ok) continue;
+                sm100::tc_fence_after();
+                xa_issue_pv<D, F16>(tmem + C::col_o(q), tmem + C::col_p(q), dd.v0 + s * dd.tile, n, j > u.jb);
+                sm100::tc_commit(&bars[C::bPFree + q]);
+                ++g[q];
+            }
+            if (ok) sm100::tc_commit(&bars[C::bVEmpty + s]);
+        }
+    }
+    if (!ok) {
+        record_error(kErrDeviceTimeout);
+        *abort_flag = 1;
+    }
+    sm100::tc_commit(&bars[C::bDrain + 1]);
+    sm100::mbar_wait(&bars[C::bDrain + 1], 0, lim);
+}
+
+// d = 128 (P aliases S): PV_q(j-1) before S_q(j) from one thread, so that the
+// completion of S_q(j) also says that PV_q(j-1) is done.
+template <int D, bool KV8, bool F16>
+__device__ void xa_mma(const XaParams &p, uint8_t *smem, uint64_t *bars, uint32_t tmem,
+                       volatile uint32_t *abort_flag) {
+    using C = XaCfg<D, KV8>;
+    const uint64_t lim = p.wait_limit_ns;
+    const XaDescs<D, KV8> dd(smem);
+    const int bV = xa_v_bar<D, KV8>(p);
+    int kv0 = 0, uq = 0, g[2] = {0, 0};  // kv0: ring index of the unit's first block; g: P blocks consumed
+    bool ok = true;
+    for (int unit = blockIdx.x; ok && unit < p.n_units; unit += gridDim.x) {
+        const XaUnit u = xa_unit(p, unit);
+        const int n_blk = u.je - u.jb;
+        if (n_blk <= 0) continue;
+        const int qs = uq % C::kQStages;
+        ok = sm100::mbar_wait(&bars[C::bQFull + qs], (uq / C::kQStages) & 1, lim);
+        ++uq;
+        for (int j = 0; ok && j <= n_blk; ++j) {
+            if (*abort_flag) {
+                ok = false;
+                break;
+            }
+            const int kv = kv0 + j, s = kv % C::kStages;
+            const int sp = (kv + C::kStages - 1) % C::kStages;  // the previous block's stage
+            if (j < n_blk) ok = sm100::mbar_wait(&bars[C::bKFull + s], (kv / C::kStages) & 1, lim);
+            if (ok && j > 0) ok = sm100::mbar_wait(&bars[bV + sp], ((kv - 1) / C::kStages) & 1, lim);
+            if (!ok) break;
+            sm100::tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                if (!ok || q >= u.nt) continue;
+                if (j > 0) {
+                    ok = sm100::mbar_wait(&bars[C::bPFull + q], g[q] & 1, lim);
+                    if (!ok) continue;
+                    sm100::tc_fence_after();
+                    xa_issue_pv<D, F16>(tmem + C::col_o(q), tmem + C::col_p(q), dd.v0 + sp * dd.tile,
+                                        xa_block_keys(u, u.jb + j - 1), j > 1);
+                    sm100::tc_commit(&bars[C::bPFree + q]);
+                    ++g[q];
+                }
+                if (j < n_blk) {
+                    xa_issue_s<D, F16>(tmem + C::col_s(q), dd.q0 + (qs * 2 + q) * dd.tile, dd.k0 + s * dd.tile,
+                                       xa_block_keys(u, u.jb + j));
+                    sm100::tc_commit(&bars[C::bSFull + q]);
+                }
+            }
+            if (!ok) break;
+            if (j < n_blk) sm100::tc_commit(&bars[C::bKEmpty + s]);
+            if (j == n_blk - 1) sm100::tc_commit(&bars[C::bQEmpty + qs]);
+            if (j > 0) sm100::tc_commit(&bars[C::bVEmpty + sp]);
+        }
+        kv0 += n_blk;
+    }
+    if (!ok) {
+        record_error(kErrDeviceTimeout);
+        *abort_flag = 1;
+    }
+    sm100::tc_commit(&bars[C::bDrain]);
+    sm100::mbar_wait(&bars[C::bDrain], 0, lim);
+}
+
+// ---------------------------------------------------------------------------
+// 16-bit values: rows of unkept keys set to zero (one warp). P is 0 there, but
+// a NaN or an infinity in padding would still spread through the product.
+// ---------------------------------------------------------------------------
+template <int D>
+__device__ void xa_clear_unkept(const XaParams &p, uint8_t *smem, uint64_t *bars, volatile uint32_t *abort_flag) {
+    using C = XaCfg<D, false>;
+    const uint64_t lim = p.wait_limit_ns;
+    const int lane = threadIdx.x & 31;
+    int kv = 0;
+    bool ok = true;
+    for (int unit = blockIdx.x; ok && unit < p.n_units; unit += gridDim.x) {
+        const XaUnit u = xa_unit(p, unit);
+        for (int j = u.jb; j < u.je; ++j, ++kv) {
+            const int s = kv % C::kStages, n = xa_block_keys(u, j);
+            uint32_t w[4];
+            xa_keep(p, u, j, n, w);
+            ok = !*abort_flag && sm100::mbar_wait(&bars[C::bVFull + s], (kv / C::kStages) & 1, lim);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            uint8_t *tile = smem + C::kOffV + s * C::kTileBytes;
+            const int n16 = (n + 15) & ~15;  // rows that the product reads
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int row = 32 * c + lane;
+                if (row < n16 && !(w[c] >> lane & 1)) {
+#pragma unroll
+                    for (int ch = 0; ch < C::kChunks; ++ch)
+#pragma unroll
+                        for (int v = 0; v < 8; ++v)
+                            *reinterpret_cast<uint4 *>(tile + ch * C::kChunkBytes + row * 128 + v * 16) =
+                                make_uint4(0, 0, 0, 0);
+                }
+            }
+            sm100::fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) sm100::mbar_arrive(&bars[C::bVReady + s]);
+        }
+    }
+    if (!ok) {
+        record_error(kErrDeviceTimeout);
+        *abort_flag = 1;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit cache: code blocks to bf16 tiles (one warpgroup). code * scale is
+// exact in bf16 for the power-of-two scales that npa_kv8_store writes (an
+// e4m3 number has 4 significant bits); another scale is rounded once. Values
+// of unkept keys are written as zeros.
+// ---------------------------------------------------------------------------
+template <int D>
+__device__ __forceinline__ void xa_convert_tile(const uint8_t *codes, uint8_t *tile, float s0, float s1,
+                                                const uint32_t (&w)[4], int tid) {
+    using C = XaCfg<D, true>;
+    constexpr int kPerRow = D / 16;  // 16-code pieces of a row
+#pragma unroll
+    for (int i = 0; i < kPerRow; ++i) {
+        const int idx = tid + 128 * i;
+        const int row = idx / kPerRow, piece = idx % kPerRow;
+        const uint4 c4 = *reinterpret_cast<const uint4 *>(codes + idx * 16);
+        const float sc = row < kKv8Block ? s0 : s1;
+        const uint32_t keep = w[row >> 5] >> (row & 31) & 1u;
+        const uint32_t c[4] = {c4.x, c4.y, c4.z, c4.w};
+        uint32_t o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t h2 = sm100::e4m3x2_to_f16x2(c[k >> 1] >> ((k & 1) * 16));
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
+            o[k] = keep ? sm100::pack_bf16x2(f.x * sc, f.y * sc) : 0u;
+        }
+        uint8_t *dst = tile + (piece >> 2) * C::kChunkBytes + row * 128;
+        const int p0 = (piece & 3) * 2;
+        *reinterpret_cast<uint4 *>(dst + ((p0 ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(dst + (((p0 + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+}
+
+template <int D>
+__device__ void xa_convert(const XaParams &p, uint8_t *smem, uint64_t *bars, volatile uint32_t *abort_flag) {
+    using C = XaCfg<D, true>;
+    const uint64_t lim = p.wait_limit_ns;
+    const int tid = threadIdx.x - C::kConvWarp * 32;
+    int kv = 0;
+    bool ok = true;
+    for (int unit = blockIdx.x; ok && unit < p.n_units; unit += gridDim.x) {
+        const XaUnit u = xa_unit(p, unit);
+        const size_t sbase = ((size_t)u.b * p.kv_heads + u.kvh) * p.scale_blocks;
+        const int last = p.scale_blocks - 1;  // a block past the cache's last repeats it (its rows are not kept)
+        for (int j = u.jb; j < u.je; ++j, ++kv) {
+            const int i0 = min(2 * j, last), i1 = min(2 * j + 1, last);
+            const float ks0 = __ldg(p.k_scale + sbase + i0), ks1 = __ldg(p.k_scale + sbase + i1);
+            const float vs0 = __ldg(p.v_scale + sbase + i0), vs1 = __ldg(p.v_scale + sbase + i1);
+            uint32_t w[4];
+            xa_keep(p, u, j, xa_block_keys(u, j), w);
+            const int cs = kv % C::kCodeStages, cpar = (kv / C::kCodeStages) & 1;
+            const int s = kv % C::kStages, use = kv / C::kStages;
+            ok = !*abort_flag && sm100::mbar_wait(&bars[C::bKCFull + cs], cpar, lim) &&
+                 (use == 0 || sm100::mbar_wait(&bars[C::bKEmpty + s], (use - 1) & 1, lim));
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            xa_convert_tile<D>(smem + C::kOffKC + cs * C::kCodeBytes, smem + C::kOffK + s * C::kTileBytes, ks0, ks1, w,
+                               tid);
+            sm100::fence_proxy_async();
+            sm100::mbar_arrive(&bars[C::bKFull + s]);
+            sm100::mbar_arrive(&bars[C::bKCEmpty + cs]);
+            ok = sm100::mbar_wait(&bars[C::bVCFull + cs], cpar, lim) &&
+                 (use == 0 || sm100::mbar_wait(&bars[C::bVEmpty + s], (use - 1) & 1, lim));
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            xa_convert_tile<D>(smem + C::kOffVC + cs * C::kCodeBytes, smem + C::kOffV + s * C::kTileBytes, vs0, vs1, w,
+                               tid);
+            sm100::fence_proxy_async();
+            sm100::mbar_arrive(&bars[C::bVFull + s]);
+            sm100::mbar_arrive(&bars[C::bVCEmpty + cs]);
+        }
+    }
+    if (!ok) {
+        record_error(kErrDeviceTimeout);
+        *abort_flag = 1;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Softmax and epilogue
+// ---------------------------------------------------------------------------
+// The scores of a block's first 32 * NCH keys, unkept ones as -inf.
+template <int NCH>
+__device__ __forceinline__ void xa_load_scores(uint32_t t_s, const uint32_t (&w)[4], float (&s)[32 * NCH]) {
+    if constexpr (NCH == 4) {
+        uint32_t r[128];
+        sm100::tmem_ld128(t_s, r);
+#pragma unroll
+        for (int i = 0; i < 128; ++i) s[i] = __uint_as_float(r[i]);
+    } else {
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) {
+            uint32_t r[32];
+            sm100::tmem_ld32(t_s + 32 * c, r);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[32 * c + i] = __uint_as_float(r[i]);
+        }
+    }
+    uint32_t all = 0xffffffffu;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) all &= w[c];
+    if (all != 0xffffffffu) {
+#pragma unroll
+        for (int i = 0; i < 32 * NCH; ++i)
+            if (!(w[i >> 5] >> (i & 31) & 1u)) s[i] = -INFINITY;
+    }
+}
+
+template <int NCH>
+__device__ __forceinline__ void xa_store_p(uint32_t t_p, const uint32_t (&pk)[16 * NCH]) {
+    if constexpr (NCH == 4) {
+        sm100::tmem_st64(t_p, pk);
+    } else {
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) {
+            uint32_t r[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i] = pk[16 * c + i];
+            sm100::tmem_st16(t_p + 16 * c, r);
+        }
+    }
+}
+
+template <int D, bool KV8, bool F16>
+struct XaSoftmax {
+    using C = XaCfg<D, KV8>;
+    // A block whose maximum exceeds the reference by more than kLead moves it
+    // to kBelow under the maximum: P stays within 2^8 in bf16. In f16 the
+    // probabilities are kept 2^7 higher (at most 2^15), so that those 2^-24
+    // below the row's largest are still normal numbers.
+    static constexpr float kLead = F16 ? 15.f : kRescaleLog2;
+    static constexpr float kBelow = F16 ? 7.f : 0.f;
+
+    const XaParams &p;
+    uint64_t *bars;
+    uint64_t lim;
+    uint32_t tS, tO, tP;
+    int q, warp;  // tile, warp within the warpgroup
+    bool lane0;
+    int g, tb;    // blocks of this tile so far; blocks of two-tile units so far
+    float R, R_prev, l;
+
+    __device__ __forceinline__ bool take_turn() {
+        return !C::kUseTurn || (q == 0 && tb == 0) ||
+               warp_wait(&bars[C::bTurn + 4 * q + warp], (q == 0 ? tb - 1 : tb) & 1, lim);
+    }
+    __device__ __forceinline__ void pass_turn() {
+        if (C::kUseTurn) {
+            __syncwarp();
+            if (lane0) sm100::mbar_arrive(&bars[C::bTurn + 4 * (1 - q) + warp]);
+        }
+    }
+
+    // One block of at most 32 * NCH keys; false when a wait ran out.
+    template <int NCH>
+    __device__ __forceinline__ bool block(const uint32_t (&w)[4], bool first, bool turns) {
+        constexpr int kN = 32 * NCH;
+        float s[kN];
+        xa_load_scores<NCH>(tS, w, s);
+        if (C::kSeparateP) {
+            sm100::tc_fence_before();
+            sm100::mbar_arrive(&bars[C::bSFree + q]);
+        }
+        const float bm = row_max<kN>(s) * p.scale_log2;
+        if (bm > R + kLead) R = bm - kBelow;
+        if (turns && !take_turn()) return false;
+        uint32_t pk[kN / 2];
+        const float sum = exp_block<kN, F16>(s, p.scale_log2, R, pk);
+        if (turns) pass_turn();
+        const float alpha = (R == R_prev) ? 1.f : sm100::ex2_approx(R_prev - R);
+        if (C::kSeparateP && !first) {
+            if (!warp_wait(&bars[C::bPFree + q], (g - 1) & 1, lim)) return false;
+            sm100::tc_fence_after();
+        }
+        if (!first && __any_sync(0xffffffffu, alpha != 1.f)) rescale(alpha);
+        l = l * alpha + sum;
+        xa_store_p<NCH>(tP, pk);
+        sm100::tc_fence_before();
+        sm100::mbar_arrive(&bars[C::bPFull + q]);
+        R_prev = R;
+        return true;
+    }
+
+    // The same in two passes over the scores in TMEM, 32 at a time, for the
+    // 8-bit kernel: its 512 threads leave 128 registers each at launch, too few
+    // to hold a row of scores.
+    template <int NCH>
+    __device__ __forceinline__ bool block_lean(const uint32_t (&w)[4], bool first, bool turns) {
+        float bm = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) {
+            float s[32];
+            xa_load_scores<1>(tS + 32 * c, {w[c], 0, 0, 0}, s);
+            bm = fmaxf(bm, row_max<32>(s));
+        }
+        bm *= p.scale_log2;
+        if (bm > R + kLead) R = bm - kBelow;
+        const float alpha = (R == R_prev) ? 1.f : sm100::ex2_approx(R_prev - R);
+        if (C::kSeparateP && !first) {
+            if (!warp_wait(&bars[C::bPFree + q], (g - 1) & 1, lim)) return false;
+            sm100::tc_fence_after();
+        }
+        if (!first && __any_sync(0xffffffffu, alpha != 1.f)) rescale(alpha);
+        if (turns && !take_turn()) return false;
+        float sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) {
+            float s[32];
+            xa_load_scores<1>(tS + 32 * c, {w[c], 0, 0, 0}, s);
+            uint32_t pk[16];
+            sum += exp_block<32, F16>(s, p.scale_log2, R, pk);
+            sm100::tmem_st16(tP + 16 * c, pk);
+        }
+        if (turns) pass_turn();
+        l = l * alpha + sum;
+        sm100::tc_fence_before();
+        if (C::kSeparateP) sm100::mbar_arrive(&bars[C::bSFree + q]);
+        sm100::mbar_arrive(&bars[C::bPFull + q]);
+        R_prev = R;
+        return true;
+    }
+
+    // O *= alpha.
+    __device__ __forceinline__ void rescale(float alpha) {
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            sm100::tmem_ld32(tO + c * 32, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            sm100::tmem_st32(tO + c * 32, o);
+        }
+    }
+
+    template <int NCH>
+    __device__ __forceinline__ bool run_block(const uint32_t (&w)[4], bool first, bool turns) {
+        if constexpr (KV8)
+            return block_lean<NCH>(w, first, turns);
+        else
+            return block<NCH>(w, first, turns);
+    }
+
+    // A warp whose 32 rows lie past the last query keeps the barriers' counts.
+    __device__ __forceinline__ bool idle_block(bool first, bool turns) {
+        if (C::kSeparateP) sm100::mbar_arrive(&bars[C::bSFree + q]);
+        if (turns) {
+            if (!take_turn()) return false;
+            pass_turn();
+        }
+        if (C::kSeparateP && !first && !warp_wait(&bars[C::bPFree + q], (g - 1) & 1, lim)) return false;
+        sm100::mbar_arrive(&bars[C::bPFull + q]);
+        return true;
+    }
+};
+
+template <int D, bool KV8, bool F16>
+__device__ void xa_softmax(const XaParams &p, uint8_t *smem, uint64_t *bars, uint32_t tmem,
+                           volatile uint32_t *abort_flag, int q) {
+    using C = XaCfg<D, KV8>;
+    const uint64_t lim = p.wait_limit_ns;
+    const int row = threadIdx.x & 127;
+    const int warp = row >> 5;
+    const uint32_t lane_off = uint32_t(warp) * 32u << 16;
+    XaSoftmax<D, KV8, F16> st{p,    bars, lim,  tmem + lane_off + C::col_s(q), tmem + lane_off + C::col_o(q),
+                              tmem + lane_off + C::col_p(q), q, warp, (threadIdx.x & 31) == 0, 0, 0, 0.f, 0.f, 0.f};
+    uint8_t *stage = smem + C::kOffO + q * C::kChunkBytes;
+    int ep = 0;  // uses of the warpgroup's own barrier
+    auto group_sync = [&]() {
+        sm100::mbar_arrive(&bars[C::bEpi + q]);
+        return warp_wait(&bars[C::bEpi + q], (ep++) & 1, lim);
+    };
+    bool ok = true;
+    for (int unit = blockIdx.x; ok && unit < p.n_units; unit += gridDim.x) {
+        const XaUnit u = xa_unit(p, unit);
+        if (q >= u.nt) continue;
+        const int grow = u.row0 + q * 128 + row;  // this thread's query
+        const bool active = u.row0 + q * 128 + warp * 32 < p.Lq;
+        const bool turns = u.nt == 2;
+        st.R = st.R_prev = -INFINITY;
+        st.l = 0.f;
+        for (int j = u.jb; j < u.je; ++j) {
+            const int n = xa_block_keys(u, j);
+            uint32_t w[4];
+            xa_keep(p, u, j, n, w);
+            ok = warp_wait(&bars[C::bSFull + q], st.g & 1, lim);
+            if (!ok) break;
+            sm100::tc_fence_after();
+            const bool first = j == u.jb;
+            if (!active)
+                ok = st.idle_block(first, turns);
+            else if (n > 96)
+                ok = st.template run_block<4>(w, first, turns);
+            else if (n > 64)
+                ok = st.template run_block<3>(w, first, turns);
+            else if (n > 32)
+                ok = st.template run_block<2>(w, first, turns);
+            else
+                ok = st.template run_block<1>(w, first, turns);
+            ++st.g;
+            st.tb += turns;
+            if (!ok) break;
+        }
+        const bool any = u.je > u.jb;
+        // the last P.V product of this tile
+        if (ok && any) ok = warp_wait(&bars[C::bPFree + q], (st.g - 1) & 1, lim);
+        if (!ok) break;
+        sm100::tc_fence_after();
+        const size_t bh = (size_t)u.b * p.heads + u.h;
+        if (p.n_splits > 1) {
+            const size_t rows = (size_t)p.B * p.heads * p.Lq;
+            const size_t prow = u.split * rows + bh * p.Lq + grow;
+            const bool valid = bound_row(grow < p.Lq, prow, rows * p.n_splits);
+            if (valid) *reinterpret_cast<float2 *>(p.ml + prow * 2) = make_float2(any ? st.R_prev : -INFINITY, st.l);
+            if (any && active) {
+                float4 *part = reinterpret_cast<float4 *>(p.o_part + prow * D);
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    sm100::tmem_ld32(st.tO + c * 32, o);
+                    if (valid) {
+#pragma unroll
+                        for (int v = 0; v < 8; ++v)
+                            part[c * 8 + v] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
+                                                          __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
+                    }
+                }
+            }
+            continue;
+        }
+        // O / l through shared memory, 64 columns at a time (128-byte rows,
+        // the tensor map's swizzle), and out by TMA
+        const float inv_l = st.l > 0.f ? 1.f / st.l : st.l == 0.f ? 0.f : st.l;
+        for (int ch = 0; ch < C::kChunks; ++ch) {
+            if (row == 0) sm100::bulk_wait_read();  // the previous store has read the stage
+            ok = group_sync();
+            if (!ok) break;
+            if (active) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t o[32];
+                    if (any) {
+                        sm100::tmem_ld32(st.tO + ch * 64 + c * 32, o);
+                    }
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        uint32_t h[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float a = __uint_as_float(o[8 * v + 2 * i]), b = __uint_as_float(o[8 * v + 2 * i + 1]);
+                            h[i] = any && st.l != 0.f ? sm100::pack_16x2<F16>(a * inv_l, b * inv_l) : 0u;
+                        }
+                        *reinterpret_cast<uint4 *>(stage + row * 128 + (((c * 4 + v) ^ (row & 7)) << 4)) =
+                            make_uint4(h[0], h[1], h[2], h[3]);
+                    }
+                }
+            }
+            sm100::fence_proxy_async();
+            ok = group_sync();
+            if (!ok) break;
+            if (row == 0) {
+                sm100::tma_store_4d(&p.tm_o, stage, ch * 64, bound_coord(u.row0 + q * 128, p.Lq),
+                                    bound_coord(u.h, p.heads), bound_coord(u.b, p.B));
+                sm100::bulk_commit();
+            }
+        }
+    }
+    if (row == 0) sm100::bulk_wait_all();
+    if (!ok) {
+        record_error(kErrDeviceTimeout);
+        *abort_flag = 1;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The kernel
+// ---------------------------------------------------------------------------
+template <int D, bool KV8, bool F16>
+__global__ void __launch_bounds__(XaCfg<D, KV8>::kThreads, 1)
+    xa_fwd_kernel(const __grid_constant__ XaParams p) {
+    using C = XaCfg<D, KV8>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = sm100::smem_u32(smem_raw);
+    uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
+    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);  // [0] TMEM base, [1] abort flag
+    const int warp = threadIdx.x >> 5;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kQStages; ++s) {
+            sm100::mbar_init(&bars[C::bQFull + s], 1);
+            sm100::mbar_init(&bars[C::bQEmpty + s], 1);
+        }
+        for (int s = 0; s < C::kStages; ++s) {
+            sm100::mbar_init(&bars[C::bKFull + s], KV8 ? 128 : 1);
+            sm100::mbar_init(&bars[C::bKEmpty + s], 1);
+            sm100::mbar_init(&bars[C::bVFull + s], KV8 ? 128 : 1);
+            sm100::mbar_init(&bars[C::bVEmpty + s], 1);
+            sm100::mbar_init(&bars[C::bVReady + s], 1);
+        }
+        for (int s = 0; s < C::kCodeStages; ++s) {
+            sm100::mbar_init(&bars[C::bKCFull + s], 1);
+            sm100::mbar_init(&bars[C::bKCEmpty + s], 128);
+            sm100::mbar_init(&bars[C::bVCFull + s], 1);
+            sm100::mbar_init(&bars[C::bVCEmpty + s], 128);
+        }
+        for (int q = 0; q < 2; ++q) {
+            sm100::mbar_init(&bars[C::bSFull + q], 1);
+            sm100::mbar_init(&bars[C::bSFree + q], 128);
+            sm100::mbar_init(&bars[C::bPFull + q], 128);
+            sm100::mbar_init(&bars[C::bPFree + q], 1);
+            for (int k = 0; k < 4; ++k) sm100::mbar_init(&bars[C::bTurn + 4 * q + k], 1);
+            sm100::mbar_init(&bars[C::bEpi + q], 128);
+            sm100::mbar_init(&bars[C::bDrain + q], 1);
+        }
+        misc[1] = 0;
+        sm100::fence_barrier_init();
+    }
+    if (warp == C::kCtlWarp) {
+        sm100::tmem_alloc(&misc[0], C::kTmemCols);
+        sm100::tmem_relinquish();
+    }
+    sm100::tc_fence_before();
+    __syncthreads();
+    sm100::tc_fence_after();
+    const uint32_t tmem = misc[0];
+    volatile uint32_t *abort_flag = &misc[1];
+
+    if (KV8 && warp >= C::kConvWarp) {
+        sm100::setmaxnreg_dec<C::kRegsConv>();
+        if constexpr (KV8) xa_convert<D>(p, smem, bars, abort_flag);
+    } else if (warp >= C::kCtlWarp) {
+        sm100::setmaxnreg_dec<C::kRegsCtl>();
+        const int role = warp - C::kCtlWarp;
+        if (!KV8 && role == 3) {
+            if constexpr (!KV8)
+                if (p.kv_lens || p.key_mask) xa_clear_unkept<D>(p, smem, bars, abort_flag);
+        } else if ((threadIdx.x & 31) == 0) {
+            if (role == 0) xa_producer<D, KV8>(p, smem, bars, abort_flag);
+            if constexpr (C::kSeparateP) {
+                if (role == 1) xa_mma_s<D, KV8, F16>(p, smem, bars, tmem, abort_flag);
+                if (role == 2) xa_mma_pv<D, KV8, F16>(p, smem, bars, tmem, abort_flag);
+            } else {
+                if (role == 1) xa_mma<D, KV8, F16>(p, smem, bars, tmem, abort_flag);
+            }
+        }
+    } else {
+        sm100::setmaxnreg_inc<C::kRegsSoftmax>();
+        xa_softmax<D, KV8, F16>(p, smem, bars, tmem, abort_flag, warp >> 2);
+    }
+
+    sm100::tc_fence_before();
+    __syncthreads();
+    sm100::tc_fence_after();
+    if (warp == C::kCtlWarp) {
+        __syncwarp();
+        sm100::tmem_dealloc(tmem, C::kTmemCols);
+    }
+}
+
+// Merges the key-range splits: one warp per query row. With m* the largest
+// reference, o = sum_s 2^(m_s - m*) O_s / sum_s 2^(m_s - m*) l_s; a split
+// without keys has m_s = -inf and no O.
+struct XaCombineParams {
+    const float *o_part, *ml;
+    void *o;
+    long long sb, sh, st;  // strides of o in elements
+    int n_splits, rows, heads, Lq;
+};
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) xa_combine_kernel(const __grid_constant__ XaCombineParams p) {
+    const int r = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (r >= p.rows) return;
+    const int lane = threadIdx.x & 31;
+    constexpr int kPer = D / 32;
+    float mstar = -INFINITY;
+    for (int s = lane; s < p.n_splits; s += 32) mstar = fmaxf(mstar, p.ml[((size_t)s * p.rows + r) * 2]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mstar = fmaxf(mstar, __shfl_xor_sync(0xffffffffu, mstar, o));
+    float acc[kPer];
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
+    float L = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < p.n_splits; ++s) {
+        const size_t pr = (size_t)s * p.rows + r;
+        const float2 ml = __ldg(reinterpret_cast<const float2 *>(p.ml) + pr);
+        if (ml.x == -INFINITY) continue;
+        const float wgt = sm100::ex2_approx(ml.x - mstar);
+        L += wgt * ml.y;
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) acc[c] += wgt * p.o_part[pr * D + lane * kPer + c];
+    }
+    const float inv = L > 0.f ? 1.f / L : L;
+    const int bh = r / p.Lq, i = r - bh * p.Lq, b = bh / p.heads, h = bh - b * p.heads;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.o) + b * p.sb + h * p.sh + i * p.st +
+                                                 lane * kPer);
+#pragma unroll
+    for (int c = 0; c < kPer; c += 2)
+        dst[c / 2] = L == 0.f ? 0u : sm100::pack_16x2<F16>(acc[c] * inv, acc[c + 1] * inv);
+}
+
+}  // namespace npa

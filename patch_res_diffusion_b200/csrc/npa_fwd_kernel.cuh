@@ -502,8 +502,8 @@ __device__ __forceinline__ float row_max(const float (&s)[KB]) {
     return sm100::max3(sm100::max3(mk[0], mk[1], mk[2]), sm100::max3(mk[3], mk[4], mk[5]), fmaxf(mk[6], mk[7]));
 }
 
-// p = 2^(s*c - ref) for KB scores: packed bf16 pairs into pk, float32 sum returned.
-template <int KB>
+// p = 2^(s*c - ref) for KB scores: packed bf16 (or f16) pairs into pk, float32 sum returned.
+template <int KB, bool kF16 = false>
 __device__ __forceinline__ float exp_block(const float (&s)[KB], float c, float ref, uint32_t (&pk)[KB / 2]) {
     const float neg = (ref == -INFINITY) ? 0.f : -ref;
     const uint64_t c2 = sm100::pack_f32x2(c, c);
@@ -516,7 +516,7 @@ __device__ __forceinline__ float exp_block(const float (&s)[KB], float c, float 
         sm100::unpack_f32x2(x2, x0, x1);
         const float p0 = sm100::ex2_approx(x0);
         const float p1 = sm100::ex2_approx(x1);
-        pk[i] = sm100::pack_bf16x2(p0, p1);
+        pk[i] = sm100::pack_16x2<kF16>(p0, p1);
         acc[i & 3] = sm100::add_f32x2(acc[i & 3], sm100::pack_f32x2(p0, p1));
     }
     float a0, a1, b0, b1, c0, c1, d0, d1;
