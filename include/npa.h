@@ -273,7 +273,7 @@ npa_status npa_cross_attention_fwd(const void *q, const void *k, const void *v, 
 /* Workspace bytes npa_cross_attention_fwd and npa_kv8_cross_attention_fwd use
  * for their planned split count on the current device (0: none needed, or
  * invalid arguments). */
-size_t npa_cross_attention_workspace_size(int B, int heads, int Lq, int Lk, int d);
+size_t npa_cross_attention_workspace_size(int B, int heads, int kv_heads, int Lq, int Lk, int d);
 
 /* Keys and values held in 8 bits: e4m3 codes (1-4-3, largest 448) with one
  * float32 scale for each block of 64 tokens of a head, value = code * scale.
@@ -324,17 +324,17 @@ typedef enum { NPA_ACT_NONE = 0, NPA_ACT_SILU = 1 } npa_activation;
  * and 0. groups divides C; C <= 4096. Statistics and arithmetic in float32.
  * y may be x itself (same strides) but must not otherwise overlap an input.
  * `workspace`: caller-owned device memory, 16-byte aligned, at least
- * npa_group_norm_workspace_size() bytes, not overlapping any other buffer
- * (NPA_ERR_INVALID_ARG when NULL or short); calls that overlap on the GPU need
- * workspaces of their own. Pointers need their element's alignment only;
+ * npa_group_norm_workspace_size() bytes (0 for small tensors: NULL will do),
+ * not overlapping any other buffer (NPA_ERR_INVALID_ARG when short); calls
+ * that overlap on the GPU need workspaces of their own. Pointers need their element's alignment only;
  * 16-byte aligned rows (C and the strides multiples of 16 bytes) run fastest. */
 npa_status npa_group_norm_act(const void *x, const void *weight, const void *bias, void *y, npa_dtype dtype,
                               npa_dtype weight_dtype, int B, int N, int C, int groups, int64_t x_batch_stride,
                               int64_t x_token_stride, int64_t y_batch_stride, int64_t y_token_stride, float eps,
                               npa_activation act, void *workspace, size_t workspace_bytes, npa_stream_t stream);
 
-/* Workspace bytes of npa_group_norm_act on the current device (0 for invalid
- * arguments). */
+/* Workspace bytes of npa_group_norm_act on the current device, whatever the
+ * alignment of x and y (0: none needed, or invalid arguments). */
 size_t npa_group_norm_workspace_size(npa_dtype dtype, int B, int N, int C, int groups);
 
 /* Workspace bytes npa_global_query_attention_fwd uses for its full split

@@ -38,8 +38,8 @@ and allocate outputs and workspaces; the computation is the same C call.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -160,7 +160,7 @@ def _load(path: str) -> ctypes.CDLL:
         st, kv8, f = ctypes.POINTER(_Strides), ctypes.POINTER(_Kv8Cache), ctypes.c_float
         L.npa_cross_attention_fwd.argtypes = [vp] * 4 + [i] * 7 + [st] * 4 + [vp, vp, f, vp, ctypes.c_size_t, vp]
         L.npa_cross_attention_fwd.restype = i
-        L.npa_cross_attention_workspace_size.argtypes = [i] * 5
+        L.npa_cross_attention_workspace_size.argtypes = [i] * 6
         L.npa_cross_attention_workspace_size.restype = ctypes.c_size_t
         L.npa_kv8_store.argtypes = [vp, vp, kv8] + [i] * 5 + [vp, i, st, st, vp]
         L.npa_kv8_store.restype = i
@@ -204,8 +204,8 @@ def _stream(stream) -> Optional[int]:
     if stream is None:
         try:
             import torch
-            if torch.cuda.is_available():
-                return int(torch.cuda.current_stream().cuda_stream)
+            if torch.cuda.is_initialized() or torch.cuda.is_available():
+                return _raw_stream_of()(torch.cuda.current_device())
         except ImportError:
             pass
         return None
@@ -296,9 +296,19 @@ def asg_guidance_combine(eps, eps_ref, mask, out, n_patches: int, B: int, C: int
            "asg_guidance_combine")
 
 
+@functools.lru_cache(maxsize=1024)
 def _strides(s):
-    """None (contiguous) or (batch, head, token) strides in elements."""
+    """None (contiguous) or a tuple of (batch, head, token) strides in elements."""
     return None if s is None else ctypes.byref(_Strides(*s))
+
+
+@functools.lru_cache(maxsize=None)
+def _raw_stream_of():
+    """A function from a device index to its current stream's handle (torch's
+    cheap query of it where this version has one)."""
+    import torch
+    return getattr(torch._C, "_cuda_getCurrentRawStream",
+                   lambda index: int(torch.cuda.current_stream(index).cuda_stream))
 
 
 def npa_cross_attention_fwd(q, k, v, o, dtype: int, B: int, heads: int, kv_heads: int, Lq: int, Lk: int, d: int,
@@ -314,8 +324,8 @@ def npa_cross_attention_fwd(q, k, v, o, dtype: int, B: int, heads: int, kv_heads
            "npa_cross_attention_fwd")
 
 
-def npa_cross_attention_workspace_size(B, heads, Lq, Lk, d) -> int:
-    return int(lib().npa_cross_attention_workspace_size(B, heads, Lq, Lk, d))
+def npa_cross_attention_workspace_size(B, heads, kv_heads, Lq, Lk, d) -> int:
+    return int(lib().npa_cross_attention_workspace_size(B, heads, kv_heads, Lq, Lk, d))
 
 
 def npa_kv8_store(k, v, cache_k, cache_v, k_scale, v_scale, capacity: int, dtype: int, B: int, kv_heads: int, d: int,
@@ -485,62 +495,66 @@ def asg_combine(eps, eps_ref, mask, w_t: float, out=None, stream=None):
 
 
 # ---------------------------------------------------------------------------
-# The steps around the self-attention
+# The steps around the self-attention. These calls are short (some run for a
+# few microseconds), so what does not change from call to call - stride
+# structures, dtype codes, workspace sizes - is looked up, not built again.
 # ---------------------------------------------------------------------------
 
-def _dtype_code(t, allowed) -> int:
+@functools.lru_cache(maxsize=None)
+def _dtype_codes():
     import torch
-    code = {torch.bfloat16: NPA_DTYPE_BF16, torch.float16: NPA_DTYPE_FP16, torch.float32: NPA_DTYPE_FP32}.get(t.dtype)
+    return {torch.bfloat16: NPA_DTYPE_BF16, torch.float16: NPA_DTYPE_FP16, torch.float32: NPA_DTYPE_FP32}
+
+
+def _dtype_code(t, allowed) -> int:
+    code = _dtype_codes().get(t.dtype)
     if code not in allowed:
         raise ValueError(f"unsupported dtype {t.dtype}")
     return code
 
 
-def _same_device(*tensors):
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+def _device_of(first, *others):
+    """The CUDA device that all the tensors (or None) are on."""
+    dev = first.device
     if dev.type != "cuda":
         raise ValueError(f"expected CUDA tensors, got {dev}")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
     return dev
 
 
-@contextlib.contextmanager
-def _launch_on(dev, stream):
-    """Makes ``dev`` and, when given, ``stream`` current, so that outputs and
-    workspaces come from the stream that the call runs on; yields its handle."""
+def _run_on(dev, stream, body):
+    """``body()`` with ``dev`` and, when given, ``stream`` current, so that
+    outputs and workspaces come from the stream that the call runs on."""
     import torch
-    with contextlib.ExitStack() as stack:
-        if dev.index != torch.cuda.current_device():
-            stack.enter_context(torch.cuda.device(dev))
-        if stream is not None:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=dev)
-            stack.enter_context(torch.cuda.stream(stream))
-        yield torch.cuda.current_stream().cuda_stream
+    if stream is None and dev.index == torch.cuda.current_device():
+        return body()
+    with torch.cuda.device(dev):
+        if stream is None:
+            return body()
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        with torch.cuda.stream(stream):
+            return body()
 
 
-def _heads_view(name, t, B=None, heads=None, L=None, d=None):
-    """Checks a [B, heads, L, d] tensor and returns its (batch, head, token) strides."""
-    if t.dim() != 4:
-        raise ValueError(f"{name}: expected [B, heads, L, d], got {tuple(t.shape)}")
-    for got, want in zip(t.shape, (B, heads, L, d)):
-        if want is not None and got != want:
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(B, heads, L, d)}")
+def _heads_strides(name, t, shape):
+    """Checks a [B, heads, L, d] tensor's shape and returns its (batch, head, token) strides."""
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected {tuple(shape)}, got {tuple(t.shape)}")
     s = t.stride()
-    if s[3] != 1 and t.shape[3] != 1:
+    if s[3] != 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
     return s[:3]
 
 
 def _kept_keys(kv_lens, key_mask, B, Lk):
     import torch
-    if kv_lens is not None and (kv_lens.dtype != torch.int32 or tuple(kv_lens.shape) != (B,) or
-                                not kv_lens.is_contiguous()):
+    if kv_lens is not None and (kv_lens.dtype != torch.int32 or kv_lens.shape != (B,) or not kv_lens.is_contiguous()):
         raise ValueError(f"kv_lens: expected a contiguous int32 tensor of {B} lengths")
-    if key_mask is not None and (key_mask.dtype not in (torch.bool, torch.uint8) or
-                                 tuple(key_mask.shape) != (B, Lk) or not key_mask.is_contiguous()):
+    if key_mask is not None and (key_mask.dtype not in (torch.bool, torch.uint8) or key_mask.shape != (B, Lk) or
+                                 not key_mask.is_contiguous()):
         raise ValueError(f"key_mask: expected a contiguous bool or uint8 tensor [{B}, {Lk}]")
 
 
@@ -552,10 +566,14 @@ def _scale(scale) -> float:
     return float(scale)
 
 
-def _split_workspace(split, B, heads, Lq, Lk, d, dev):
-    import torch
-    nbytes = npa_cross_attention_workspace_size(B, heads, Lq, Lk, d) if split else 0
-    return (torch.empty(nbytes, dtype=torch.uint8, device=dev), nbytes) if nbytes else (None, 0)
+@functools.lru_cache(maxsize=1024)
+def _xa_workspace_size(device_index, B, heads, kv_heads, Lq, Lk, d) -> int:
+    return npa_cross_attention_workspace_size(B, heads, kv_heads, Lq, Lk, d)   # of the current device: the key's first part
+
+
+@functools.lru_cache(maxsize=1024)
+def _gn_workspace_size(device_index, code, B, N, C, groups) -> int:
+    return npa_group_norm_workspace_size(code, B, N, C, groups)
 
 
 def cross_attention(q, k, v, kv_lens=None, key_mask=None, scale: Optional[float] = None, out=None, split: bool = True,
@@ -563,30 +581,35 @@ def cross_attention(q, k, v, kv_lens=None, key_mask=None, scale: Optional[float]
     """Cross attention on torch bf16 or fp16 CUDA tensors: q [B, heads, Lq, d],
     k and v [B, kv_heads, Lk, d], any strides that are multiples of 8 elements
     with the last axis contiguous (a projection's ``[B, L, heads, d]`` seen
-    through ``transpose(1, 2)``). Keys that ``kv_lens`` (int32 [B]) or
-    ``key_mask`` (bool or uint8 [B, Lk], true: attend) leave out are not read;
+    through ``transpose(1, 2)``). What ``kv_lens`` (int32 [B]) or ``key_mask``
+    (bool or uint8 [B, Lk], true: attend) leave out does not reach the output;
     a row without keys gives zeros. ``scale`` defaults to 1/sqrt(d). With
     ``split`` a workspace is allocated so that the key range of few queries can
     be split across the GPU. Returns ``out`` (by default laid out like q)."""
     import torch
-    qs = _heads_view("q", q)
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError(f"expected [B, heads, L, d], got {tuple(q.shape)} and {tuple(k.shape)}")
     B, heads, Lq, d = q.shape
-    ks = _heads_view("k", k, B, None, None, d)
     kv_heads, Lk = k.shape[1], k.shape[2]
-    vs = _heads_view("v", v, B, kv_heads, Lk, d)
+    qs = _heads_strides("q", q, q.shape)
+    ks = _heads_strides("k", k, (B, kv_heads, Lk, d))
+    vs = _heads_strides("v", v, k.shape)
     code = _dtype_code(q, (NPA_DTYPE_BF16, NPA_DTYPE_FP16))
-    _kept_keys(kv_lens, key_mask, B, Lk)
-    dev = _same_device(q, k, v, kv_lens, key_mask, out)
-    with _launch_on(dev, stream) as handle:
-        if out is None:
-            out = torch.empty_like(q)
-        if not q.dtype == k.dtype == v.dtype == out.dtype:
-            raise ValueError("q, k, v and out must have one dtype")
-        os_ = _heads_view("out", out, B, heads, Lq, d)
-        ws, nbytes = _split_workspace(split, B, heads, Lq, Lk, d, dev)
-        npa_cross_attention_fwd(q, k, v, out, code, B, heads, kv_heads, Lq, Lk, d, qs, ks, vs, os_, kv_lens, key_mask,
-                                _scale(scale), ws, nbytes, handle)
-    return out
+    if not q.dtype == k.dtype == v.dtype or (out is not None and out.dtype != q.dtype):
+        raise ValueError("q, k, v and out must have one dtype")
+    if kv_lens is not None or key_mask is not None:
+        _kept_keys(kv_lens, key_mask, B, Lk)
+    dev = _device_of(q, k, v, kv_lens, key_mask, out)
+
+    def call():
+        o = torch.empty_like(q) if out is None else out
+        nbytes = _xa_workspace_size(dev.index, B, heads, kv_heads, Lq, Lk, d) if split else 0
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        npa_cross_attention_fwd(q, k, v, o, code, B, heads, kv_heads, Lq, Lk, d, qs, ks, vs,
+                                _heads_strides("out", o, q.shape), kv_lens, key_mask, _scale(scale), ws, nbytes)
+        return o
+
+    return _run_on(dev, stream, call)
 
 
 class Kv8Cache:
@@ -604,14 +627,14 @@ class Kv8Cache:
                              f"got {tuple(k.shape)} and {tuple(v.shape)}")
         want = (k.shape[0], k.shape[1], k.shape[2] // KV8_BLOCK)
         for t in (k_scale, v_scale):
-            if tuple(t.shape) != want or t.dtype != torch.float32:
+            if t.shape != want or t.dtype != torch.float32:
                 raise ValueError(f"expected float32 scales {want}, got {t.dtype} {tuple(t.shape)}")
         for t in (k, v):
             if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
                 raise ValueError(f"expected e4m3 or uint8 codes, got {t.dtype}")
-        if not all(t.is_contiguous() for t in (k, v, k_scale, v_scale)):
+        if not (k.is_contiguous() and v.is_contiguous() and k_scale.is_contiguous() and v_scale.is_contiguous()):
             raise ValueError("a cache's tensors must be contiguous")
-        _same_device(k, v, k_scale, v_scale)
+        _device_of(k, v, k_scale, v_scale)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
 
     @classmethod
@@ -635,19 +658,19 @@ def kv8_store(cache: Kv8Cache, k, v, start: int = 0, starts=None, stream=None) -
     ``starts[b]`` (int32 [B]) in batch row b."""
     import torch
     B, kv_heads, capacity, d = cache.k.shape
-    ks = _heads_view("k", k, B, kv_heads, None, d)
+    if k.dim() != 4:
+        raise ValueError(f"expected [B, heads, L, d], got {tuple(k.shape)}")
     n = k.shape[2]
-    vs = _heads_view("v", v, B, kv_heads, n, d)
+    ks = _heads_strides("k", k, (B, kv_heads, n, d))
+    vs = _heads_strides("v", v, k.shape)
     code = _dtype_code(k, (NPA_DTYPE_BF16, NPA_DTYPE_FP16))
     if v.dtype != k.dtype:
         raise ValueError("k and v must have one dtype")
-    if starts is not None and (starts.dtype != torch.int32 or tuple(starts.shape) != (B,) or
-                               not starts.is_contiguous()):
+    if starts is not None and (starts.dtype != torch.int32 or starts.shape != (B,) or not starts.is_contiguous()):
         raise ValueError(f"starts: expected a contiguous int32 tensor of {B} positions")
-    dev = _same_device(cache.k, k, v, starts)
-    with _launch_on(dev, stream) as handle:
-        npa_kv8_store(k, v, cache.k, cache.v, cache.k_scale, cache.v_scale, capacity, code, B, kv_heads, d, start, n,
-                      starts, ks, vs, handle)
+    dev = _device_of(cache.k, k, v, starts)
+    _run_on(dev, stream, lambda: npa_kv8_store(k, v, cache.k, cache.v, cache.k_scale, cache.v_scale, capacity, code, B,
+                                               kv_heads, d, start, n, starts, ks, vs))
 
 
 def kv8_cross_attention(q, cache: Kv8Cache, n_tokens: Optional[int] = None, kv_lens=None, key_mask=None,
@@ -656,22 +679,28 @@ def kv8_cross_attention(q, cache: Kv8Cache, n_tokens: Optional[int] = None, kv_l
     ``n_tokens`` (default: all) tokens of an 8-bit cache."""
     import torch
     cB, kv_heads, capacity, cd = cache.k.shape
-    qs = _heads_view("q", q, cB, None, None, cd)
+    if q.dim() != 4:
+        raise ValueError(f"expected [B, heads, L, d], got {tuple(q.shape)}")
     B, heads, Lq, d = q.shape
+    qs = _heads_strides("q", q, (cB, heads, Lq, cd))
     Lk = capacity if n_tokens is None else int(n_tokens)
     _dtype_code(q, (NPA_DTYPE_BF16,))
-    _kept_keys(kv_lens, key_mask, B, Lk)
-    dev = _same_device(q, cache.k, kv_lens, key_mask, out)
-    with _launch_on(dev, stream) as handle:
-        if out is None:
-            out = torch.empty_like(q)
-        if out.dtype != q.dtype:
-            raise ValueError("q and out must have one dtype")
-        os_ = _heads_view("out", out, B, heads, Lq, d)
-        ws, nbytes = _split_workspace(split, B, heads, Lq, Lk, d, dev)
-        npa_kv8_cross_attention_fwd(q, cache.k, cache.v, cache.k_scale, cache.v_scale, capacity, out, B, heads,
-                                    kv_heads, Lq, Lk, d, qs, os_, kv_lens, key_mask, _scale(scale), ws, nbytes, handle)
-    return out
+    if out is not None and out.dtype != q.dtype:
+        raise ValueError("q and out must have one dtype")
+    if kv_lens is not None or key_mask is not None:
+        _kept_keys(kv_lens, key_mask, B, Lk)
+    dev = _device_of(q, cache.k, kv_lens, key_mask, out)
+
+    def call():
+        o = torch.empty_like(q) if out is None else out
+        nbytes = _xa_workspace_size(dev.index, B, heads, kv_heads, Lq, Lk, d) if split else 0
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        npa_kv8_cross_attention_fwd(q, cache.k, cache.v, cache.k_scale, cache.v_scale, capacity, o, B, heads,
+                                    kv_heads, Lq, Lk, d, qs, _heads_strides("out", o, q.shape), kv_lens, key_mask,
+                                    _scale(scale), ws, nbytes)
+        return o
+
+    return _run_on(dev, stream, call)
 
 
 _ACTIVATIONS = {None: NPA_ACT_NONE, "none": NPA_ACT_NONE, "silu": NPA_ACT_SILU}
@@ -695,22 +724,24 @@ def group_norm(x, groups: int, weight=None, bias=None, eps: float = 1e-5, act: O
     for name, t in (("weight", weight), ("bias", bias)):
         if t is None:
             continue
-        if tuple(t.shape) != (C,) or t.dtype not in (x.dtype, torch.float32) or not t.is_contiguous():
-            raise ValueError(f"{name}: expected a contiguous [{C}] tensor of {x.dtype} or float32")
+        if t.shape != (C,) or not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous [{C}] tensor")
         wcode = _dtype_code(t, (code, NPA_DTYPE_FP32))
     if weight is not None and bias is not None and weight.dtype != bias.dtype:
         raise ValueError("weight and bias must have one dtype")
-    dev = _same_device(x, weight, bias, out)
-    with _launch_on(dev, stream) as handle:
-        if out is None:
-            out = torch.empty((B, N, C), dtype=x.dtype, device=dev)
-        if out.dtype != x.dtype or out.shape != x.shape:
-            raise ValueError("out must have x's shape and dtype")
-        for name, t in (("x", x), ("out", out)):
-            if C > 1 and t.stride(2) != 1:
-                raise ValueError(f"{name}: channels must be contiguous")
-        nbytes = npa_group_norm_workspace_size(code, B, N, C, groups)
-        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
-        npa_group_norm_act(x, weight, bias, out, code, wcode, B, N, C, groups, x.stride(0), x.stride(1),
-                           out.stride(0), out.stride(1), float(eps), _ACTIVATIONS[act], ws, nbytes, handle)
-    return out
+    if out is not None and (out.dtype != x.dtype or out.shape != x.shape):
+        raise ValueError("out must have x's shape and dtype")
+    dev = _device_of(x, weight, bias, out)
+
+    def call():
+        y = torch.empty((B, N, C), dtype=x.dtype, device=dev) if out is None else out
+        xs, ys = x.stride(), y.stride()
+        if C > 1 and (xs[2] != 1 or ys[2] != 1):
+            raise ValueError("channels must be contiguous")
+        nbytes = _gn_workspace_size(dev.index, code, B, N, C, groups)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        npa_group_norm_act(x, weight, bias, y, code, wcode, B, N, C, groups, xs[0], xs[1], ys[0], ys[1], float(eps),
+                           _ACTIVATIONS[act], ws, nbytes)
+        return y
+
+    return _run_on(dev, stream, call)

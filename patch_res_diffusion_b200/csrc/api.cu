@@ -48,6 +48,8 @@ struct DeviceState {
     int l2_bytes = 0;
     bool xa_checked = false;  // the cross-attention kernels (on their first use)
     npa_status xa_status = NPA_ERR_UNSUPPORTED;
+    bool gn_checked = false;  // the group norm's cluster kernels
+    npa_status gn_status = NPA_ERR_UNSUPPORTED;
 };
 DeviceState g_dev[kMaxDevices];
 
@@ -842,37 +844,101 @@ npa_status validate_kv8(const npa_kv8_cache *cache, int B, int kv_heads, int d) 
 // Group norm
 // ---------------------------------------------------------------------------
 struct GnPlan {
-    int vec, cols, rows, threads;
-    int stat_tiles, stat_rows, apply_tiles, apply_rows;
-    size_t stat_smem, apply_smem, bytes;
+    int vec, cols, rows, threads, segs;
+    int cw;               // channels of a chunk
+    int cluster;          // > 0: gn_cluster_kernel with this many blocks
+    int tiles, tile_rows;
+    int item_rows;        // gn_step_kernel: batch rows of an item
+    size_t smem, bytes;   // dynamic shared memory; workspace
 };
 
-// Tiles per batch row: enough blocks for `per_sm` on every multiprocessor, of
-// at least one batch of tokens per thread.
-void gn_tiles(int B, int N, int rows, int per_sm, int batch, int sm_count, int *tiles, int *tile_rows) {
-    long long t = ((long long)per_sm * sm_count + B - 1) / B;
-    const long long most = ((long long)N + (long long)rows * batch - 1) / ((long long)rows * batch);
-    if (t > most) t = most;
-    if (t < 1) t = 1;
-    long long r = (N + t - 1) / t;
-    r = (r + rows - 1) / rows * rows;
-    *tile_rows = (int)r;
-    *tiles = (int)((N + r - 1) / r);
+// Bytes of an item that is read twice: it, the one before it (being
+// normalised) and that one's results have to stay in the 126 MB L2 together.
+constexpr double kGnItemBytes = 40e6;
+// Shared memory of a cluster block's share of its chunk at most.
+constexpr size_t kGnSlabBytes = 200 * 1024;
+
+void gn_shape(GnPlan *pl, int max_threads) {
+    const int ncol = pl->cw / pl->vec;
+    pl->cols = ncol < npa::kGnThreads ? ncol : npa::kGnThreads;
+    pl->rows = pl->cols < max_threads ? max_threads / pl->cols : 1;
 }
 
-GnPlan plan_gn(int B, int N, int C, int groups, int vec, int sm_count) {
+void gn_threads(GnPlan *pl) { pl->threads = (pl->cols * pl->rows + 31) / 32 * 32; }
+
+// Tokens cut into `tiles` tiles of whole block rows.
+void gn_tiles(GnPlan *pl, int N, long long tiles) {
+    long long r = (N + tiles - 1) / tiles;
+    if (r < pl->rows) r = pl->rows;
+    pl->tile_rows = (int)((r + pl->rows - 1) / pl->rows * pl->rows);
+    pl->tiles = (int)(((long long)N + pl->tile_rows - 1) / pl->tile_rows);
+}
+
+int lcm(int a, int b) {
+    int x = a, y = b;
+    while (y) {
+        const int t = x % y;
+        x = y;
+        y = t;
+    }
+    return a / x * b;
+}
+
+GnPlan plan_gn(int B, int N, int C, int groups, int vec, int elem, int sm_count) {
     GnPlan pl;
+    std::memset(&pl, 0, sizeof(pl));
+    const int cpg = C / groups;
     pl.vec = vec;
-    const int ncol = C / vec;
-    pl.cols = ncol < npa::kGnThreads ? ncol : npa::kGnThreads;
-    pl.rows = pl.cols < 256 ? 256 / pl.cols : 1;
-    if (pl.rows > N) pl.rows = N;
-    pl.threads = (pl.cols * pl.rows + 31) / 32 * 32;
-    gn_tiles(B, N, pl.rows, 4, npa::kGnBatch, sm_count, &pl.stat_tiles, &pl.stat_rows);
-    gn_tiles(B, N, pl.rows, 8, 4, sm_count, &pl.apply_tiles, &pl.apply_rows);
-    pl.stat_smem = ((size_t)2 * pl.rows * C + pl.rows) * sizeof(float);
-    pl.apply_smem = (size_t)2 * groups * sizeof(float);
-    pl.bytes = (size_t)B * groups * pl.stat_tiles * sizeof(float2);
+    pl.segs = std::min(vec, (vec - 1) / cpg + 2);
+    if (vec == 1) pl.segs = 1;
+    // the narrowest chunk of whole groups and whole 32-byte sectors that
+    // divides the channels, widened to 128 bytes where that divides them too
+    int chunk = C;
+    if (vec > 1) {
+        const int unit = lcm(cpg, 32 / elem);
+        for (int m = 1; (long long)unit * m <= C; ++m)
+            if (C % (unit * m) == 0) {
+                chunk = unit * m;
+                if (chunk * elem >= 128) break;
+            }
+    }
+    // cluster form: the least number of blocks whose shared memory holds a
+    // chunk, or more while the GPU is not full
+    if (vec > 1 && chunk / vec <= npa::kGnThreads && C / chunk <= 65535) {
+        pl.cw = chunk;
+        gn_shape(&pl, 256);
+        for (int s = 1; s <= npa::kGnMaxCluster; s *= 2) {
+            gn_tiles(&pl, N, s);
+            const size_t ng = chunk / cpg;
+            const size_t slab = (size_t)(pl.tile_rows / pl.rows) * pl.cols * pl.rows * 16;
+            const size_t smem = slab + (size_t)pl.rows * (chunk / vec) * pl.segs * 8 + (size_t)s * ng * 8 + ng * 8;
+            const bool enough = (long long)B * (C / chunk) * s >= sm_count || s == npa::kGnMaxCluster ||
+                                N <= 2LL * s * pl.rows;
+            if (smem > kGnSlabBytes || !enough) continue;
+            pl.cluster = s;
+            pl.tiles = s;  // trailing blocks may have no tokens
+            pl.smem = smem;
+            gn_threads(&pl);
+            return pl;
+        }
+    }
+    // items through L2: batch rows together while they fit, else the channel
+    // chunks of one (as many groups as fit)
+    const double row_bytes = (double)N * C * elem;
+    pl.cw = C;
+    pl.item_rows = (int)std::min<double>(B, std::max(1.0, std::floor(kGnItemBytes / row_bytes)));
+    if (row_bytes > kGnItemBytes && vec > 1 && chunk < C) {
+        pl.cw = chunk;
+        for (int w = chunk; w <= C; w += chunk)
+            if (C % w == 0 && (double)N * w * elem <= kGnItemBytes) pl.cw = w;
+    }
+    gn_shape(&pl, npa::kGnThreads);
+    gn_threads(&pl);
+    const long long want = std::min<long long>(npa::kGnMaxTiles, (2LL * sm_count + pl.item_rows - 1) / pl.item_rows);
+    const long long most = ((long long)N + 4LL * pl.rows - 1) / (4LL * pl.rows);
+    gn_tiles(&pl, N, std::max(1LL, std::min(want, most)));
+    pl.smem = std::max((size_t)pl.rows * ((pl.cw + vec - 1) / vec) * pl.segs * 8, (size_t)(pl.cw / cpg) * 8);
+    pl.bytes = (size_t)B * groups * pl.tiles * sizeof(float2);
     return pl;
 }
 
@@ -887,34 +953,74 @@ bool gn_vectors(int C, npa_dtype dtype, const void *x, const void *y, const int6
     return C % unit == 0 && aligned16(x) && aligned16(y);
 }
 
+template <typename T>
+bool prepare_gn_kernel() {
+    return cudaFuncSetAttribute(npa::gn_cluster_kernel<T, 16 / sizeof(T)>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)kGnSlabBytes) == cudaSuccess;
+}
+
+// ensure_ready plus the cluster kernels' shared memory, once per device.
+npa_status ensure_gn_ready(int *sm_count) {
+    const npa_status st = ensure_ready(sm_count);
+    if (st != NPA_OK) return st;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return NPA_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceState &ds = g_dev[dev];
+    if (!ds.gn_checked) {
+        const bool ok = prepare_gn_kernel<__nv_bfloat16>() && prepare_gn_kernel<__half>() && prepare_gn_kernel<float>();
+        ds.gn_status = ok ? NPA_OK : NPA_ERR_CUDA;
+        ds.gn_checked = true;
+    }
+    return ds.gn_status;
+}
+
 template <typename T, int kVec>
-npa_status launch_gn(const npa::GnParams &prm, const GnPlan &pl, int B, npa_stream_t stream) {
+npa_status launch_gn(const npa::GnParams &prm, const GnPlan &pl, int B, int C, npa_stream_t stream) {
     npa::GnParams p = prm;
     void *args[1] = {&p};
-    const void *stats = (const void *)npa::gn_stats_kernel<T, kVec>;
-    const void *apply = (const void *)npa::gn_apply_kernel<T, kVec>;
-    if (cudaLaunchKernel(stats, dim3(pl.stat_tiles, B), dim3(pl.threads), args, pl.stat_smem, (cudaStream_t)stream) !=
-        cudaSuccess)
-        return NPA_ERR_CUDA;
-    // the normalisation may start while the statistics finish; it waits for
-    // them on the device
     cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3(pl.apply_tiles, B);
     cfg.blockDim = dim3(pl.threads);
-    cfg.dynamicSmemBytes = pl.apply_smem;
+    cfg.dynamicSmemBytes = pl.smem;
     cfg.stream = (cudaStream_t)stream;
     cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelExC(&cfg, apply, args) == cudaSuccess ? NPA_OK : NPA_ERR_CUDA;
+    if (pl.cluster) {
+        if constexpr (kVec > 1) {
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = pl.cluster;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.numAttrs = 1;
+            cfg.gridDim = dim3(pl.cluster, C / pl.cw, B);
+            return cudaLaunchKernelExC(&cfg, (const void *)npa::gn_cluster_kernel<T, kVec>, args) == cudaSuccess
+                       ? NPA_OK
+                       : NPA_ERR_CUDA;
+        }
+        return NPA_ERR_CUDA;  // not planned
+    }
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    const int chunks = C / pl.cw, groups_of_rows = (B + pl.item_rows - 1) / pl.item_rows;
+    const long long items = (long long)chunks * groups_of_rows;
+    for (long long s = 0; s <= items; ++s) {
+        p.apply_b = p.stat_b;
+        p.apply_nb = p.stat_nb;
+        p.apply_c = p.stat_c;
+        p.stat_b = (int)(s / chunks) * pl.item_rows;
+        p.stat_nb = s < items ? std::min(pl.item_rows, B - p.stat_b) : 0;
+        p.stat_c = (int)(s % chunks) * pl.cw;
+        cfg.gridDim = dim3(pl.tiles, std::max(p.stat_nb, p.apply_nb));
+        cfg.numAttrs = s > 0 ? 1 : 0;  // the first launch follows other work
+        if (cudaLaunchKernelExC(&cfg, (const void *)npa::gn_step_kernel<T, kVec>, args) != cudaSuccess)
+            return NPA_ERR_CUDA;
+    }
+    return NPA_OK;
 }
 
 template <typename T>
-npa_status launch_gn_vec(const npa::GnParams &prm, const GnPlan &pl, int B, npa_stream_t stream) {
-    return pl.vec == 1 ? launch_gn<T, 1>(prm, pl, B, stream) : launch_gn<T, 16 / sizeof(T)>(prm, pl, B, stream);
+npa_status launch_gn_vec(const npa::GnParams &prm, const GnPlan &pl, int B, int C, npa_stream_t stream) {
+    return pl.vec == 1 ? launch_gn<T, 1>(prm, pl, B, C, stream) : launch_gn<T, 16 / sizeof(T)>(prm, pl, B, C, stream);
 }
 
 }  // namespace
@@ -1108,8 +1214,8 @@ npa_status asg_guidance_combine(const void *eps, const void *eps_ref, const void
     return e == cudaSuccess ? NPA_OK : NPA_ERR_CUDA;
 }
 
-size_t npa_cross_attention_workspace_size(int B, int heads, int Lq, int Lk, int d) {
-    if (validate_xa_sizes(B, heads, heads, Lq, Lk, d, 0.f, nullptr) != NPA_OK) return 0;
+size_t npa_cross_attention_workspace_size(int B, int heads, int kv_heads, int Lq, int Lk, int d) {
+    if (validate_xa_sizes(B, heads, kv_heads, Lq, Lk, d, 0.f, nullptr) != NPA_OK) return 0;
     int dev = 0, sm = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return 0;
@@ -1241,8 +1347,8 @@ size_t npa_group_norm_workspace_size(npa_dtype dtype, int B, int N, int C, int g
         return 0;
     // whichever of the vector and the single-element form needs more
     const int unit = 16 / gn_elem(dtype);
-    size_t n = plan_gn(B, N, C, groups, 1, sm).bytes;
-    if (C % unit == 0) n = std::max(n, plan_gn(B, N, C, groups, unit, sm).bytes);
+    size_t n = plan_gn(B, N, C, groups, 1, gn_elem(dtype), sm).bytes;
+    if (C % unit == 0) n = std::max(n, plan_gn(B, N, C, groups, unit, gn_elem(dtype), sm).bytes);
     return n;
 }
 
@@ -1250,7 +1356,7 @@ npa_status npa_group_norm_act(const void *x, const void *weight, const void *bia
                               npa_dtype weight_dtype, int B, int N, int C, int groups, int64_t x_batch_stride,
                               int64_t x_token_stride, int64_t y_batch_stride, int64_t y_token_stride, float eps,
                               npa_activation act, void *workspace, size_t workspace_bytes, npa_stream_t stream) {
-    if (!x || !y || !workspace) return NPA_ERR_INVALID_ARG;
+    if (!x || !y) return NPA_ERR_INVALID_ARG;
     if (B < 1 || N < 1 || C < 1 || groups < 1 || C % groups != 0 || !std::isfinite(eps) || eps < 0.f)
         return NPA_ERR_INVALID_ARG;
     if (act != NPA_ACT_NONE && act != NPA_ACT_SILU) return NPA_ERR_INVALID_ARG;
@@ -1280,10 +1386,11 @@ npa_status npa_group_norm_act(const void *x, const void *weight, const void *bia
     const size_t wb = (size_t)C * welem;
     if ((weight && overlaps(y, yb, weight, wb)) || (bias && overlaps(y, yb, bias, wb))) return NPA_ERR_INVALID_ARG;
     int sm_count = 0;
-    const npa_status st = ensure_ready(&sm_count);
+    const npa_status st = ensure_gn_ready(&sm_count);
     if (st != NPA_OK) return st;
-    const GnPlan pl = plan_gn(B, N, C, groups, gn_vectors(C, dtype, x, y, s) ? 16 / elem : 1, sm_count);
+    const GnPlan pl = plan_gn(B, N, C, groups, gn_vectors(C, dtype, x, y, s) ? 16 / elem : 1, elem, sm_count);
     if (workspace_bytes < pl.bytes) return NPA_ERR_INVALID_ARG;
+    if (pl.bytes && !workspace) return NPA_ERR_INVALID_ARG;
     if (overlaps(workspace, pl.bytes, x, xb) || overlaps(workspace, pl.bytes, y, yb) ||
         (weight && overlaps(workspace, pl.bytes, weight, wb)) || (bias && overlaps(workspace, pl.bytes, bias, wb)))
         return NPA_ERR_INVALID_ARG;
@@ -1301,19 +1408,18 @@ npa_status npa_group_norm_act(const void *x, const void *weight, const void *bia
     prm.N = N;
     prm.G = groups;
     prm.cpg = C / groups;
-    prm.cw = C;
+    prm.cw = pl.cw;
     prm.cols = pl.cols;
     prm.rows = pl.rows;
-    prm.stat_tiles = pl.stat_tiles;
-    prm.stat_rows = pl.stat_rows;
-    prm.apply_tiles = pl.apply_tiles;
-    prm.apply_rows = pl.apply_rows;
+    prm.segs = pl.segs;
+    prm.tiles = pl.tiles;
+    prm.tile_rows = pl.tile_rows;
     prm.eps = eps;
     prm.silu = act == NPA_ACT_SILU;
     prm.part = static_cast<float2 *>(workspace);
-    if (dtype == NPA_DTYPE_BF16) return launch_gn_vec<__nv_bfloat16>(prm, pl, B, stream);
-    if (dtype == NPA_DTYPE_FP16) return launch_gn_vec<__half>(prm, pl, B, stream);
-    return launch_gn_vec<float>(prm, pl, B, stream);
+    if (dtype == NPA_DTYPE_BF16) return launch_gn_vec<__nv_bfloat16>(prm, pl, B, C, stream);
+    if (dtype == NPA_DTYPE_FP16) return launch_gn_vec<__half>(prm, pl, B, C, stream);
+    return launch_gn_vec<float>(prm, pl, B, C, stream);
 }
 
 int pcpp_neighbor_rows(int strip_rows, double p) { return neighbor_rows(strip_rows, p); }

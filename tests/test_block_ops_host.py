@@ -79,7 +79,8 @@ def test_cross_attention_overlaps(L):
 
 def test_workspace_size_of_bad_arguments(L):
     f = L.npa_cross_attention_workspace_size
-    assert f(0, 4, 1, 77, 64) == 0 and f(1, 4, 1, 77, 96) == 0 and f(1, 4, -1, 77, 64) == 0
+    assert f(0, 4, 4, 1, 77, 64) == 0 and f(1, 4, 4, 1, 77, 96) == 0 and f(1, 4, 4, -1, 77, 64) == 0
+    assert f(1, 4, 3, 1, 77, 64) == 0
 
 
 def kv8c(k=K, v=V, ks=0xB0000000, vs=0xC0000000, cap=128):
@@ -120,7 +121,7 @@ def norm(L, x=Q, w=V, b=MASK, y=O, dtype=0, wdtype=0, B=2, N=10, C=64, G=8, xs=(
 
 
 def test_group_norm_refusals(L):
-    assert norm(L, x=None) == BAD and norm(L, y=None) == BAD and norm(L, ws=None) == BAD
+    assert norm(L, x=None) == BAD and norm(L, y=None) == BAD
     for name in ("B", "N", "C", "G"):
         assert norm(L, **{name: 0}) == BAD
     assert norm(L, G=7) == BAD and norm(L, eps=-1.0) == BAD and norm(L, eps=float("nan")) == BAD

@@ -208,7 +208,7 @@ def test_workspace_sizes(npa):
     B, h, Lq, Lk, d = 1, 3, 20, 6000, 64
     q, k, v = qkv(91, B, h, h, Lq, Lk, d)
     ref, mag = oracle.cross_attention(f64(q), f64(k), f64(v))
-    full = npa.npa_cross_attention_workspace_size(B, h, Lq, Lk, d)
+    full = npa.npa_cross_attention_workspace_size(B, h, h, Lq, Lk, d)
     assert full > 0
     one = B * h * Lq * (d + 2) * 4
     for nbytes in (0, one, 2 * one, 3 * one + 4, full):

@@ -100,6 +100,43 @@ def test_large(npa):
     run_and_check(npa, x, 32, randn(25, 320), randn(26, 320), act="silu")
 
 
+@pytest.mark.parametrize("B,N,C,groups,dtype", [(1, 40000, 128, 32, "bf16"), (3, 20000, 64, 4, "fp16"),
+                                                (5, 50000, 128, 32, "bf16"), (2, 300000, 48, 3, "bf16"),
+                                                (1, 45000, 320, 32, "fp32"), (2, 4096, 640, 32, "bf16"),
+                                                (1, 16384, 320, 32, "bf16"), (9, 1500, 72, 9, "fp32")])
+def test_plans(npa, B, N, C, groups, dtype):
+    """Sizes on both sides of what a cluster holds: one item, several batch
+    rows to an item (a shorter last one), channel chunks, blocks of a cluster
+    without tokens."""
+    x = randn(70, B, N, C, dtype=dtype) + randn(71, C, dtype=dtype)
+    y = x.clone()
+    a = run_and_check(npa, x, groups, randn(72, C, dtype=dtype), randn(73, C, dtype=dtype), act="silu", dtype=dtype)
+    npa.group_norm(y, groups, randn(72, C, dtype=dtype), randn(73, C, dtype=dtype), act="silu", out=y)
+    assert torch.equal(bits(a), bits(y))
+
+
+def test_workspace(npa):
+    """A short workspace is refused; what lies past it stays; none is needed for small tensors."""
+    assert npa.npa_group_norm_workspace_size(npa.NPA_DTYPE_BF16, 2, 1024, 1280, 32) > 0   # rows may be misaligned
+    x = randn(74, 1, 1024, 1280)
+    y, z = torch.empty_like(x), torch.empty_like(x)
+    args = (npa.NPA_DTYPE_BF16, npa.NPA_DTYPE_BF16, 1, 1024, 1280, 32, 1024 * 1280, 1280, 1024 * 1280, 1280, 1e-5, 0)
+    npa.npa_group_norm_act(x, None, None, y, *args, None, 0)
+    x = randn(75, 1, 40000, 320)
+    y = torch.empty_like(x)
+    args = (npa.NPA_DTYPE_BF16, npa.NPA_DTYPE_BF16, 1, 40000, 320, 32, 40000 * 320, 320, 40000 * 320, 320, 1e-5, 0)
+    n = npa.npa_group_norm_workspace_size(npa.NPA_DTYPE_BF16, 1, 40000, 320, 32)
+    ws = torch.full((n // 4 + 16,), 7.0, device="cuda")
+    with pytest.raises(npa.NpaError):
+        npa.npa_group_norm_act(x, None, None, y, *args, ws, n // 2)
+    with pytest.raises(npa.NpaError):
+        npa.npa_group_norm_act(x, None, None, y, *args, None, 0)
+    npa.npa_group_norm_act(x, None, None, y, *args, ws, n)
+    torch.cuda.synchronize()
+    assert (ws[n // 4:] == 7.0).all()
+    assert torch.equal(bits(y), bits(npa.group_norm(x, 32)))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_strides_in_place_and_guards(npa, dtype):
     """A slice of a concatenated tensor in, a slice of another out, rest
