@@ -48,7 +48,7 @@ struct DeviceState {
     int l2_bytes = 0;
     bool xa_checked = false;  // the cross-attention kernels (on their first use)
     npa_status xa_status = NPA_ERR_UNSUPPORTED;
-    bool gn_checked = false;  // the group norm's cluster kernels
+    bool gn_checked = false;  // the group norm's kernels
     npa_status gn_status = NPA_ERR_UNSUPPORTED;
 };
 DeviceState g_dev[kMaxDevices];
@@ -844,27 +844,25 @@ npa_status validate_kv8(const npa_kv8_cache *cache, int B, int kv_heads, int d) 
 // Group norm
 // ---------------------------------------------------------------------------
 struct GnPlan {
-    int vec, cols, rows, threads, segs;
+    int vec, cols, rows, threads;
     int cw;               // channels of a chunk
-    int cluster;          // > 0: gn_cluster_kernel with this many blocks
+    int cluster;          // > 0: gn_cluster_kernel with this many blocks (0: three launches)
     int tiles, tile_rows;
-    int item_rows;        // gn_step_kernel: batch rows of an item
+    int apply_tiles, apply_rows;
     size_t smem, bytes;   // dynamic shared memory; workspace
 };
 
-// Bytes of an item that is read twice: it, the one before it (being
-// normalised) and that one's results have to stay in the 126 MB L2 together.
-constexpr double kGnItemBytes = 40e6;
+// Batches of tokens of a normalising thread.
+constexpr int kGnApplyBatches = 6;
 // Shared memory of a cluster block's share of its chunk at most.
 constexpr size_t kGnSlabBytes = 200 * 1024;
 
-void gn_shape(GnPlan *pl, int max_threads) {
+void gn_shape(GnPlan *pl) {
     const int ncol = pl->cw / pl->vec;
     pl->cols = ncol < npa::kGnThreads ? ncol : npa::kGnThreads;
-    pl->rows = pl->cols < max_threads ? max_threads / pl->cols : 1;
+    pl->rows = npa::kGnThreads / pl->cols;
+    pl->threads = (pl->cols * pl->rows + 31) / 32 * 32;
 }
-
-void gn_threads(GnPlan *pl) { pl->threads = (pl->cols * pl->rows + 31) / 32 * 32; }
 
 // Tokens cut into `tiles` tiles of whole block rows.
 void gn_tiles(GnPlan *pl, int N, long long tiles) {
@@ -889,8 +887,6 @@ GnPlan plan_gn(int B, int N, int C, int groups, int vec, int elem, int sm_count)
     std::memset(&pl, 0, sizeof(pl));
     const int cpg = C / groups;
     pl.vec = vec;
-    pl.segs = std::min(vec, (vec - 1) / cpg + 2);
-    if (vec == 1) pl.segs = 1;
     // the narrowest chunk of whole groups and whole 32-byte sectors that
     // divides the channels, widened to 128 bytes where that divides them too
     int chunk = C;
@@ -906,39 +902,33 @@ GnPlan plan_gn(int B, int N, int C, int groups, int vec, int elem, int sm_count)
     // chunk, or more while the GPU is not full
     if (vec > 1 && chunk / vec <= npa::kGnThreads && C / chunk <= 65535) {
         pl.cw = chunk;
-        gn_shape(&pl, 256);
+        gn_shape(&pl);
         for (int s = 1; s <= npa::kGnMaxCluster; s *= 2) {
             gn_tiles(&pl, N, s);
             const size_t ng = chunk / cpg;
             const size_t slab = (size_t)(pl.tile_rows / pl.rows) * pl.cols * pl.rows * 16;
-            const size_t smem = slab + (size_t)pl.rows * (chunk / vec) * pl.segs * 8 + (size_t)s * ng * 8 + ng * 8;
+            const size_t smem = slab + (size_t)pl.rows * (chunk + 1) * 8 + (size_t)s * ng * 8 + ng * 8;
             const bool enough = (long long)B * (C / chunk) * s >= sm_count || s == npa::kGnMaxCluster ||
-                                N <= 2LL * s * pl.rows;
+                                N <= 8LL * s * pl.rows;
             if (smem > kGnSlabBytes || !enough) continue;
             pl.cluster = s;
             pl.tiles = s;  // trailing blocks may have no tokens
             pl.smem = smem;
-            gn_threads(&pl);
             return pl;
         }
     }
-    // items through L2: batch rows together while they fit, else the channel
-    // chunks of one (as many groups as fit)
-    const double row_bytes = (double)N * C * elem;
+    // three launches. Statistics: about three blocks for every multiprocessor,
+    // of a batch of tokens for each thread at least; normalisation: short
+    // blocks, many more than fit at once
     pl.cw = C;
-    pl.item_rows = (int)std::min<double>(B, std::max(1.0, std::floor(kGnItemBytes / row_bytes)));
-    if (row_bytes > kGnItemBytes && vec > 1 && chunk < C) {
-        pl.cw = chunk;
-        for (int w = chunk; w <= C; w += chunk)
-            if (C % w == 0 && (double)N * w * elem <= kGnItemBytes) pl.cw = w;
-    }
-    gn_shape(&pl, npa::kGnThreads);
-    gn_threads(&pl);
-    const long long want = std::min<long long>(npa::kGnMaxTiles, (2LL * sm_count + pl.item_rows - 1) / pl.item_rows);
-    const long long most = ((long long)N + 4LL * pl.rows - 1) / (4LL * pl.rows);
-    gn_tiles(&pl, N, std::max(1LL, std::min(want, most)));
-    pl.smem = std::max((size_t)pl.rows * ((pl.cw + vec - 1) / vec) * pl.segs * 8, (size_t)(pl.cw / cpg) * 8);
-    pl.bytes = (size_t)B * groups * pl.tiles * sizeof(float2);
+    gn_shape(&pl);
+    const long long batch = (long long)npa::kGnBatch * pl.rows;
+    const long long want = std::min<long long>(npa::kGnMaxTiles, (3LL * sm_count + B - 1) / B);
+    gn_tiles(&pl, N, std::max(1LL, std::min(want, (N + batch - 1) / batch)));
+    pl.apply_rows = (int)std::min<long long>(kGnApplyBatches * batch, INT_MAX / 2);
+    pl.apply_tiles = (int)(((long long)N + pl.apply_rows - 1) / pl.apply_rows);
+    pl.smem = (size_t)pl.rows * (C + 1) * 8;
+    pl.bytes = (size_t)B * groups * (pl.tiles + 1) * sizeof(float2);
     return pl;
 }
 
@@ -955,11 +945,12 @@ bool gn_vectors(int C, npa_dtype dtype, const void *x, const void *y, const int6
 
 template <typename T>
 bool prepare_gn_kernel() {
-    return cudaFuncSetAttribute(npa::gn_cluster_kernel<T, 16 / sizeof(T)>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    constexpr int kVec = 16 / sizeof(T);
+    return cudaFuncSetAttribute(npa::gn_cluster_kernel<T, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)kGnSlabBytes) == cudaSuccess;
 }
 
-// ensure_ready plus the cluster kernels' shared memory, once per device.
+// ensure_ready plus the group norm kernels' shared memory, once per device.
 npa_status ensure_gn_ready(int *sm_count) {
     const npa_status st = ensure_ready(sm_count);
     if (st != NPA_OK) return st;
@@ -999,23 +990,21 @@ npa_status launch_gn(const npa::GnParams &prm, const GnPlan &pl, int B, int C, n
         }
         return NPA_ERR_CUDA;  // not planned
     }
+    cfg.gridDim = dim3(pl.tiles, B);
+    if (cudaLaunchKernelExC(&cfg, (const void *)npa::gn_stats_kernel<T, kVec>, args) != cudaSuccess) return NPA_ERR_CUDA;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
-    const int chunks = C / pl.cw, groups_of_rows = (B + pl.item_rows - 1) / pl.item_rows;
-    const long long items = (long long)chunks * groups_of_rows;
-    for (long long s = 0; s <= items; ++s) {
-        p.apply_b = p.stat_b;
-        p.apply_nb = p.stat_nb;
-        p.apply_c = p.stat_c;
-        p.stat_b = (int)(s / chunks) * pl.item_rows;
-        p.stat_nb = s < items ? std::min(pl.item_rows, B - p.stat_b) : 0;
-        p.stat_c = (int)(s % chunks) * pl.cw;
-        cfg.gridDim = dim3(pl.tiles, std::max(p.stat_nb, p.apply_nb));
-        cfg.numAttrs = s > 0 ? 1 : 0;  // the first launch follows other work
-        if (cudaLaunchKernelExC(&cfg, (const void *)npa::gn_step_kernel<T, kVec>, args) != cudaSuccess)
-            return NPA_ERR_CUDA;
-    }
-    return NPA_OK;
+    cfg.numAttrs = 1;
+    cfg.dynamicSmemBytes = 0;
+    int n = B * p.G;
+    void *merge_args[2] = {&p, &n};
+    cfg.gridDim = dim3((n + 3) / 4);
+    cfg.blockDim = dim3(128);
+    if (cudaLaunchKernelExC(&cfg, (const void *)npa::gn_merge_kernel, merge_args) != cudaSuccess) return NPA_ERR_CUDA;
+    cfg.gridDim = dim3(pl.apply_tiles, B);
+    cfg.blockDim = dim3(pl.threads);
+    return cudaLaunchKernelExC(&cfg, (const void *)npa::gn_apply_kernel<T, kVec>, args) == cudaSuccess ? NPA_OK
+                                                                                                       : NPA_ERR_CUDA;
 }
 
 template <typename T>
@@ -1411,12 +1400,16 @@ npa_status npa_group_norm_act(const void *x, const void *weight, const void *bia
     prm.cw = pl.cw;
     prm.cols = pl.cols;
     prm.rows = pl.rows;
-    prm.segs = pl.segs;
+    prm.by_cols = npa::SmallDiv(pl.cols);
+    prm.by_cpg = npa::SmallDiv(C / groups);
     prm.tiles = pl.tiles;
     prm.tile_rows = pl.tile_rows;
     prm.eps = eps;
     prm.silu = act == NPA_ACT_SILU;
+    prm.apply_tiles = pl.apply_tiles;
+    prm.apply_rows = pl.apply_rows;
     prm.part = static_cast<float2 *>(workspace);
+    prm.mean_rstd = prm.part + (size_t)B * groups * pl.tiles;
     if (dtype == NPA_DTYPE_BF16) return launch_gn_vec<__nv_bfloat16>(prm, pl, B, C, stream);
     if (dtype == NPA_DTYPE_FP16) return launch_gn_vec<__half>(prm, pl, B, C, stream);
     return launch_gn_vec<float>(prm, pl, B, C, stream);

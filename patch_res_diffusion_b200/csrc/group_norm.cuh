@@ -2,24 +2,29 @@
 // (npa_group_norm_act):
 //   y[b, n, c] = act((x[b, n, c] - mean[b, g]) * rstd[b, g] * w[c] + bias[c]),  g = c / (C / groups),
 // mean and variance over the N tokens and the C / groups channels of a group.
-// Bound by memory: x read once and y written once. Two kernels reach that:
+// Bound by memory: x read once and y written once at best.
 //
 //  * gn_cluster_kernel: a cluster of up to 8 blocks holds a chunk of whole
 //    groups of one batch row in its shared memory, exchanges the groups'
 //    statistics through distributed shared memory and normalises from there.
 //    One launch, one pass over x. Taken when the chunk fits.
-//  * gn_step_kernel: otherwise the work is cut into items (a few batch rows, or
-//    a channel chunk of one) small enough to stay in L2 between their two
-//    passes. Launch s takes the statistics of item s and normalises item s - 1,
-//    so reading new data from memory and writing results overlap; a launch
-//    starts under the end of the one before it (programmatic serialisation)
-//    and waits for it only between its two halves.
+//  * otherwise gn_stats_kernel (x read, a pair for each token tile and group),
+//    gn_merge_kernel (the tiles of a group merged) and gn_apply_kernel (x read
+//    again, y written). The last one walks the tokens from the end, so that
+//    what the first one read last is still in L2. A launch starts under the end
+//    of the one before it (programmatic serialisation) and loads its first
+//    tokens before it waits for that one. Cutting x into items that stay in L2
+//    between the passes was slower: 258 us instead of 182 for [2, 262144, 320]
+//    bf16, whose items of 42 MB leave each launch too little to do.
 //
 // Nothing is accumulated with atomics: results do not depend on the order in
-// which blocks run. Statistics are float32 throughout and never a difference
-// of large sums: a thread takes the mean and the squared deviations of kBatch
-// values of one channel as defined (the values are in registers, so the second
-// pass costs no memory), and pairs (n, mean, M2) are merged by
+// which blocks run. Statistics are float32 throughout. A thread sums x - K and
+// (x - K)^2 of a channel, K the mean of that channel's first kGnBatch values it
+// sees, and takes M2 = sum (x - K)^2 - (sum (x - K))^2 / n. The subtraction
+// loses at most n (K - mean)^2 2^-24, and since K is the mean of kGnBatch
+// members, the group's M2 is at least kGnBatch (K - mean)^2: n is kept to
+// kGnRun, so the loss is below 2^-17 of M2 even for the worst data. Pairs
+// (n, mean, M2) are then merged by
 //   mean = sum n_i mean_i / n,   M2 = sum M2_i + sum n_i (mean_i - mean)^2.
 //
 // A thread owns one 16-byte column of channels (kVec = 8 or 4; 1 where
@@ -32,15 +37,28 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "kv8_store.cuh"
 
 namespace npa {
 
-constexpr int kGnThreads = 512;        // threads of a block at most
+constexpr int kGnThreads = 256;        // threads of a block at most
 constexpr int kGnMaxChannels = 4096;   // the block's statistics are kept in shared memory
-constexpr int kGnMaxTiles = 320;       // token tiles of an item at most: ten per lane when they are merged
+constexpr int kGnMaxTiles = 512;       // token tiles of an item at most
 constexpr int kGnMaxCluster = 8;       // the portable cluster size
+constexpr int kGnBatch = 4;            // tokens that a thread takes at a time
+constexpr int kGnLanes = 8;            // lanes that merge one group's channels
+constexpr int kGnRun = 512;            // values that share one shift K at most
+
+// n / d for 0 <= n < 2^16 and 1 <= d < 2^16: with m = floor(2^32 / d) + 1 the
+// product's error n (d - 2^32 mod d) / d stays below 2^32 / d.
+struct SmallDiv {
+    uint32_t m;  // 0: d = 1
+    __host__ __device__ SmallDiv() : m(0) {}
+    __host__ __device__ explicit SmallDiv(int d) : m(d > 1 ? uint32_t((1ull << 32) / d) + 1 : 0) {}
+    __device__ __forceinline__ int operator()(int n) const { return m ? int(__umulhi(uint32_t(n), m)) : n; }
+};
 
 struct GnParams {
     const void *x;
@@ -49,16 +67,15 @@ struct GnParams {
     int w_f32;             // w, bias are float32 (else of x's type)
     long long xsb, xst, ysb, yst;  // batch and token strides, elements
     int N, G, cpg;         // tokens, groups, channels per group
-    int cw;                // channels of a chunk: whole groups
+    int cw;                // channels of a chunk: whole groups (all but in gn_cluster_kernel)
     int cols, rows;        // block shape: columns (of kVec channels) x tokens
-    int segs;              // groups that kVec neighbouring channels touch at most
-    int tiles, tile_rows;  // token tiles (gn_cluster_kernel: blocks of the cluster) and tokens in each
+    SmallDiv by_cols, by_cpg;
+    int tiles, tile_rows;  // token tiles of the statistics (gn_cluster_kernel: blocks of the cluster), tokens in each
     float eps;
     int silu;
-    // gn_step_kernel: batch rows and first channel of the item whose
-    // statistics are taken and of the one that is normalised (rows 0: none)
-    int stat_b, stat_nb, stat_c, apply_b, apply_nb, apply_c;
+    int apply_tiles, apply_rows;  // token tiles of the normalisation and tokens in each
     float2 *part;          // [B][G][tiles] (mean, M2)
+    float2 *mean_rstd;     // [B][G]
 };
 
 template <typename T, int kVec>
@@ -103,161 +120,238 @@ __device__ __forceinline__ void let_next_kernel_start() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Sum over kLanes neighbouring lanes.
+template <int kLanes>
+__device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = kLanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
-// Mean and squared deviations of each of a thread's kVec channels, merged over
-// the values it has seen.
+// Sums of a thread's kVec channels; its entries (mean, M2) in shared memory
+// take one run of at most kGnRun values after the other.
 template <int kVec>
 struct GnAcc {
-    float mean[kVec], m2[kVec];
-    int n = 0;
-    __device__ __forceinline__ GnAcc() {
+    float shift[kVec], sum[kVec], square[kVec];  // K, sum (x - K), sum (x - K)^2
+    float2 *entry;
+    int n = 0, run = 0;  // values in the entries; in the current run
+    __device__ __forceinline__ explicit GnAcc(float2 *e) : entry(e) {}
+    // kCount more values of each channel.
+    template <typename V, int kCount>
+    __device__ __forceinline__ void add(const typename V::Raw *raw) {
+        if (run == 0) {
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) mean[k] = m2[k] = 0.f;
-    }
-    template <typename V, int kBatch>
-    __device__ __forceinline__ void add(const typename V::Raw (&raw)[kBatch], int valid) {
-        if (valid >= kBatch) {
-            float s[kVec], d2[kVec];
+            for (int k = 0; k < kVec; ++k) shift[k] = sum[k] = square[k] = 0.f;
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) s[k] = d2[k] = 0.f;
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
+            for (int i = 0; i < kCount; ++i) {
                 float f[kVec];
                 V::widen(raw[i], f);
 #pragma unroll
-                for (int k = 0; k < kVec; ++k) s[k] += f[k];
+                for (int k = 0; k < kVec; ++k) shift[k] = fmaf(f[k], 1.f / kCount, shift[k]);
             }
+        }
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) s[k] *= 1.f / kBatch;
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                float f[kVec];
-                V::widen(raw[i], f);
-#pragma unroll
-                for (int k = 0; k < kVec; ++k) d2[k] = fmaf(f[k] - s[k], f[k] - s[k], d2[k]);
-            }
-            const float share = __fdividef(float(kBatch), float(n + kBatch));
-            const float cross = share * float(n);
+        for (int i = 0; i < kCount; ++i) {
+            float f[kVec];
+            V::widen(raw[i], f);
 #pragma unroll
             for (int k = 0; k < kVec; ++k) {
-                const float d = s[k] - mean[k];
-                mean[k] = fmaf(d, share, mean[k]);
-                m2[k] += fmaf(d * d, cross, d2[k]);
-            }
-            n += kBatch;
-        } else {
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                if (i >= valid) break;
-                float f[kVec];
-                V::widen(raw[i], f);
-                const float share = __fdividef(1.f, float(n + 1));
-#pragma unroll
-                for (int k = 0; k < kVec; ++k) {
-                    const float d = f[k] - mean[k];
-                    mean[k] = fmaf(d, share, mean[k]);
-                    m2[k] = fmaf(d, f[k] - mean[k], m2[k]);
-                }
-                ++n;
+                const float d = f[k] - shift[k];
+                sum[k] += d;
+                square[k] = fmaf(d, d, square[k]);
             }
         }
+        run += kCount;
+        if (run >= kGnRun) flush();
     }
-    // One entry (mean, M2) for each group that column `col` touches.
-    __device__ __forceinline__ void store(const GnParams &p, int col, float2 *entry) const {
-        const int g0 = col * kVec / p.cpg;
-        for (int s = 0; s < p.segs; ++s) {
-            const int lo = (g0 + s) * p.cpg - col * kVec, hi = lo + p.cpg;  // the group's channels of this column
-            float sum = 0.f, cnt = 0.f;
+    __device__ __forceinline__ void flush() {
+        if (run == 0) {  // no values at all: entries of weight 0
+            if (n > 0) return;
 #pragma unroll
-            for (int k = 0; k < kVec; ++k)
-                if (k >= lo && k < hi) {
-                    sum += mean[k];
-                    cnt += 1.f;
-                }
-            const float mu = cnt > 0.f ? __fdividef(sum, cnt) : 0.f;
-            float q = 0.f;
-#pragma unroll
-            for (int k = 0; k < kVec; ++k)
-                if (k >= lo && k < hi) q += fmaf(float(n) * (mean[k] - mu), mean[k] - mu, m2[k]);
-            entry[s] = make_float2(mu, q);
+            for (int k = 0; k < kVec; ++k) entry[k] = make_float2(0.f, 0.f);
+            return;
         }
+        const float inv = __fdividef(1.f, float(run));
+        const float share = __fdividef(float(run), float(n + run)), cross = share * float(n);
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) {
+            const float d = sum[k] * inv, mean = d + shift[k], m2 = fmaf(-sum[k], d, square[k]);
+            float2 old = make_float2(mean, 0.f);
+            if (n) old = entry[k];
+            const float e = mean - old.x;
+            entry[k] = make_float2(fmaf(e, share, old.x), old.y + fmaf(e * e, cross, m2));
+        }
+        n += run;
+        run = 0;
     }
 };
 
-// (mean, M2) of one group over a tile of `tokens` tokens, from the block's
-// entries [rows][columns of the chunk][segs]. One warp; every lane gets them.
-template <int kVec>
-__device__ __forceinline__ float2 gn_group_of_block(const GnParams &p, const float2 *entry, int g, int tokens) {
-    const int lane = threadIdx.x & 31;
-    const int v0 = g * p.cpg / kVec, v1 = ((g + 1) * p.cpg - 1) / kVec, nv = v1 - v0 + 1;
-    const int ncol = p.cw / kVec, entries = p.rows * nv;
-    float s = 0.f;
-    for (int i = lane; i < entries; i += 32) {
-        const int y = i / nv, v = v0 + i - y * nv;
-        const int ch = min((v + 1) * kVec, (g + 1) * p.cpg) - max(v * kVec, g * p.cpg);
-        const int n = (tokens - y + p.rows - 1) / p.rows;
-        s = fmaf(float(n * ch), entry[((size_t)y * ncol + v) * p.segs + g - v * kVec / p.cpg].x, s);
-    }
-    const float mean = warp_sum(s) / (float(tokens) * float(p.cpg));
-    float m2 = 0.f;
-    for (int i = lane; i < entries; i += 32) {
-        const int y = i / nv, v = v0 + i - y * nv;
-        const int ch = min((v + 1) * kVec, (g + 1) * p.cpg) - max(v * kVec, g * p.cpg);
-        const int n = (tokens - y + p.rows - 1) / p.rows;
-        const float2 e = entry[((size_t)y * ncol + v) * p.segs + g - v * kVec / p.cpg];
-        const float d = e.x - mean;
-        m2 += fmaf(float(n * ch) * d, d, e.y);
-    }
-    return make_float2(mean, warp_sum(m2));
+// body(g, lane) for g = 0 .. n - 1, kGnLanes neighbouring threads to a group.
+// Every thread of a warp runs the same number of rounds (with the last group
+// again where there is none left), so body may exchange values between lanes.
+template <typename Body>
+__device__ __forceinline__ void for_groups(int n, Body body) {
+    const int per_round = blockDim.x / kGnLanes;
+    for (int g0 = 0; g0 < n; g0 += per_round)
+        body(min(g0 + int(threadIdx.x) / kGnLanes, n - 1), int(threadIdx.x) % kGnLanes);
 }
 
-template <typename T>
-__device__ __forceinline__ float gn_weight(const void *w, int f32, int c) {
-    return f32 ? __ldg(static_cast<const float *>(w) + c) : float(static_cast<const T *>(w)[c]);
+// From a block's entries [rows][cw + 1] (mean, M2) over a tile of `tokens`
+// tokens: emit(g, lane, pair) for every group of the chunk, by each of its
+// lanes. First the rows of a channel are merged (into its row 0), by one
+// thread or, where there are many rows, by kGnLanes, then kGnLanes threads
+// merge the channels of a group.
+template <int kLanes>
+__device__ __forceinline__ void gn_merge_rows(const GnParams &p, float2 *entry, int tokens, int c, int lane) {
+    const int base = tokens / p.rows, more = tokens - base * p.rows;  // tokens of row y: base, one more for y < more
+    const float n0 = float(base), n1 = float(base + 1);
+    float s = 0.f, m2 = 0.f;
+#pragma unroll 4
+    for (int y = lane; y < p.rows; y += kLanes) s = fmaf(y < more ? n1 : n0, entry[y * (p.cw + 1) + c].x, s);
+    const float mean = lanes_sum<kLanes>(s) / float(tokens);
+#pragma unroll 4
+    for (int y = lane; y < p.rows; y += kLanes) {
+        const float2 q = entry[y * (p.cw + 1) + c];
+        const float d = q.x - mean;
+        m2 += fmaf((y < more ? n1 : n0) * d, d, q.y);
+    }
+    m2 = lanes_sum<kLanes>(m2);
+    if (lane == 0) entry[c] = make_float2(mean, m2);
 }
 
-__device__ __forceinline__ float silu(float y) { return __fdividef(y, 1.f + __expf(-y)); }
+template <typename Emit>
+__device__ __forceinline__ void gn_groups_of_block(const GnParams &p, float2 *entry, int tokens, Emit emit) {
+    __syncthreads();
+    if (p.rows > kGnLanes) {
+        const int per_round = blockDim.x / kGnLanes, c = int(threadIdx.x) / kGnLanes, lane = int(threadIdx.x) % kGnLanes;
+        // the channels past the last are read and written by nobody, but take part in the exchange
+        for (int c0 = 0; c0 < p.cw; c0 += per_round)
+            gn_merge_rows<kGnLanes>(p, entry, c0 + c < p.cw ? tokens : 1, min(c0 + c, p.cw), lane);
+    } else {
+        for (int c = threadIdx.x; c < p.cw; c += blockDim.x) gn_merge_rows<1>(p, entry, tokens, c, 0);
+    }
+    __syncthreads();
+    const float inv_cpg = 1.f / float(p.cpg);
+    for_groups(p.by_cpg(p.cw), [&](int g, int lane) {
+        const float2 *e = entry + g * p.cpg;
+        float s = 0.f, m2 = 0.f;
+        for (int c = lane; c < p.cpg; c += kGnLanes) s += e[c].x;
+        const float mean = lanes_sum<kGnLanes>(s) * inv_cpg;
+        for (int c = lane; c < p.cpg; c += kGnLanes) {
+            const float d = e[c].x - mean;
+            m2 += fmaf(float(tokens) * d, d, e[c].y);
+        }
+        emit(g, lane, make_float2(mean, lanes_sum<kGnLanes>(m2)));
+    });
+}
 
-// What a thread needs to normalise its column.
+// (mean, rstd) of a group from its pairs over p.tiles <= kLanes * kPer tiles,
+// by kLanes neighbouring lanes. Tiles hold p.tile_rows tokens, the one at
+// p.N's end fewer, any after it none.
+template <int kLanes, int kPer>
+__device__ __forceinline__ float2 gn_merge_tiles(const GnParams &p, const float2 *pair, int pitch, int lane) {
+    float2 q[kPer];
+    float w[kPer], s = 0.f, m2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int t = lane + kLanes * i;
+        q[i] = t < p.tiles ? pair[(size_t)t * pitch] : make_float2(0.f, 0.f);
+        w[i] = t < p.tiles ? float(min(max(p.N - t * p.tile_rows, 0), p.tile_rows)) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) s = fmaf(w[i], q[i].x, s);
+    const float mean = lanes_sum<kLanes>(s) / float(p.N);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const float d = q[i].x - mean;
+        m2 += w[i] > 0.f ? fmaf(w[i] * float(p.cpg) * d, d, q[i].y) : 0.f;
+    }
+    return make_float2(mean, rsqrtf(lanes_sum<kLanes>(m2) / (float(p.N) * float(p.cpg)) + p.eps));
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// What a thread needs to normalise its column: weight and bias are read early,
+// the statistics come later.
 template <typename T, int kVec>
 struct GnAffine {
-    float mean[kVec], a[kVec], bias[kVec];
-    int act;
-    __device__ __forceinline__ GnAffine(const GnParams &p, const float *sm_mean, const float *sm_rstd, int col, int c0)
-        : act(p.silu) {
+    float a[kVec], bias[kVec];  // y = x a + bias
+    __device__ __forceinline__ void weights(const GnParams &p, int col, int c0) {
+        const int c = c0 + col * kVec;
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) {
-            const int g = (col * kVec + k) / p.cpg, c = c0 + col * kVec + k;
-            mean[k] = sm_mean[g];
-            a[k] = sm_rstd[g] * (p.w ? gn_weight<T>(p.w, p.w_f32, c) : 1.f);
-            bias[k] = p.bias ? gn_weight<T>(p.bias, p.w_f32, c) : 0.f;
+        for (int k = 0; k < kVec; ++k) a[k] = 1.f, bias[k] = 0.f;
+        if (p.w_f32) {
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) {
+                if (p.w) a[k] = __ldg(static_cast<const float *>(p.w) + c + k);
+                if (p.bias) bias[k] = __ldg(static_cast<const float *>(p.bias) + c + k);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) {
+                if (p.w) a[k] = float(static_cast<const T *>(p.w)[c + k]);
+                if (p.bias) bias[k] = float(static_cast<const T *>(p.bias)[c + k]);
+            }
         }
     }
-    __device__ __forceinline__ typename GnVec<T, kVec>::Raw operator()(typename GnVec<T, kVec>::Raw raw) const {
+    // mean_rstd: of the chunk's groups. x a - mean a costs no more precision
+    // than the mean's own rounding.
+    __device__ __forceinline__ void statistics(const GnParams &p, const float2 *mean_rstd, int col) {
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) {
+            const float2 s = mean_rstd[p.by_cpg(col * kVec + k)];
+            a[k] *= s.y;
+            bias[k] = fmaf(-s.x, a[k], bias[k]);
+        }
+    }
+    template <bool kSilu>
+    __device__ __forceinline__ typename GnVec<T, kVec>::Raw apply(typename GnVec<T, kVec>::Raw raw) const {
         float f[kVec];
         GnVec<T, kVec>::widen(raw, f);
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) f[k] = fmaf(f[k] - mean[k], a[k], bias[k]);
-        if (act) {
+        for (int k = 0; k < kVec; ++k) f[k] = fmaf(f[k], a[k], bias[k]);
+        if constexpr (kSilu) {
+            // z / (1 + e^-z), two to a reciprocal: 1 / u = v / (u v). The power
+            // is kept below 2^63 so that u v is finite; z < -43 then gives
+            // z 2^-63, below 5e-18 in size.
+            float u[kVec];
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) f[k] = silu(f[k]);
+            for (int k = 0; k < kVec; ++k) u[k] = 1.f + sm100::ex2_approx(fminf(-1.4426950408889634f * f[k], 63.f));
+#pragma unroll
+            for (int k = 0; k + 1 < kVec; k += 2) {
+                const float r = rcp_approx(u[k] * u[k + 1]);
+                f[k] *= r * u[k + 1];
+                f[k + 1] *= r * u[k];
+            }
+            if (kVec % 2) f[kVec - 1] *= rcp_approx(u[kVec - 1]);
         }
         return GnVec<T, kVec>::narrow(f);
     }
 };
 
 // ---------------------------------------------------------------------------
+// Asynchronous copies of 16 bytes into a thread's own shared memory slots
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void copy16_async(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sm100::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest N groups of this thread's copies have landed.
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ---------------------------------------------------------------------------
 // A chunk in a cluster's shared memory
 // ---------------------------------------------------------------------------
 // Grid (cluster blocks, channel chunks, batch rows). Shared memory: the
-// block's tokens, 16 bytes per thread and step (a thread reads back what it
-// wrote itself), then the entries, the cluster's pairs [blocks][groups], and
-// mean and rstd [groups].
+// block's tokens, 16 bytes per thread and step, then the entries, the
+// cluster's pairs [blocks][groups], and (mean, rstd) [groups].
 template <typename T, int kVec>
 __global__ void __launch_bounds__(kGnThreads) gn_cluster_kernel(const __grid_constant__ GnParams p) {
     using V = GnVec<T, kVec>;
@@ -265,154 +359,178 @@ __global__ void __launch_bounds__(kGnThreads) gn_cluster_kernel(const __grid_con
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     extern __shared__ uint4 gn_smem16[];
-    const int ng = p.cw / p.cpg, threads = p.cols * p.rows;
-    const int steps = (p.tile_rows + p.rows - 1) / p.rows;
+    const int ng = p.by_cpg(p.cw), threads = p.cols * p.rows;
+    const int steps = p.tile_rows / p.rows;
     Raw *slab = reinterpret_cast<Raw *>(gn_smem16);
     float2 *entry = reinterpret_cast<float2 *>(slab + (size_t)steps * threads);
-    float2 *pairs = entry + (size_t)p.rows * (p.cw / kVec) * p.segs;
-    float *sm_mean = reinterpret_cast<float *>(pairs + (size_t)p.tiles * ng), *sm_rstd = sm_mean + ng;
+    float2 *pairs = entry + (size_t)p.rows * (p.cw + 1);
+    float2 *mean_rstd = pairs + (size_t)p.tiles * ng;
 
     // the other blocks' shared memory is written below: they have to be there
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const int rank = blockIdx.x, b = blockIdx.z, c0 = blockIdx.y * p.cw;
-    const int tx = threadIdx.x % p.cols, ty = threadIdx.x / p.cols;
+    const int ty = p.by_cols(threadIdx.x), tx = threadIdx.x - ty * p.cols;
     const int r0 = rank * p.tile_rows, tokens = max(0, min(p.tile_rows, p.N - r0));
-    constexpr int kBatch = 8;
     const int mine = ty < p.rows ? (tokens - ty + p.rows - 1) / p.rows : 0;  // this thread's tokens
-    const long long xstep = (long long)p.rows * p.xst;
+    constexpr int kGroup = 8, kAhead = 4;  // tokens of a copy group, groups in flight
+    slab += threadIdx.x;
+    GnAffine<T, kVec> f;
     if (ty < p.rows) {
+        const long long step = (long long)p.rows * p.xst;
         const T *src = static_cast<const T *>(p.x) + b * p.xsb + c0 + tx * kVec + (long long)(r0 + ty) * p.xst;
-        GnAcc<kVec> acc;
-        for (int k = 0; k < mine; k += kBatch) {
-            Raw raw[kBatch];
+        auto fetch = [&](int k) {
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                if (k + i < mine) raw[i] = *reinterpret_cast<const Raw *>(src + (k + i) * xstep);
+            for (int i = 0; i < kGroup; ++i)
+                if (k + i < mine) copy16_async(slab + (size_t)(k + i) * threads, src + (k + i) * step);
+            copy_commit();
+        };
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                if (k + i < mine) slab[(size_t)(k + i) * threads + threadIdx.x] = raw[i];
-            acc.template add<V>(raw, mine - k);
+        for (int a = 0; a < kAhead; ++a) fetch(a * kGroup);
+        f.weights(p, tx, c0);
+        GnAcc<kVec> acc(entry + (size_t)ty * (p.cw + 1) + tx * kVec);
+        for (int k = 0; k < mine; k += kGroup) {
+            copy_wait<kAhead - 1>();
+            const Raw *at = slab + (size_t)k * threads;
+            const int left = min(mine - k, kGroup);
+            if (left == kGroup) {
+                Raw raw[kGroup];
+#pragma unroll
+                for (int i = 0; i < kGroup; ++i) raw[i] = at[(size_t)i * threads];
+                acc.template add<V, kGroup>(raw);
+            } else {
+                for (int i = 0; i < left; ++i, at += threads) acc.template add<V, 1>(at);
+            }
+            fetch(k + kAhead * kGroup);
         }
-        acc.store(p, tx, entry + ((size_t)ty * p.cols + tx) * p.segs);
+        acc.flush();
     }
-    __syncthreads();
+    __syncwarp();
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    for (int g = threadIdx.x >> 5; g < ng; g += warps) {
-        const float2 q = tokens > 0 ? gn_group_of_block<kVec>(p, entry, g, tokens) : make_float2(0.f, 0.f);
+    // a block without tokens counts with weight 0
+    gn_groups_of_block(p, entry, max(tokens, 1), [&](int g, int lane, float2 q) {
         if (lane < p.tiles) cluster.map_shared_rank(pairs, lane)[rank * ng + g] = q;
-    }
+    });
     cluster.sync();
-    for (int g = threadIdx.x; g < ng; g += blockDim.x) {
-        const float total = float(p.N);
-        float s = 0.f, m2 = 0.f;
-        for (int t = 0; t < p.tiles; ++t)
-            s = fmaf(float(max(0, min(p.tile_rows, p.N - t * p.tile_rows))), pairs[t * ng + g].x, s);
-        const float mean = s / total;
-        for (int t = 0; t < p.tiles; ++t) {
-            const float2 q = pairs[t * ng + g];
-            const float d = q.x - mean;
-            m2 += fmaf(float(max(0, min(p.tile_rows, p.N - t * p.tile_rows))) * float(p.cpg) * d, d, q.y);
-        }
-        sm_mean[g] = mean;
-        sm_rstd[g] = rsqrtf(m2 / (total * float(p.cpg)) + p.eps);
-    }
+    for_groups(ng, [&](int g, int lane) {
+        const float2 q = gn_merge_tiles<kGnLanes, kGnMaxCluster / kGnLanes>(p, pairs + g, ng, lane);
+        if (lane == 0) mean_rstd[g] = q;
+    });
     __syncthreads();
     if (ty >= p.rows) return;
-    const GnAffine<T, kVec> f(p, sm_mean, sm_rstd, tx, c0);
+    f.statistics(p, mean_rstd, tx);
     T *dst = static_cast<T *>(p.y) + b * p.ysb + c0 + tx * kVec + (long long)(r0 + ty) * p.yst;
+    const long long step = (long long)p.rows * p.yst;
+    auto write = [&](auto silu) {
 #pragma unroll 4
-    for (int k = 0; k < mine; ++k)
-        *reinterpret_cast<Raw *>(dst + (long long)k * p.rows * p.yst) = f(slab[(size_t)k * threads + threadIdx.x]);
+        for (int k = 0; k < mine; ++k, dst += step, slab += threads)
+            *reinterpret_cast<Raw *>(dst) = f.template apply<decltype(silu)::value>(*slab);
+    };
+    if (p.silu)
+        write(std::true_type{});
+    else
+        write(std::false_type{});
 }
 
 // ---------------------------------------------------------------------------
-// Items through L2
+// Three launches
 // ---------------------------------------------------------------------------
+// Grid (token tiles, batch rows). Shared memory: the entries.
 template <typename T, int kVec>
-__global__ void __launch_bounds__(kGnThreads, 2) gn_step_kernel(const __grid_constant__ GnParams p) {
+__global__ void __launch_bounds__(kGnThreads, 3) gn_stats_kernel(const __grid_constant__ GnParams p) {
     using V = GnVec<T, kVec>;
     using Raw = typename V::Raw;
-    constexpr int kBatch = 4;  // tokens in flight per thread
-    extern __shared__ uint4 gn_smem16[];  // statistics: the entries; normalisation: mean and rstd [groups of the item]
-    let_next_kernel_start();
-    const int tile = blockIdx.x;
-    const int tx = threadIdx.x % p.cols, ty = threadIdx.x / p.cols;
-    const int r0 = tile * p.tile_rows, r1 = min(p.N, r0 + p.tile_rows);
-    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5, ng = p.cw / p.cpg;
+    extern __shared__ uint4 gn_smem16[];
     float2 *entry = reinterpret_cast<float2 *>(gn_smem16);
-    const bool stat = blockIdx.y < p.stat_nb;
-    if (stat) {
-        const T *x = static_cast<const T *>(p.x) + (p.stat_b + blockIdx.y) * p.xsb + p.stat_c;
-        for (int col = tx; ty < p.rows && col * kVec < p.cw; col += p.cols) {
-            const T *src = x + col * kVec;
-            GnAcc<kVec> acc;
-            for (int r = r0 + ty; r < r1; r += p.rows * kBatch) {
-                Raw raw[kBatch];
+    let_next_kernel_start();
+    const int tile = blockIdx.x, b = blockIdx.y;
+    const int ty = p.by_cols(threadIdx.x), tx = threadIdx.x - ty * p.cols;
+    const int r0 = tile * p.tile_rows, tokens = min(p.N - r0, p.tile_rows);
+    const T *src = static_cast<const T *>(p.x) + b * p.xsb + tx * kVec + (long long)(r0 + ty) * p.xst;
+    const long long step = (long long)p.rows * p.xst;
+    for (int col = tx; ty < p.rows && col * kVec < p.cw; col += p.cols, src += p.cols * kVec) {
+        GnAcc<kVec> acc(entry + (size_t)ty * (p.cw + 1) + col * kVec);
+        const T *at = src;
+        int left = (tokens - ty + p.rows - 1) / p.rows;  // this thread's tokens
+        Raw raw[kGnBatch], next[kGnBatch];               // the next batch is on its way while one is summed
+        auto fetch = [&](Raw(&to)[kGnBatch]) {
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i)
-                    if (r + i * p.rows < r1)
-                        raw[i] = *reinterpret_cast<const Raw *>(src + (long long)(r + i * p.rows) * p.xst);
-                acc.template add<V>(raw, (r1 - r + p.rows - 1) / p.rows);
-            }
-            acc.store(p, col, entry + ((size_t)ty * (p.cw / kVec) + col) * p.segs);
+            for (int i = 0; i < kGnBatch; ++i, at += step) to[i] = *reinterpret_cast<const Raw *>(at);
+        };
+        if (left >= kGnBatch) fetch(raw);
+        for (; left >= kGnBatch; left -= kGnBatch) {
+            if (left >= 2 * kGnBatch) fetch(next);
+            acc.template add<V, kGnBatch>(raw);
+#pragma unroll
+            for (int i = 0; i < kGnBatch; ++i) raw[i] = next[i];
         }
-        __syncthreads();
+        for (; left > 0; --left, at += step) {
+            const Raw one = *reinterpret_cast<const Raw *>(at);
+            acc.template add<V, 1>(&one);
+        }
+        acc.flush();
     }
-    // everything launched before is complete: the previous launch's statistics
-    // can be read, and a launch that waits for this one waits for those too
+    float2 *out = p.part + (size_t)b * p.G * p.tiles + tile;
+    gn_groups_of_block(p, entry, tokens, [&](int g, int lane, float2 q) {
+        if (lane == 0) out[(size_t)g * p.tiles] = q;
+    });
+}
+
+// One warp to a (batch row, group).
+__global__ void __launch_bounds__(128) gn_merge_kernel(const __grid_constant__ GnParams p, int n) {
+    let_next_kernel_start();
+    const int g = blockIdx.x * 4 + (threadIdx.x >> 5);
     wait_for_previous_kernel();
-    if (stat) {
-        float2 *out = p.part + ((size_t)(p.stat_b + blockIdx.y) * p.G + p.stat_c / p.cpg) * p.tiles + tile;
-        for (int g = threadIdx.x >> 5; g < ng; g += warps) {
-            const float2 q = gn_group_of_block<kVec>(p, entry, g, r1 - r0);
-            if (lane == 0) out[(size_t)g * p.tiles] = q;
-        }
-        __syncthreads();
-    }
-    if (blockIdx.y >= p.apply_nb) return;
-    float *sm_mean = reinterpret_cast<float *>(gn_smem16), *sm_rstd = sm_mean + ng;
-    const int b = p.apply_b + blockIdx.y;
-    for (int g = threadIdx.x >> 5; g < ng; g += warps) {
-        const float2 *part = p.part + ((size_t)b * p.G + p.apply_c / p.cpg + g) * p.tiles;
-        constexpr int kPer = kGnMaxTiles / 32;
-        float2 q[kPer];
+    if (g >= n) return;
+    const float2 q = gn_merge_tiles<32, kGnMaxTiles / 32>(p, p.part + (size_t)g * p.tiles, 1, threadIdx.x & 31);
+    if ((threadIdx.x & 31) == 0) p.mean_rstd[g] = q;
+}
+
+// Grid (token tiles, batch rows), both from the end.
+template <typename T, int kVec>
+__global__ void __launch_bounds__(kGnThreads, 3) gn_apply_kernel(const __grid_constant__ GnParams p) {
+    using V = GnVec<T, kVec>;
+    using Raw = typename V::Raw;
+    let_next_kernel_start();
+    const int ty = p.by_cols(threadIdx.x), tx = threadIdx.x - ty * p.cols;
+    const int r0 = (gridDim.x - 1 - blockIdx.x) * p.apply_rows, tokens = min(p.N - r0, p.apply_rows);
+    const int b = gridDim.y - 1 - blockIdx.y;
+    const T *src = static_cast<const T *>(p.x) + b * p.xsb + tx * kVec + (long long)(r0 + ty) * p.xst;
+    T *out = static_cast<T *>(p.y) + b * p.ysb + tx * kVec + (long long)(r0 + ty) * p.yst;
+    const long long xstep = (long long)p.rows * p.xst, ystep = (long long)p.rows * p.yst;
+    const float2 *mean_rstd = p.mean_rstd + (size_t)b * p.G;
+    bool waited = false;
+    for (int col = tx; ty < p.rows && col * kVec < p.cw; col += p.cols, src += p.cols * kVec, out += p.cols * kVec) {
+        const T *at = src;
+        T *dst = out;
+        int left = (tokens - ty + p.rows - 1) / p.rows;
+        Raw raw[kGnBatch], next[kGnBatch];  // the next batch is on its way while one is written
+        auto fetch = [&](Raw(&to)[kGnBatch]) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) q[i] = lane + 32 * i < p.tiles ? part[lane + 32 * i] : make_float2(0.f, 0.f);
-        const float total = float(p.N);
-        float s = 0.f, m2 = 0.f;
+            for (int i = 0; i < kGnBatch; ++i, at += xstep) to[i] = __ldcs(reinterpret_cast<const Raw *>(at));
+        };
+        if (left >= kGnBatch) fetch(raw);
+        GnAffine<T, kVec> f;
+        f.weights(p, col, 0);
+        if (!waited) wait_for_previous_kernel();
+        waited = true;
+        f.statistics(p, mean_rstd, col);
+        auto write = [&](auto silu) {
+            constexpr bool kSilu = decltype(silu)::value;
+            for (; left >= kGnBatch; left -= kGnBatch) {
+                if (left >= 2 * kGnBatch) fetch(next);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            s = fmaf(float(max(0, min(p.tile_rows, p.N - (lane + 32 * i) * p.tile_rows))), q[i].x, s);
-        const float mean = warp_sum(s) / total;
+                for (int i = 0; i < kGnBatch; ++i, dst += ystep)
+                    __stcs(reinterpret_cast<Raw *>(dst), f.template apply<kSilu>(raw[i]));
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const float d = q[i].x - mean;
-            m2 += fmaf(float(max(0, min(p.tile_rows, p.N - (lane + 32 * i) * p.tile_rows))) * float(p.cpg) * d, d, q[i].y);
-        }
-        m2 = warp_sum(m2);
-        if (lane == 0) {
-            sm_mean[g] = mean;
-            sm_rstd[g] = rsqrtf(m2 / (total * float(p.cpg)) + p.eps);
-        }
-    }
-    __syncthreads();
-    if (ty >= p.rows) return;
-    for (int col = tx; col * kVec < p.cw; col += p.cols) {
-        const GnAffine<T, kVec> f(p, sm_mean, sm_rstd, col, p.apply_c);
-        const T *src = static_cast<const T *>(p.x) + b * p.xsb + p.apply_c + col * kVec;
-        T *dst = static_cast<T *>(p.y) + b * p.ysb + p.apply_c + col * kVec;
-        for (int r = r0 + ty; r < r1; r += p.rows * kBatch) {
-            Raw raw[kBatch];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                if (r + i * p.rows < r1)
-                    raw[i] = __ldcs(reinterpret_cast<const Raw *>(src + (long long)(r + i * p.rows) * p.xst));
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                if (r + i * p.rows < r1)
-                    __stcs(reinterpret_cast<Raw *>(dst + (long long)(r + i * p.rows) * p.yst), f(raw[i]));
-        }
+                for (int i = 0; i < kGnBatch; ++i) raw[i] = next[i];
+            }
+            for (; left > 0; --left, at += xstep, dst += ystep)
+                __stcs(reinterpret_cast<Raw *>(dst), f.template apply<kSilu>(__ldcs(reinterpret_cast<const Raw *>(at))));
+        };
+        if (p.silu)
+            write(std::true_type{});
+        else
+            write(std::false_type{});
     }
 }
 
