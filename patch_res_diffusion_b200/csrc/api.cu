@@ -15,6 +15,7 @@
 #include "npa.h"
 #include "asg_combine.cuh"
 #include "cross_attention.cuh"
+#include "cross_attention_short.cuh"
 #include "group_norm.cuh"
 #include "kv8_store.cuh"
 #include "md_combine.cuh"
@@ -599,6 +600,14 @@ bool prepare_xa_kernel() {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) == cudaSuccess;
 }
 
+constexpr int kMaxSmem = 227 * 1024;
+
+template <int D, bool F16>
+bool prepare_xs_kernel() {
+    return cudaFuncSetAttribute(npa::xa_short_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) ==
+           cudaSuccess;
+}
+
 // ensure_ready plus the cross-attention kernels' limits, once per device.
 npa_status ensure_xa_ready(int *sm_count) {
     const npa_status st = ensure_ready(sm_count);
@@ -610,7 +619,9 @@ npa_status ensure_xa_ready(int *sm_count) {
     if (!ds.xa_checked) {
         const bool ok = prepare_xa_kernel<64, false, false>() && prepare_xa_kernel<64, false, true>() &&
                         prepare_xa_kernel<128, false, false>() && prepare_xa_kernel<128, false, true>() &&
-                        prepare_xa_kernel<64, true, false>() && prepare_xa_kernel<128, true, false>();
+                        prepare_xa_kernel<64, true, false>() && prepare_xa_kernel<128, true, false>() &&
+                        prepare_xs_kernel<64, false>() && prepare_xs_kernel<64, true>() &&
+                        prepare_xs_kernel<128, false>() && prepare_xs_kernel<128, true>();
         ds.xa_status = ok ? NPA_OK : NPA_ERR_UNSUPPORTED;
         ds.xa_checked = true;
     }
@@ -661,16 +672,16 @@ npa_status make_view(View *v, const void *ptr, const npa_strides *s, int B, int 
     return NPA_OK;
 }
 
-// 4D map {d, L, heads, B}; an axis with stride 0 becomes one entry long (the
+// 4D map {d, L, heads, B}, boxes of `rows` tokens; an axis with stride 0 becomes one entry long (the
 // kernel multiplies its coordinate by 0).
-bool encode_view(CUtensorMap *m, const View &v, bool f16) {
+bool encode_view(CUtensorMap *m, const View &v, bool f16, int rows = 128) {
     const bool codes = v.elem == 1;
     const cuuint64_t dims[4] = {(cuuint64_t)v.d, (cuuint64_t)v.L, (cuuint64_t)(v.sh ? v.heads : 1),
                                 (cuuint64_t)(v.sb ? v.B : 1)};
     const cuuint64_t row = (cuuint64_t)v.d * v.elem;
     const cuuint64_t strides[3] = {(cuuint64_t)v.st * v.elem, v.sh ? (cuuint64_t)v.sh * v.elem : row,
                                    v.sb ? (cuuint64_t)v.sb * v.elem : row};
-    const cuuint32_t box[4] = {codes ? (cuuint32_t)v.d : 64u, 128, 1, 1};
+    const cuuint32_t box[4] = {codes ? (cuuint32_t)v.d : 64u, (cuuint32_t)rows, 1, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     return g_encode(m,
                     codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8
@@ -744,6 +755,27 @@ npa_status validate_xa_buffers(const XaCall &c) {
     return NPA_OK;
 }
 
+template <int D, bool F16>
+npa_status launch_xs_kernel(const XaCall &c, const npa::XaParams &a, int sm_count, npa_stream_t stream) {
+    using C = npa::XsCfg<D>;
+    npa::XsParams prm;
+    std::memset(&prm, 0, sizeof(prm));
+    prm.a = a;
+    prm.kv_rows = (a.Lk + 15) / 16 * 16;
+    prm.kv_stages = C::smem_bytes(prm.kv_rows, 2) <= kMaxSmem ? 2 : 1;
+    prm.n_qtiles = (a.Lq + 127) / 128;
+    prm.n_tiles = a.B * a.heads * prm.n_qtiles;  // at most twice the units
+    prm.by_qtiles = npa::FastDiv(prm.n_qtiles);
+    if (!encode_view(&prm.a.tm_k, c.k, F16, prm.kv_rows) || !encode_view(&prm.a.tm_v, c.v, F16, prm.kv_rows))
+        return NPA_ERR_CUDA;
+    void *args[1] = {&prm};
+    const unsigned grid = (unsigned)(prm.n_tiles < sm_count ? prm.n_tiles : sm_count);
+    return cudaLaunchKernel((const void *)npa::xa_short_kernel<D, F16>, dim3(grid), dim3(C::kThreads), args,
+                            C::smem_bytes(prm.kv_rows, prm.kv_stages), (cudaStream_t)stream) == cudaSuccess
+               ? NPA_OK
+               : NPA_ERR_CUDA;
+}
+
 npa_status launch_xa(const XaCall &c, npa_stream_t stream) {
     int sm_count = 0;
     const npa_status st = ensure_xa_ready(&sm_count);
@@ -786,10 +818,18 @@ npa_status launch_xa(const XaCall &c, npa_stream_t stream) {
         prm.ml = prm.o_part + (size_t)splits * rows * d;
     }
     prm.n_units = (int)(base * splits);
-    if (!encode_view(&prm.tm_q, c.q, c.f16) || !encode_view(&prm.tm_k, c.k, c.f16) ||
-        !encode_view(&prm.tm_v, c.v, c.f16) || !encode_view(&prm.tm_o, c.o, c.f16))
-        return NPA_ERR_CUDA;
+    prm.by_splits = npa::FastDiv(splits);
+    prm.by_qpairs = npa::FastDiv(prm.n_qpairs);
+    prm.by_heads = npa::FastDiv(heads);
+    prm.by_group = npa::FastDiv(prm.group);
     const bool kv8 = c.k_scale != nullptr;
+    if (!encode_view(&prm.tm_q, c.q, c.f16) || !encode_view(&prm.tm_o, c.o, c.f16)) return NPA_ERR_CUDA;
+    if (!kv8 && Lk <= npa::kXaShortKeys)
+        return d == 64 ? (c.f16 ? launch_xs_kernel<64, true>(c, prm, sm_count, stream)
+                                : launch_xs_kernel<64, false>(c, prm, sm_count, stream))
+                       : (c.f16 ? launch_xs_kernel<128, true>(c, prm, sm_count, stream)
+                                : launch_xs_kernel<128, false>(c, prm, sm_count, stream));
+    if (!encode_view(&prm.tm_k, c.k, c.f16) || !encode_view(&prm.tm_v, c.v, c.f16)) return NPA_ERR_CUDA;
     const void *kernel;
     unsigned threads, smem;
     auto pick = [&](const void *k, auto cfg) {

@@ -41,6 +41,19 @@ namespace npa {
 constexpr int kKv8Block = 64;  // tokens of one head that share a scale of the 8-bit cache
 constexpr int kXaMaxSplits = 64;  // key-range splits at most
 
+// n / d for 0 <= n < 2^31, d >= 1: with s = ceil(log2 d) and m = ceil(2^(31 +
+// s) / d), the product n m exceeds 2^(31 + s) n / d by less than 2^(31 + s) / d.
+struct FastDiv {
+    uint32_t m;
+    int s;
+    FastDiv() = default;
+    __host__ explicit FastDiv(int d) : s(0) {
+        while ((1ll << s) < d) ++s;
+        m = uint32_t(((1ull << (31 + s)) + d - 1) / d);
+    }
+    __device__ __forceinline__ int operator()(int n) const { return int((uint64_t(uint32_t(n)) * m) >> (31 + s)); }
+};
+
 struct XaParams {
     CUtensorMap tm_q;  // 4D {d, Lq, heads, B}, box {64, 128, 1, 1}, 128B swizzle
     CUtensorMap tm_k;  // 4D {d, Lk, kv_heads, B}, box {64, 128, 1, 1}, 128B swizzle; codes: box {d, 128, 1, 1}, none
@@ -54,6 +67,7 @@ struct XaParams {
     int q_b, q_h, k_b, k_h, v_b, v_h;  // 1, or 0 along an axis that the tensor repeats (stride 0)
     int n_qpairs;                      // ceil(Lq / 256)
     int n_splits, n_units;
+    FastDiv by_splits, by_qpairs, by_heads, by_group;
     float scale_log2;
     unsigned long long wait_limit_ns;
     float *o_part;  // n_splits > 1: [n_splits][B * heads * Lq][d] unnormalised O
@@ -134,18 +148,22 @@ struct XaUnit {
 
 __device__ __forceinline__ XaUnit xa_unit(const XaParams &p, int unit) {
     XaUnit u;
-    u.split = unit % p.n_splits;
-    const int r = unit / p.n_splits;
-    const int bh = r / p.n_qpairs;
+    const int r = p.by_splits(unit);
+    u.split = unit - r * p.n_splits;
+    const int bh = p.by_qpairs(r);
     u.row0 = (r - bh * p.n_qpairs) * 256;
-    u.b = bh / p.heads;
+    u.b = p.by_heads(bh);
     u.h = bh - u.b * p.heads;
-    u.kvh = u.h / p.group;
+    u.kvh = p.by_group(u.h);
     u.nt = p.Lq - u.row0 > 128 ? 2 : 1;
     u.len = p.kv_lens ? min(max(__ldg(p.kv_lens + u.b), 0), p.Lk) : p.Lk;
-    const long long nblk = (u.len + 127) / 128;
-    u.jb = int(nblk * u.split / p.n_splits);
-    u.je = int(nblk * (u.split + 1) / p.n_splits);
+    const int nblk = (u.len + 127) / 128;  // < 2^24, and n_splits <= 64
+    u.jb = 0;
+    u.je = nblk;
+    if (p.n_splits > 1) {
+        u.jb = p.by_splits(nblk * u.split);
+        u.je = p.by_splits(nblk * (u.split + 1));
+    }
     return u;
 }
 
@@ -596,13 +614,13 @@ __device__ __forceinline__ void xa_load_scores(uint32_t t_s, const uint32_t (&w)
             for (int i = 0; i < 32; ++i) s[32 * c + i] = __uint_as_float(r[i]);
         }
     }
-    uint32_t all = 0xffffffffu;
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) all &= w[c];
-    if (all != 0xffffffffu) {
+    for (int c = 0; c < NCH; ++c) {
+        if (w[c] != 0xffffffffu) {
 #pragma unroll
-        for (int i = 0; i < 32 * NCH; ++i)
-            if (!(w[i >> 5] >> (i & 31) & 1u)) s[i] = -INFINITY;
+            for (int i = 0; i < 32; ++i)
+                if (!(w[c] >> i & 1u)) s[32 * c + i] = -INFINITY;
+        }
     }
 }
 
