@@ -604,8 +604,12 @@ constexpr int kMaxSmem = 227 * 1024;
 
 template <int D, bool F16>
 bool prepare_xs_kernel() {
-    return cudaFuncSetAttribute(npa::xa_short_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) ==
-           cudaSuccess;
+    using C = npa::XsCfg<D>;
+    void (*kernel)(npa::XsParams) = npa::xa_short_kernel<D, F16>;
+    cudaFuncAttributes attr;
+    if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess) return false;
+    if (C::kSplitRegs && attr.numRegs != (int)C::kRegsLaunch) return false;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) == cudaSuccess;
 }
 
 // ensure_ready plus the cross-attention kernels' limits, once per device.

@@ -6,14 +6,15 @@
 // heads x 65536 queries x 77 keys at d = 64). The kernel is built to keep many
 // query tiles moving: keys and values of a (batch, head) are loaded once and
 // stay in shared memory while the CTA walks that head's tiles, and NW
-// warpgroups work on tiles of their own, each with its own Q buffers, tensor
-// memory and barriers. A warpgroup's tile is one pass without a running
-// maximum: S = Q K^T, softmax of the whole row, O = P V. Its chain of waits is
-// long (about 4,000 cycles), but four chains overlap on a multiprocessor.
+// warpgroups work on tiles of their own, each with its own issuing warp, Q
+// buffers, tensor memory and barriers. A warpgroup's tile is one pass without a
+// running maximum: S = Q K^T, softmax of the whole row, O = P V. A tile's chain
+// of waits is long, but NW chains overlap on a multiprocessor.
 //
-// Warps: 4 * NW compute (NW = 4 at d = 64, 2 at d = 128), then one that loads
-// keys and values, clears unkept value rows and publishes which keys are kept.
-// The first thread of each warpgroup issues its loads, products and stores.
+// Warps: 4 * NW compute (NW = 4 at d = 64, 2 at d = 128), NW issuers (one
+// thread each: query loads, products, output stores), then one that loads keys
+// and values, clears unkept value rows and publishes which keys are kept. An
+// issuer starts the next tile's S before it stores this one's output.
 // TMEM per warpgroup: S in columns 0..127; P over S's first 64; O in 64..127
 // (d = 64, over S: every row of it has been read when P V starts) or 128..255.
 // O leaves through the tile's own Q buffer, which the S product has read.
@@ -31,7 +32,13 @@ struct XsCfg {
     static constexpr int kChunks = D / 64;
     static constexpr int kChunkBytes = 128 * 128;
     static constexpr int kTileBytes = kChunks * kChunkBytes;
-    static constexpr int kThreads = NW * 128 + 32;
+    // d = 64: six warpgroups (the issuers and the loader have one each), and
+    // the compute ones take the others' registers; d = 128: three.
+    static constexpr int kThreads = D == 64 ? 768 : 384;
+    static constexpr int kIssueWarp = NW * 4, kLoadWarp = D == 64 ? 20 : 10;
+    static constexpr bool kSplitRegs = D == 64;
+    static constexpr uint32_t kRegsLaunch = D == 64 ? 80 : 168, kRegsCompute = 104, kRegsOther = 32;
+    static_assert(!kSplitRegs || 128 * (4 * kRegsCompute + 2 * kRegsOther) <= kThreads * kRegsLaunch, "register split");
     static constexpr int kTmemCols = 512;
     static constexpr int kColsPerWg = 512 / NW;
     static constexpr int kColO = D == 64 ? 64 : 128;
@@ -142,15 +149,13 @@ __device__ void xs_loader(const XsParams &p, uint8_t *kv, uint64_t *bars, uint32
         if (issued > s) sm100::mbar_wait(&bars[C::bKVFull + s], ((issued - 1 - s) / p.kv_stages) & 1, lim);
 }
 
+// One thread per warpgroup: query loads, products and output stores of its tiles.
 template <int D, bool F16>
-__device__ void xs_compute(const XsParams &p, uint8_t *smem, uint8_t *kv, uint64_t *bars, const uint32_t *kept,
-                           uint32_t tmem0, volatile uint32_t *abort_flag, int wg) {
+__device__ void xs_issue(const XsParams &p, uint8_t *smem, uint8_t *kv, uint64_t *bars, const uint32_t *kept,
+                         uint32_t tmem0, volatile uint32_t *abort_flag, int wg) {
     using C = XsCfg<D>;
     const uint64_t lim = p.a.wait_limit_ns;
-    const int row = threadIdx.x & 127, warp = row >> 5;
-    const bool leader = row == 0;
     const uint32_t tmem = tmem0 + wg * C::kColsPerWg;
-    const uint32_t t_row = tmem + (uint32_t(warp) * 32u << 16);
     uint8_t *q0 = smem + wg * 2 * C::kTileBytes;
     const int stage_bytes = C::kv_stage_bytes(p.kv_rows), half = stage_bytes / 2, chunk = p.kv_rows * 128;
     const uint64_t q_desc = sm100::sdesc_sw128(sm100::smem_u32(q0), 16, 1024);
@@ -159,7 +164,7 @@ __device__ void xs_compute(const XsParams &p, uint8_t *smem, uint8_t *kv, uint64
     int t0, t1;
     xs_tiles(p, &t0, &t1);
     const int bh0 = p.by_qtiles(t0), last_seq = p.by_qtiles(t1 - 1) - bh0;
-    auto load_q = [&](int t, int buf) {  // leader
+    auto load_q = [&](int t, int buf) {
         const int bh = p.by_qtiles(t), b = p.a.by_heads(bh);
         const int qb = bound_coord(b, p.a.B), qh = bound_coord(bh - b * p.a.heads, p.a.heads);
         uint64_t *bar = &bars[C::bQFull + 2 * wg + buf];
@@ -169,110 +174,195 @@ __device__ void xs_compute(const XsParams &p, uint8_t *smem, uint8_t *kv, uint64
             sm100::tma_load_4d(q0 + buf * C::kTileBytes + c * C::kChunkBytes, &p.a.tm_q, bar, c * 64,
                                bound_coord((t - bh * p.n_qtiles) * 128, p.a.Lq), qh * p.a.q_h, qb * p.a.q_b);
     };
-    int issued = 0;  // Q tiles loaded so far
-    if (leader) {
-        if (wg == 0) sm100::tma_prefetch_desc(&p.a.tm_o);
-        for (int t = t0 + wg; t < t1 && issued < 2; t += C::NW, ++issued) load_q(t, issued);  // tiles 0 and 1
-    }
-    // the products of one tile; leader
-    auto issue_s = [&](int buf, int stage, int n) {
-        constexpr uint32_t kId0 =
-            F16 ? sm100::idesc_f16_f32(128, 0, false, false) : sm100::idesc_bf16_f32(128, 0, false, false);
-        const uint32_t id = kId0 | (uint32_t((n + 15) >> 4) << 18);
-        const uint64_t q = q_desc + uint64_t((buf * C::kTileBytes) >> 4), k = k_desc + uint64_t((stage * stage_bytes) >> 4);
+    auto store_o = [&](int t, int buf) {
+        const int bh = p.by_qtiles(t), b = p.a.by_heads(bh);
+        const int ob = bound_coord(b, p.a.B), oh = bound_coord(bh - b * p.a.heads, p.a.heads);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-            sm100::mma_ss(tmem, q + uint64_t(((kk >> 2) * C::kChunkBytes + (kk & 3) * 32) >> 4),
-                          k + uint64_t(((kk >> 2) * chunk + (kk & 3) * 32) >> 4), id, kk > 0 ? 1u : 0u);
-        sm100::tc_commit(&bars[C::bS + wg]);
+        for (int c = 0; c < C::kChunks; ++c)
+            sm100::tma_store_4d(&p.a.tm_o, q0 + buf * C::kTileBytes + c * C::kChunkBytes, c * 64,
+                                bound_coord((t - bh * p.n_qtiles) * 128, p.a.Lq), oh, ob);
+        sm100::bulk_commit();
     };
-    int seq = -1;  // key/value set in use, counted from the CTA's first
-    int i = 0, m = 0;  // tiles done; tiles with keys done
+    int loaded = 0;  // Q tiles asked for
+    for (int t = t0 + wg; t < t1 && loaded < 2; t += C::NW, ++loaded) load_q(t, loaded);
+    if (wg == 0) sm100::tma_prefetch_desc(&p.a.tm_o);
+    int seq = -1;      // key/value set in use, counted from the CTA's first
+    int i = 0, m = 0;  // tiles begun; tiles with keys begun
     bool ok = true;
-    // moves on to set `to`, releasing the ones before it
+    // moves on to key/value set `to`, releasing the ones before it
     auto advance = [&](int to) {
         while (ok && seq < to) {
-            if (seq >= 0 && leader) sm100::mbar_arrive(&bars[C::bKVEmpty + seq % p.kv_stages]);
+            if (seq >= 0) sm100::mbar_arrive(&bars[C::bKVEmpty + seq % p.kv_stages]);
             ++seq;
-            ok = warp_wait(&bars[C::bKVReady + seq % p.kv_stages], (seq / p.kv_stages) & 1, lim);
+            ok = sm100::mbar_wait(&bars[C::bKVReady + seq % p.kv_stages], (seq / p.kv_stages) & 1, lim);
         }
     };
-    for (int t = t0 + wg; t < t1; t += C::NW, ++i) {
-        const int bh = p.by_qtiles(t), b = p.a.by_heads(bh);
-        const int row0 = (t - bh * p.n_qtiles) * 128;
-        const int buf = i & 1;
-        advance(bh - bh0);
-        ok = ok && !*abort_flag && warp_wait(&bars[C::bQFull + 2 * wg + buf], (i >> 1) & 1, lim);
-        if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-        }
-        const int stage = seq % p.kv_stages;
-        const int n = int(kept[stage * 8 + 4]);
-        const bool active = row0 + warp * 32 < p.a.Lq && n > 0;  // some row of this warp is a query with keys
-        uint8_t *tile = q0 + buf * C::kTileBytes;
-        float l = 0.f;
-        if (n > 0) {
-            if (leader) {
+    for (int t = t0 + wg;; t += C::NW, ++i) {
+        // the previous tile's output is staged: its tensor memory is free
+        if (i > 0) ok = ok && sm100::mbar_wait(&bars[C::bE + wg], (i - 1) & 1, lim);
+        ok = ok && !*abort_flag;
+        if (!ok) break;
+        const bool more = t < t1;
+        int n = 0, stage = 0;
+        if (more) {
+            advance(p.by_qtiles(t) - bh0);
+            ok = ok && sm100::mbar_wait(&bars[C::bQFull + 2 * wg + (i & 1)], (i >> 1) & 1, lim);
+            if (!ok) break;
+            stage = seq % p.kv_stages;
+            n = int(kept[stage * 8 + 4]);
+            if (n > 0) {
+                constexpr uint32_t kId0 =
+                    F16 ? sm100::idesc_f16_f32(128, 0, false, false) : sm100::idesc_bf16_f32(128, 0, false, false);
+                const uint32_t id = kId0 | (uint32_t((n + 15) >> 4) << 18);
+                const uint64_t q = q_desc + uint64_t(((i & 1) * C::kTileBytes) >> 4);
+                const uint64_t k = k_desc + uint64_t((stage * stage_bytes) >> 4);
                 sm100::tc_fence_after();
-                issue_s(buf, stage, n);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    sm100::mma_ss(tmem, q + uint64_t(((kk >> 2) * C::kChunkBytes + (kk & 3) * 32) >> 4),
+                                  k + uint64_t(((kk >> 2) * chunk + (kk & 3) * 32) >> 4), id, kk > 0 ? 1u : 0u);
+                sm100::tc_commit(&bars[C::bS + wg]);
             }
         }
-        // the next tile goes into the buffer that the previous one's output
-        // has left by now
-        if (leader && i > 0 && t + C::NW < t1) {
-            sm100::bulk_wait_read();
-            load_q(t + C::NW, buf ^ 1);
-            ++issued;
+        if (i > 0) {
+            store_o(t - C::NW, (i - 1) & 1);
+            if (t + C::NW < t1) {  // the tile after next, into the buffer that this store has read
+                sm100::bulk_wait_read();
+                load_q(t + C::NW, (i - 1) & 1);
+                ++loaded;
+            }
         }
+        if (!more) break;
+        if (n > 0) {
+            ok = sm100::mbar_wait(&bars[C::bP + wg], m & 1, lim);
+            if (!ok) break;
+            sm100::tc_fence_after();
+            constexpr uint32_t kId =
+                F16 ? sm100::idesc_f16_f32(128, D, false, true) : sm100::idesc_bf16_f32(128, D, false, true);
+            const uint64_t v = v_desc + uint64_t((stage * stage_bytes) >> 4);
+            const int steps = (n + 15) >> 4;
+            for (int kk = 0; kk < steps; ++kk)
+                sm100::mma_ts(tmem + C::kColO, tmem + kk * 8, v + uint64_t((kk * 2048) >> 4), kId, kk > 0 ? 1u : 0u);
+            sm100::tc_commit(&bars[C::bO + wg]);
+            ++m;
+        }
+    }
+    advance(last_seq);
+    if (!ok) {
+        record_error(kErrDeviceTimeout);
+        *abort_flag = 1;
+    }
+    // products and copies in flight end, stores complete
+    sm100::tc_commit(&bars[C::bDrain + wg]);
+    sm100::mbar_wait(&bars[C::bDrain + wg], 0, lim);
+    for (int k = i; k < loaded; ++k) sm100::mbar_wait(&bars[C::bQFull + 2 * wg + (k & 1)], (k >> 1) & 1, lim);
+    sm100::bulk_wait_all();
+}
+
+// W scores of a row from TMEM, unkept ones as -inf.
+template <int W>
+__device__ __forceinline__ void xs_scores(uint32_t t_s, uint32_t keep, float (&s)[W]) {
+    uint32_t r[W];
+    if constexpr (W == 32)
+        sm100::tmem_ld32(t_s, r);
+    else
+        sm100::tmem_ld16(t_s, r);
+#pragma unroll
+    for (int i = 0; i < W; ++i) s[i] = __uint_as_float(r[i]);
+    if ((keep | (W == 32 ? 0u : 0xffff0000u)) != 0xffffffffu) {
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            if (!(keep >> i & 1u)) s[i] = -INFINITY;
+    }
+}
+
+template <int W>
+__device__ __forceinline__ float xs_max(const float (&s)[W]) {
+    float m[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+    for (int i = 4; i + 4 < W; i += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = sm100::max3(m[k], s[i + k], s[i + 4 + k]);
+    if (W % 8 == 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = fmaxf(m[k], s[W - 4 + k]);
+    }
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+template <int D, bool F16>
+__device__ void xs_compute(const XsParams &p, uint8_t *smem, uint64_t *bars, const uint32_t *kept, uint32_t tmem0,
+                           volatile uint32_t *abort_flag, int wg) {
+    using C = XsCfg<D>;
+    const uint64_t lim = p.a.wait_limit_ns;
+    const int row = threadIdx.x & 127, warp = row >> 5;
+    const uint32_t t_row = tmem0 + wg * C::kColsPerWg + (uint32_t(warp) * 32u << 16);
+    const float c2 = p.a.scale_log2;
+    int t0, t1;
+    xs_tiles(p, &t0, &t1);
+    const int bh0 = p.by_qtiles(t0);
+    int seq = -1, i = 0, m = 0;  // as in xs_issue
+    bool ok = true;
+    for (int t = t0 + wg; t < t1; t += C::NW, ++i) {
+        const int bh = p.by_qtiles(t);
+        const int row0 = (t - bh * p.n_qtiles) * 128;
+        if (seq != bh - bh0) {  // this set is not released before the tile is done; the ones between may be gone
+            seq = bh - bh0;
+            ok = warp_wait(&bars[C::bKVReady + seq % p.kv_stages], (seq / p.kv_stages) & 1, lim);
+            if (!ok) break;
+        }
+        const uint32_t *keep = kept + seq % p.kv_stages * 8;
+        const int n = int(keep[4]);
+        const bool active = row0 + warp * 32 < p.a.Lq && n > 0;  // some row of this warp is a query with keys
+        float l = 0.f;
         if (n > 0) {
             ok = warp_wait(&bars[C::bS + wg], m & 1, lim);
             if (!ok) break;
             sm100::tc_fence_after();
             if (active) {
-                const int chunks = (n + 31) >> 5;
+                // whole 32-key pieces, then the rest as one of 16 or 32
+                const int rest = n & 31, pieces = (n >> 5) + (rest > 16);
+                const bool half = rest > 0 && rest <= 16;
                 float mx = -INFINITY;
 #pragma unroll 1
-                for (int c = 0; c < chunks; ++c) {
-                    const uint32_t w[4] = {kept[stage * 8 + c], 0, 0, 0};
+                for (int c = 0; c < pieces; ++c) {
                     float s[32];
-                    xa_load_scores<1>(t_row + 32 * c, w, s);
-                    mx = fmaxf(mx, row_max<32>(s));
+                    xs_scores<32>(t_row + 32 * c, keep[c], s);
+                    mx = fmaxf(mx, xs_max<32>(s));
+                }
+                float tail[16];
+                if (half) {
+                    xs_scores<16>(t_row + 32 * pieces, keep[pieces], tail);
+                    mx = fmaxf(mx, xs_max<16>(tail));
                 }
                 // f16 keeps its probabilities 2^7 higher, as in XaSoftmax
-                const float ref = mx * p.a.scale_log2 - (F16 ? 7.f : 0.f);
+                const float ref = mx * c2 - (F16 ? 7.f : 0.f);
 #pragma unroll 1
-                for (int c = 0; c < chunks; ++c) {
-                    const uint32_t w[4] = {kept[stage * 8 + c], 0, 0, 0};
+                for (int c = 0; c < pieces; ++c) {
                     float s[32];
-                    xa_load_scores<1>(t_row + 32 * c, w, s);
+                    xs_scores<32>(t_row + 32 * c, keep[c], s);
                     uint32_t pk[16];
-                    l += exp_block<32, F16>(s, p.a.scale_log2, ref, pk);
+                    l += exp_block<32, F16>(s, c2, ref, pk);
                     sm100::tmem_st16(t_row + 16 * c, pk);
+                }
+                if (half) {
+                    uint32_t pk[8];
+                    l += exp_block<16, F16>(tail, c2, ref, pk);
+                    sm100::tmem_st8(t_row + 16 * pieces, pk);
                 }
             }
             sm100::tc_fence_before();
             sm100::mbar_arrive(&bars[C::bP + wg]);
-            if (leader) {
-                ok = sm100::mbar_wait(&bars[C::bP + wg], m & 1, lim);
-                if (ok) {
-                    sm100::tc_fence_after();
-                    constexpr uint32_t kId =
-                        F16 ? sm100::idesc_f16_f32(128, D, false, true) : sm100::idesc_bf16_f32(128, D, false, true);
-                    const uint64_t v = v_desc + uint64_t((stage * stage_bytes) >> 4);
-                    const int steps = (n + 15) >> 4;
-                    for (int kk = 0; kk < steps; ++kk)
-                        sm100::mma_ts(tmem + C::kColO, tmem + kk * 8, v + uint64_t((kk * 2048) >> 4), kId,
-                                      kk > 0 ? 1u : 0u);
-                    sm100::tc_commit(&bars[C::bO + wg]);
-                }
-            }
-            ok = warp_wait(&bars[C::bO + wg], m & 1, lim) && __all_sync(0xffffffffu, ok);
+            ok = warp_wait(&bars[C::bO + wg], m & 1, lim);
             if (!ok) break;
             sm100::tc_fence_after();
             ++m;
+        } else {  // the Q tile must have landed before zeros go there
+            ok = warp_wait(&bars[C::bQFull + 2 * wg + (i & 1)], (i >> 1) & 1, lim);
+            if (!ok) break;
         }
-        // O / l into the tile's Q buffer (the S product has read it), out by TMA
+        // O / l into the tile's Q buffer (the S product has read it)
+        uint8_t *tile = smem + (wg * 2 + (i & 1)) * C::kTileBytes;
         const float inv_l = l > 0.f ? 1.f / l : l;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
@@ -293,30 +383,10 @@ __device__ void xs_compute(const XsParams &p, uint8_t *smem, uint8_t *kv, uint64
         sm100::tc_fence_before();
         sm100::fence_proxy_async();
         sm100::mbar_arrive(&bars[C::bE + wg]);
-        if (leader) {
-            ok = sm100::mbar_wait(&bars[C::bE + wg], i & 1, lim);
-            if (ok) {
-                const int ob = bound_coord(b, p.a.B), oh = bound_coord(bh - b * p.a.heads, p.a.heads);
-#pragma unroll
-                for (int c = 0; c < C::kChunks; ++c)
-                    sm100::tma_store_4d(&p.a.tm_o, tile + c * C::kChunkBytes, c * 64, bound_coord(row0, p.a.Lq), oh, ob);
-                sm100::bulk_commit();
-            }
-        }
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
     }
-    advance(last_seq);
     if (!ok) {
         record_error(kErrDeviceTimeout);
         *abort_flag = 1;
-    }
-    if (leader) {
-        // products and copies in flight end, stores complete
-        sm100::tc_commit(&bars[C::bDrain + wg]);
-        sm100::mbar_wait(&bars[C::bDrain + wg], 0, lim);
-        for (int k = i; k < issued; ++k) sm100::mbar_wait(&bars[C::bQFull + 2 * wg + (k & 1)], (k >> 1) & 1, lim);
-        sm100::bulk_wait_all();
     }
 }
 
@@ -349,7 +419,7 @@ __global__ void __launch_bounds__(XsCfg<D>::kThreads, 1) xa_short_kernel(const _
         misc[1] = 0;
         sm100::fence_barrier_init();
     }
-    if (warp == C::NW * 4) {
+    if (warp == C::kLoadWarp) {
         sm100::tmem_alloc(&misc[0], C::kTmemCols);
         sm100::tmem_relinquish();
     }
@@ -358,14 +428,20 @@ __global__ void __launch_bounds__(XsCfg<D>::kThreads, 1) xa_short_kernel(const _
     sm100::tc_fence_after();
     const uint32_t tmem = misc[0];
     volatile uint32_t *abort_flag = &misc[1];
-    if (warp == C::NW * 4)
-        xs_loader<D>(p, kv, bars, kept, abort_flag);
-    else
-        xs_compute<D, F16>(p, smem, kv, bars, kept, tmem, abort_flag, warp >> 2);
+    if (warp >= C::kIssueWarp) {
+        if constexpr (C::kSplitRegs) sm100::setmaxnreg_dec<C::kRegsOther>();
+        if (warp == C::kLoadWarp)
+            xs_loader<D>(p, kv, bars, kept, abort_flag);
+        else if (warp < C::kIssueWarp + C::NW && (threadIdx.x & 31) == 0)
+            xs_issue<D, F16>(p, smem, kv, bars, kept, tmem, abort_flag, warp - C::kIssueWarp);
+    } else {
+        if constexpr (C::kSplitRegs) sm100::setmaxnreg_inc<C::kRegsCompute>();
+        xs_compute<D, F16>(p, smem, bars, kept, tmem, abort_flag, warp >> 2);
+    }
     sm100::tc_fence_before();
     __syncthreads();
     sm100::tc_fence_after();
-    if (warp == C::NW * 4) {
+    if (warp == C::kLoadWarp) {
         __syncwarp();
         sm100::tmem_dealloc(tmem, C::kTmemCols);
     }
