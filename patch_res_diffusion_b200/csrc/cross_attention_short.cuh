@@ -197,32 +197,35 @@ __device__ void xs_issue(const XsParams &p, uint8_t *smem, uint8_t *kv, uint64_t
             ok = sm100::mbar_wait(&bars[C::bKVReady + seq % p.kv_stages], (seq / p.kv_stages) & 1, lim);
         }
     };
+    constexpr uint32_t kIdS0 =
+        F16 ? sm100::idesc_f16_f32(128, 0, false, false) : sm100::idesc_bf16_f32(128, 0, false, false);
+    constexpr uint32_t kIdO =
+        F16 ? sm100::idesc_f16_f32(128, D, false, true) : sm100::idesc_bf16_f32(128, D, false, true);
     for (int t = t0 + wg;; t += C::NW, ++i) {
+        const bool more = t < t1;
+        const int set = more ? p.by_qtiles(t) - bh0 : seq;
+        const uint64_t q = q_desc + uint64_t(((i & 1) * C::kTileBytes) >> 4);
+        if (more) ok = ok && sm100::mbar_wait(&bars[C::bQFull + 2 * wg + (i & 1)], (i >> 1) & 1, lim);
         // the previous tile's output is staged: its tensor memory is free
         if (i > 0) ok = ok && sm100::mbar_wait(&bars[C::bE + wg], (i - 1) & 1, lim);
-        ok = ok && !*abort_flag;
+        if (!ok || *abort_flag) {
+            ok = false;
+            break;
+        }
+        if (set != seq) advance(set);
         if (!ok) break;
-        const bool more = t < t1;
-        int n = 0, stage = 0;
-        if (more) {
-            advance(p.by_qtiles(t) - bh0);
-            ok = ok && sm100::mbar_wait(&bars[C::bQFull + 2 * wg + (i & 1)], (i >> 1) & 1, lim);
-            if (!ok) break;
-            stage = seq % p.kv_stages;
-            n = int(kept[stage * 8 + 4]);
-            if (n > 0) {
-                constexpr uint32_t kId0 =
-                    F16 ? sm100::idesc_f16_f32(128, 0, false, false) : sm100::idesc_bf16_f32(128, 0, false, false);
-                const uint32_t id = kId0 | (uint32_t((n + 15) >> 4) << 18);
-                const uint64_t q = q_desc + uint64_t(((i & 1) * C::kTileBytes) >> 4);
-                const uint64_t k = k_desc + uint64_t((stage * stage_bytes) >> 4);
-                sm100::tc_fence_after();
+        const int stage = seq % p.kv_stages;
+        const int n = more ? int(kept[stage * 8 + 4]) : 0;
+        const uint64_t v = v_desc + uint64_t((stage * stage_bytes) >> 4);
+        if (n > 0) {
+            const uint32_t id = kIdS0 | (uint32_t((n + 15) >> 4) << 18);
+            const uint64_t k = k_desc + uint64_t((stage * stage_bytes) >> 4);
+            sm100::tc_fence_after();
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    sm100::mma_ss(tmem, q + uint64_t(((kk >> 2) * C::kChunkBytes + (kk & 3) * 32) >> 4),
-                                  k + uint64_t(((kk >> 2) * chunk + (kk & 3) * 32) >> 4), id, kk > 0 ? 1u : 0u);
-                sm100::tc_commit(&bars[C::bS + wg]);
-            }
+            for (int kk = 0; kk < D / 16; ++kk)
+                sm100::mma_ss(tmem, q + uint64_t(((kk >> 2) * C::kChunkBytes + (kk & 3) * 32) >> 4),
+                              k + uint64_t(((kk >> 2) * chunk + (kk & 3) * 32) >> 4), id, kk > 0 ? 1u : 0u);
+            sm100::tc_commit(&bars[C::bS + wg]);
         }
         if (i > 0) {
             store_o(t - C::NW, (i - 1) & 1);
@@ -237,12 +240,11 @@ __device__ void xs_issue(const XsParams &p, uint8_t *smem, uint8_t *kv, uint64_t
             ok = sm100::mbar_wait(&bars[C::bP + wg], m & 1, lim);
             if (!ok) break;
             sm100::tc_fence_after();
-            constexpr uint32_t kId =
-                F16 ? sm100::idesc_f16_f32(128, D, false, true) : sm100::idesc_bf16_f32(128, D, false, true);
-            const uint64_t v = v_desc + uint64_t((stage * stage_bytes) >> 4);
             const int steps = (n + 15) >> 4;
-            for (int kk = 0; kk < steps; ++kk)
-                sm100::mma_ts(tmem + C::kColO, tmem + kk * 8, v + uint64_t((kk * 2048) >> 4), kId, kk > 0 ? 1u : 0u);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+                if (kk < steps)
+                    sm100::mma_ts(tmem + C::kColO, tmem + kk * 8, v + uint64_t((kk * 2048) >> 4), kIdO, kk > 0 ? 1u : 0u);
             sm100::tc_commit(&bars[C::bO + wg]);
             ++m;
         }
@@ -361,24 +363,36 @@ __device__ void xs_compute(const XsParams &p, uint8_t *smem, uint64_t *bars, con
             ok = warp_wait(&bars[C::bQFull + 2 * wg + (i & 1)], (i >> 1) & 1, lim);
             if (!ok) break;
         }
-        // O / l into the tile's Q buffer (the S product has read it)
-        uint8_t *tile = smem + (wg * 2 + (i & 1)) * C::kTileBytes;
-        const float inv_l = l > 0.f ? 1.f / l : l;
+        // O / l into the tile's Q buffer (the S product has read it); without
+        // a kept key O is 0, without any key nothing was computed
+        uint8_t *dst = smem + (wg * 2 + (i & 1)) * C::kTileBytes + row * 128;
+        if (active) {
+            const float inv = l > 0.f ? 1.f / l : l;
+            const uint64_t inv2 = sm100::pack_f32x2(inv, inv);
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            if (active) sm100::tmem_ld32(t_row + C::kColO + c * 32, o);
-            uint8_t *dst = tile + (c >> 1) * C::kChunkBytes + row * 128;
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                sm100::tmem_ld32(t_row + C::kColO + c * 32, o);
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                uint32_t h[4];
+                for (int v = 0; v < 4; ++v) {
+                    uint32_t h[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    h[j] = active && l != 0.f ? sm100::pack_16x2<F16>(__uint_as_float(o[8 * v + 2 * j]) * inv_l,
-                                                                      __uint_as_float(o[8 * v + 2 * j + 1]) * inv_l)
-                                              : 0u;
-                *reinterpret_cast<uint4 *>(dst + ((((c & 1) * 4 + v) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                    for (int j = 0; j < 4; ++j) {
+                        float x, y;
+                        sm100::unpack_f32x2(sm100::fma_f32x2(sm100::pack_f32x2(__uint_as_float(o[8 * v + 2 * j]),
+                                                                               __uint_as_float(o[8 * v + 2 * j + 1])),
+                                                             inv2, 0),
+                                            x, y);
+                        h[j] = sm100::pack_16x2<F16>(x, y);
+                    }
+                    *reinterpret_cast<uint4 *>(dst + (c >> 1) * C::kChunkBytes + ((((c & 1) * 4 + v) ^ (row & 7)) << 4)) =
+                        make_uint4(h[0], h[1], h[2], h[3]);
+                }
             }
+        } else if (n <= 0) {
+#pragma unroll
+            for (int v = 0; v < 8 * C::kChunks; ++v)
+                *reinterpret_cast<uint4 *>(dst + (v >> 3) * C::kChunkBytes + (v & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
         sm100::tc_fence_before();
         sm100::fence_proxy_async();
