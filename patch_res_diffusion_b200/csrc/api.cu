@@ -15,6 +15,7 @@
 #include "npa.h"
 #include "asg_combine.cuh"
 #include "cross_attention.cuh"
+#include "cross_attention_few.cuh"
 #include "cross_attention_short.cuh"
 #include "group_norm.cuh"
 #include "kv8_store.cuh"
@@ -714,6 +715,20 @@ int plan_xa_splits(long long base_units, long long n_blocks, int sm_count) {
     return best;
 }
 
+// The same for xa_few_kernel: about four CTAs for every multiprocessor, each
+// with two steps or more for every warp.
+int plan_xf_splits(long long units, int Lk, int sm_count) {
+    const long long want = (4LL * sm_count + units - 1) / units, most = ((long long)Lk + 255) / 256;
+    return (int)std::max(1LL, std::min({want, most, (long long)npa::kXaMaxSplits}));
+}
+
+// The planned split count of a call, whichever kernel runs it.
+int plan_splits(int B, int heads, int kv_heads, int Lq, int Lk, int sm_count) {
+    if ((long long)(heads / kv_heads) * Lq <= npa::kXaFewRows)
+        return plan_xf_splits((long long)B * kv_heads, Lk, sm_count);
+    return plan_xa_splits((long long)B * heads * ((Lq + 255) / 256), ((long long)Lk + 127) / 128, sm_count);
+}
+
 size_t xa_split_bytes(int B, int heads, int Lq, int d) { return (size_t)B * heads * Lq * (d + 2) * sizeof(float); }
 
 struct XaCall {
@@ -780,6 +795,55 @@ npa_status launch_xs_kernel(const XaCall &c, const npa::XaParams &a, int sm_coun
                : NPA_ERR_CUDA;
 }
 
+npa_status launch_combine(const XaCall &c, const npa::XaParams &a, npa_stream_t stream) {
+    const int d = c.q.d;
+    const long long rows = (long long)a.B * a.heads * a.Lq;
+    npa::XaCombineParams cp{a.o_part, a.ml, const_cast<void *>(c.o.ptr), c.o.sb, c.o.sh, c.o.st, a.n_splits,
+                            (int)rows, a.heads, a.Lq};
+    void *args[1] = {&cp};
+    const void *kernel = d == 64 ? (c.f16 ? (const void *)npa::xa_combine_kernel<64, true>
+                                          : (const void *)npa::xa_combine_kernel<64, false>)
+                                 : (c.f16 ? (const void *)npa::xa_combine_kernel<128, true>
+                                          : (const void *)npa::xa_combine_kernel<128, false>);
+    return cudaLaunchKernel(kernel, dim3((unsigned)((rows + 7) / 8)), dim3(256), args, 0, (cudaStream_t)stream) ==
+                   cudaSuccess
+               ? NPA_OK
+               : NPA_ERR_CUDA;
+}
+
+template <int D, bool KV8, bool F16>
+npa_status launch_xf_kernel(const XaCall &c, const npa::XaParams &a, npa_stream_t stream) {
+    npa::XfParams prm;
+    std::memset(&prm, 0, sizeof(prm));
+    prm.q = c.q.ptr;
+    prm.k = c.k.ptr;
+    prm.v = c.v.ptr;
+    prm.o = const_cast<void *>(c.o.ptr);
+    prm.qsb = c.q.sb, prm.qsh = c.q.sh, prm.qst = c.q.st;
+    prm.ksb = c.k.sb, prm.ksh = c.k.sh, prm.kst = c.k.st;
+    prm.vsb = c.v.sb, prm.vsh = c.v.sh, prm.vst = c.v.st;
+    prm.osb = c.o.sb, prm.osh = c.o.sh, prm.ost = c.o.st;
+    prm.kv_lens = a.kv_lens;
+    prm.key_mask = a.key_mask;
+    prm.k_scale = a.k_scale;
+    prm.v_scale = a.v_scale;
+    prm.scale_blocks = a.scale_blocks;
+    prm.B = a.B, prm.heads = a.heads, prm.kv_heads = a.kv_heads, prm.group = a.group, prm.Lq = a.Lq, prm.Lk = a.Lk;
+    prm.n_splits = a.n_splits;
+    prm.scale_log2 = a.scale_log2;
+    prm.o_part = a.o_part;
+    prm.ml = a.ml;
+    const int tiles = a.group * a.Lq > 8 ? 2 : 1;
+    const unsigned smem = npa::kXaFewWarps * 8 * tiles * (D + 2) * sizeof(float);
+    const void *kernel = tiles == 2 ? (const void *)npa::xa_few_kernel<D, KV8, F16, 2>
+                                    : (const void *)npa::xa_few_kernel<D, KV8, F16, 1>;
+    void *args[1] = {&prm};
+    return cudaLaunchKernel(kernel, dim3((unsigned)(a.B * a.kv_heads * a.n_splits)), dim3(32 * npa::kXaFewWarps), args,
+                            smem, (cudaStream_t)stream) == cudaSuccess
+               ? NPA_OK
+               : NPA_ERR_CUDA;
+}
+
 npa_status launch_xa(const XaCall &c, npa_stream_t stream) {
     int sm_count = 0;
     const npa_status st = ensure_xa_ready(&sm_count);
@@ -810,7 +874,7 @@ npa_status launch_xa(const XaCall &c, npa_stream_t stream) {
     prm.wait_limit_ns = kWaitLimitNs;
     const long long base = (long long)B * heads * prm.n_qpairs;
     // as many splits as planned and as the workspace holds (one needs none)
-    int splits = plan_xa_splits(base, ((long long)Lk + 127) / 128, sm_count);
+    int splits = plan_splits(B, heads, c.k.heads, Lq, Lk, sm_count);
     const size_t per_split = xa_split_bytes(B, heads, Lq, d);
     const size_t held = c.workspace ? c.workspace_bytes / per_split : 1;
     if ((size_t)splits > held) splits = (int)held;
@@ -827,6 +891,19 @@ npa_status launch_xa(const XaCall &c, npa_stream_t stream) {
     prm.by_heads = npa::FastDiv(heads);
     prm.by_group = npa::FastDiv(prm.group);
     const bool kv8 = c.k_scale != nullptr;
+    if ((long long)prm.group * Lq <= npa::kXaFewRows) {
+        npa_status s;
+        if (kv8)
+            s = d == 64 ? launch_xf_kernel<64, true, false>(c, prm, stream)
+                        : launch_xf_kernel<128, true, false>(c, prm, stream);
+        else if (d == 64)
+            s = c.f16 ? launch_xf_kernel<64, false, true>(c, prm, stream)
+                      : launch_xf_kernel<64, false, false>(c, prm, stream);
+        else
+            s = c.f16 ? launch_xf_kernel<128, false, true>(c, prm, stream)
+                      : launch_xf_kernel<128, false, false>(c, prm, stream);
+        return s != NPA_OK || splits == 1 ? s : launch_combine(c, prm, stream);
+    }
     if (!encode_view(&prm.tm_q, c.q, c.f16) || !encode_view(&prm.tm_o, c.o, c.f16)) return NPA_ERR_CUDA;
     if (!kv8 && Lk <= npa::kXaShortKeys)
         return d == 64 ? (c.f16 ? launch_xs_kernel<64, true>(c, prm, sm_count, stream)
@@ -856,19 +933,7 @@ npa_status launch_xa(const XaCall &c, npa_stream_t stream) {
     void *args[1] = {&prm};
     if (cudaLaunchKernel(kernel, dim3(grid), dim3(threads), args, smem, (cudaStream_t)stream) != cudaSuccess)
         return NPA_ERR_CUDA;
-    if (splits > 1) {
-        npa::XaCombineParams cp{prm.o_part, prm.ml, const_cast<void *>(c.o.ptr), c.o.sb, c.o.sh, c.o.st, splits,
-                                (int)rows, heads, Lq};
-        void *cargs[1] = {&cp};
-        const void *ck = d == 64 ? (c.f16 ? (const void *)npa::xa_combine_kernel<64, true>
-                                          : (const void *)npa::xa_combine_kernel<64, false>)
-                                 : (c.f16 ? (const void *)npa::xa_combine_kernel<128, true>
-                                          : (const void *)npa::xa_combine_kernel<128, false>);
-        if (cudaLaunchKernel(ck, dim3((unsigned)((rows + 7) / 8)), dim3(256), cargs, 0, (cudaStream_t)stream) !=
-            cudaSuccess)
-            return NPA_ERR_CUDA;
-    }
-    return NPA_OK;
+    return splits > 1 ? launch_combine(c, prm, stream) : NPA_OK;
 }
 
 // A cache's own arguments.
@@ -1252,7 +1317,7 @@ size_t npa_cross_attention_workspace_size(int B, int heads, int kv_heads, int Lq
     int dev = 0, sm = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return 0;
-    const int s = plan_xa_splits((long long)B * heads * ((Lq + 255) / 256), ((long long)Lk + 127) / 128, sm);
+    const int s = plan_splits(B, heads, kv_heads, Lq, Lk, sm);
     return s > 1 ? (size_t)s * xa_split_bytes(B, heads, Lq, d) : 0;
 }
 
