@@ -715,17 +715,18 @@ int plan_xa_splits(long long base_units, long long n_blocks, int sm_count) {
     return best;
 }
 
-// The same for xa_few_kernel: about four CTAs for every multiprocessor, each
-// with two steps or more for every warp.
-int plan_xf_splits(long long units, int Lk, int sm_count) {
-    const long long want = (4LL * sm_count + units - 1) / units, most = ((long long)Lk + 255) / 256;
+// The same for xa_few_kernel: as many CTAs as run at once, each with two steps
+// or more for every warp.
+int plan_xf_splits(long long units, int rows, int Lk, int d, int sm_count) {
+    const long long want = (long long)npa::xa_few_per_sm(d, rows > 8 ? 2 : 1) * sm_count / units;
+    const long long most = ((long long)Lk + 255) / 256;
     return (int)std::max(1LL, std::min({want, most, (long long)npa::kXaMaxSplits}));
 }
 
 // The planned split count of a call, whichever kernel runs it.
-int plan_splits(int B, int heads, int kv_heads, int Lq, int Lk, int sm_count) {
-    if ((long long)(heads / kv_heads) * Lq <= npa::kXaFewRows)
-        return plan_xf_splits((long long)B * kv_heads, Lk, sm_count);
+int plan_splits(int B, int heads, int kv_heads, int Lq, int Lk, int d, int sm_count) {
+    const long long rows = (long long)(heads / kv_heads) * Lq;
+    if (rows <= npa::kXaFewRows) return plan_xf_splits((long long)B * kv_heads, (int)rows, Lk, d, sm_count);
     return plan_xa_splits((long long)B * heads * ((Lq + 255) / 256), ((long long)Lk + 127) / 128, sm_count);
 }
 
@@ -805,10 +806,18 @@ npa_status launch_combine(const XaCall &c, const npa::XaParams &a, npa_stream_t 
                                           : (const void *)npa::xa_combine_kernel<64, false>)
                                  : (c.f16 ? (const void *)npa::xa_combine_kernel<128, true>
                                           : (const void *)npa::xa_combine_kernel<128, false>);
-    return cudaLaunchKernel(kernel, dim3((unsigned)((rows + 7) / 8)), dim3(256), args, 0, (cudaStream_t)stream) ==
-                   cudaSuccess
-               ? NPA_OK
-               : NPA_ERR_CUDA;
+    // it may start under the attention kernel's end, and waits there
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3((unsigned)((rows + 3) / 4));
+    cfg.blockDim = dim3(128);
+    cfg.stream = (cudaStream_t)stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, kernel, args) == cudaSuccess ? NPA_OK : NPA_ERR_CUDA;
 }
 
 template <int D, bool KV8, bool F16>
@@ -874,7 +883,7 @@ npa_status launch_xa(const XaCall &c, npa_stream_t stream) {
     prm.wait_limit_ns = kWaitLimitNs;
     const long long base = (long long)B * heads * prm.n_qpairs;
     // as many splits as planned and as the workspace holds (one needs none)
-    int splits = plan_splits(B, heads, c.k.heads, Lq, Lk, sm_count);
+    int splits = plan_splits(B, heads, c.k.heads, Lq, Lk, d, sm_count);
     const size_t per_split = xa_split_bytes(B, heads, Lq, d);
     const size_t held = c.workspace ? c.workspace_bytes / per_split : 1;
     if ((size_t)splits > held) splits = (int)held;
@@ -1317,7 +1326,7 @@ size_t npa_cross_attention_workspace_size(int B, int heads, int kv_heads, int Lq
     int dev = 0, sm = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return 0;
-    const int s = plan_splits(B, heads, kv_heads, Lq, Lk, sm);
+    const int s = plan_splits(B, heads, kv_heads, Lq, Lk, d, sm);
     return s > 1 ? (size_t)s * xa_split_bytes(B, heads, Lq, d) : 0;
 }
 

@@ -19,9 +19,18 @@
 //          warp 9 issues both
 //   11     16-bit keys: clears the value rows of keys that are not kept
 //          (0 * NaN would reach the sums through the product otherwise)
-//   12-15  8-bit cache: converts code blocks to bf16 tiles in shared memory
+//   12-15  8-bit cache: converts code blocks to f16 tiles in shared memory
 // TMEM, the aliasing of P at d = 128, the lazily moved softmax reference and
 // the turns on the exponential unit are those of npa_fwd_kernel.cuh.
+//
+// 8-bit cache. e4m3 codes are exact in f16 and one conversion makes two, so
+// that kernel multiplies in f16 and leaves every scale to float32: q, scaled by
+// a power of two per row, is exact in f16 too (elements 2^-14 under the row's
+// largest lose at most 2^-25 of it); the block's k scale joins the softmax
+// scale; its v scale shifts the exponent of P (P' = 2^(x + log2 s_v - R)), and
+// the row sum divides it out again. (Converting code * scale to bf16 instead
+// took 900 instructions of a converting warp per block, and more than twice
+// the time of the softmax beside it.)
 //
 // What differs from the self-attention kernel: every tensor is a 4D {d, L,
 // heads, B} map with the caller's strides (a projection's [B, L, heads * d]
@@ -111,7 +120,8 @@ struct XaCfg {
     static constexpr int bVFull = bKEmpty + kStages;
     static constexpr int bVEmpty = bVFull + kStages;
     static constexpr int bVReady = bVEmpty + kStages;    // [kStages] rows of unkept keys cleared
-    static constexpr int bKCFull = bVReady + kStages;    // [kCodeStages] code blocks landed
+    static constexpr int bQReady = bVReady + kStages;    // [kQStages] 8-bit: queries in f16 (128 arrivals)
+    static constexpr int bKCFull = bQReady + kQStages;   // [kCodeStages] code blocks landed
     static constexpr int bKCEmpty = bKCFull + kCodeStages;
     static constexpr int bVCFull = bKCEmpty + kCodeStages;
     static constexpr int bVCEmpty = bVCFull + kCodeStages;
@@ -122,9 +132,16 @@ struct XaCfg {
     static constexpr int bTurn = bPFree + 2;             // [2][4]
     static constexpr int bEpi = bTurn + 8;               // [2] a softmax warpgroup's own barrier (128 arrivals)
     static constexpr int bDrain = bEpi + 2;              // [2]
-    static constexpr int kNumBars = bDrain + 2;
+    // [4] 8-bit: the row exponents of a unit are written (128 arrivals). Four
+    // sets: the converter reaches unit u + 4 only after the S products of unit
+    // u + 2, which wait for the softmax of unit u (u + 1 at the latest, where a
+    // unit has one tile only).
+    static constexpr int kExpSets = 4;
+    static constexpr int bExp = bDrain + 2;
+    static constexpr int kNumBars = bExp + (KV8 ? kExpSets : 0);
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-    static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
+    static constexpr int kOffExp = kOffMisc + 16;        // [kExpSets][2][128] 8-bit: exponent taken out of a query row
+    static constexpr int kSmemBytes = kOffExp + (KV8 ? kExpSets * 256 : 0) + 1024;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
     static constexpr uint32_t kTmemCols = 512;
     static constexpr bool kSeparateP = (D == 64);
@@ -338,7 +355,7 @@ __device__ void xa_mma_s(const XaParams &p, uint8_t *smem, uint64_t *bars, uint3
         const XaUnit u = xa_unit(p, unit);
         if (u.je <= u.jb) continue;
         const int qs = uq % C::kQStages;
-        ok = sm100::mbar_wait(&bars[C::bQFull + qs], (uq / C::kQStages) & 1, lim);
+        ok = sm100::mbar_wait(&bars[(KV8 ? C::bQReady : C::bQFull) + qs], (uq / C::kQStages) & 1, lim);
         ++uq;
         for (int j = u.jb; ok && j < u.je; ++j, ++kv) {
             if (*abort_flag) {
@@ -353,7 +370,7 @@ __device__ void xa_mma_s(const XaParams &p, uint8_t *smem, uint64_t *bars, uint3
                 if (g[q] > 0) ok = sm100::mbar_wait(&bars[C::bSFree + q], (g[q] - 1) & 1, lim);
                 if (!ok) continue;
                 sm100::tc_fence_after();
-                xa_issue_s<D, F16>(tmem + C::col_s(q), dd.q0 + (qs * 2 + q) * dd.tile, dd.k0 + s * dd.tile, n);
+                xa_issue_s<D, KV8 || F16>(tmem + C::col_s(q), dd.q0 + (qs * 2 + q) * dd.tile, dd.k0 + s * dd.tile, n);
                 sm100::tc_commit(&bars[C::bSFull + q]);
                 ++g[q];
             }
@@ -394,7 +411,7 @@ __device__ void xa_mma_pv(const XaParams &p, uint8_t *smem, uint64_t *bars, uint
                 ok = sm100::mbar_wait(&bars[C::bPFull + q], g[q] & 1, lim);
                 if (!ok) continue;
                 sm100::tc_fence_after();
-                xa_issue_pv<D, F16>(tmem + C::col_o(q), tmem + C::col_p(q), dd.v0 + s * dd.tile, n, j > u.jb);
+                xa_issue_pv<D, KV8 || F16>(tmem + C::col_o(q), tmem + C::col_p(q), dd.v0 + s * dd.tile, n, j > u.jb);
                 sm100::tc_commit(&bars[C::bPFree + q]);
                 ++g[q];
             }
@@ -425,7 +442,7 @@ __device__ void xa_mma(const XaParams &p, uint8_t *smem, uint64_t *bars, uint32_
         const int n_blk = u.je - u.jb;
         if (n_blk <= 0) continue;
         const int qs = uq % C::kQStages;
-        ok = sm100::mbar_wait(&bars[C::bQFull + qs], (uq / C::kQStages) & 1, lim);
+        ok = sm100::mbar_wait(&bars[(KV8 ? C::bQReady : C::bQFull) + qs], (uq / C::kQStages) & 1, lim);
         ++uq;
         for (int j = 0; ok && j <= n_blk; ++j) {
             if (*abort_flag) {
@@ -445,13 +462,13 @@ __device__ void xa_mma(const XaParams &p, uint8_t *smem, uint64_t *bars, uint32_
                     ok = sm100::mbar_wait(&bars[C::bPFull + q], g[q] & 1, lim);
                     if (!ok) continue;
                     sm100::tc_fence_after();
-                    xa_issue_pv<D, F16>(tmem + C::col_o(q), tmem + C::col_p(q), dd.v0 + sp * dd.tile,
+                    xa_issue_pv<D, KV8 || F16>(tmem + C::col_o(q), tmem + C::col_p(q), dd.v0 + sp * dd.tile,
                                         xa_block_keys(u, u.jb + j - 1), j > 1);
                     sm100::tc_commit(&bars[C::bPFree + q]);
                     ++g[q];
                 }
                 if (j < n_blk) {
-                    xa_issue_s<D, F16>(tmem + C::col_s(q), dd.q0 + (qs * 2 + q) * dd.tile, dd.k0 + s * dd.tile,
+                    xa_issue_s<D, KV8 || F16>(tmem + C::col_s(q), dd.q0 + (qs * 2 + q) * dd.tile, dd.k0 + s * dd.tile,
                                        xa_block_keys(u, u.jb + j));
                     sm100::tc_commit(&bars[C::bSFull + q]);
                 }
@@ -517,36 +534,62 @@ __device__ void xa_clear_unkept(const XaParams &p, uint8_t *smem, uint64_t *bars
 }
 
 // ---------------------------------------------------------------------------
-// 8-bit cache: code blocks to bf16 tiles (one warpgroup). code * scale is
-// exact in bf16 for the power-of-two scales that npa_kv8_store writes (an
-// e4m3 number has 4 significant bits); another scale is rounded once. Values
-// of unkept keys are written as zeros.
+// 8-bit cache (one warpgroup): code blocks to f16 tiles, values of unkept keys
+// as zeros (a NaN code would reach the sums through the product otherwise), and
+// the unit's query rows to f16.
 // ---------------------------------------------------------------------------
 template <int D>
-__device__ __forceinline__ void xa_convert_tile(const uint8_t *codes, uint8_t *tile, float s0, float s1,
-                                                const uint32_t (&w)[4], int tid) {
+__device__ __forceinline__ void xa_convert_tile(const uint8_t *codes, uint8_t *tile, const uint32_t (&w)[4], int tid) {
     using C = XaCfg<D, true>;
     constexpr int kPerRow = D / 16;  // 16-code pieces of a row
-#pragma unroll
+    const bool all = (w[0] & w[1] & w[2] & w[3]) == 0xffffffffu;
+#pragma unroll 2
     for (int i = 0; i < kPerRow; ++i) {
         const int idx = tid + 128 * i;
         const int row = idx / kPerRow, piece = idx % kPerRow;
-        const uint4 c4 = *reinterpret_cast<const uint4 *>(codes + idx * 16);
-        const float sc = row < kKv8Block ? s0 : s1;
-        const uint32_t keep = w[row >> 5] >> (row & 31) & 1u;
-        const uint32_t c[4] = {c4.x, c4.y, c4.z, c4.w};
-        uint32_t o[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const uint32_t h2 = sm100::e4m3x2_to_f16x2(c[k >> 1] >> ((k & 1) * 16));
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
-            o[k] = keep ? sm100::pack_bf16x2(f.x * sc, f.y * sc) : 0u;
+        uint4 c4 = *reinterpret_cast<const uint4 *>(codes + idx * 16);
+        if (!all) {
+            const uint32_t word = row < 64 ? (row < 32 ? w[0] : w[1]) : (row < 96 ? w[2] : w[3]);
+            if (!(word >> (row & 31) & 1u)) c4 = make_uint4(0, 0, 0, 0);
         }
         uint8_t *dst = tile + (piece >> 2) * C::kChunkBytes + row * 128;
         const int p0 = (piece & 3) * 2;
-        *reinterpret_cast<uint4 *>(dst + ((p0 ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4 *>(dst + (((p0 + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+        *reinterpret_cast<uint4 *>(dst + ((p0 ^ (row & 7)) << 4)) =
+            make_uint4(sm100::e4m3x2_to_f16x2(c4.x), sm100::e4m3x2_to_f16x2(c4.x >> 16), sm100::e4m3x2_to_f16x2(c4.y),
+                       sm100::e4m3x2_to_f16x2(c4.y >> 16));
+        *reinterpret_cast<uint4 *>(dst + (((p0 + 1) ^ (row & 7)) << 4)) =
+            make_uint4(sm100::e4m3x2_to_f16x2(c4.z), sm100::e4m3x2_to_f16x2(c4.z >> 16), sm100::e4m3x2_to_f16x2(c4.w),
+                       sm100::e4m3x2_to_f16x2(c4.w >> 16));
     }
+}
+
+// One query row, bf16 to f16 in place; returns the exponent taken out.
+template <int D>
+__device__ __forceinline__ int xa_convert_q_row(uint8_t *tile, int row) {
+    using C = XaCfg<D, true>;
+    uint8_t *base = tile + row * 128;
+    auto at = [&](int i) { return reinterpret_cast<uint4 *>(base + (i >> 3) * C::kChunkBytes + (((i & 7) ^ (row & 7)) << 4)); };
+    uint32_t top = 0;  // largest magnitude, as bits
+#pragma unroll 4
+    for (int i = 0; i < D / 8; ++i) {
+        const uint4 v = *at(i);
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top = max(top, max(x[k] & 0x7fffu, x[k] >> 16 & 0x7fffu));
+    }
+    const int e = top ? min(max(int(top >> 7) - 127, -126), 126) : 0;
+    const float down = __uint_as_float(uint32_t(127 - e) << 23);
+#pragma unroll 4
+    for (int i = 0; i < D / 8; ++i) {
+        const uint4 v = *at(i);
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        uint32_t h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            h[k] = sm100::pack_f16x2(__uint_as_float(x[k] << 16) * down, __uint_as_float(x[k] & 0xffff0000u) * down);
+        *at(i) = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+    return e;
 }
 
 template <int D>
@@ -554,38 +597,40 @@ __device__ void xa_convert(const XaParams &p, uint8_t *smem, uint64_t *bars, vol
     using C = XaCfg<D, true>;
     const uint64_t lim = p.wait_limit_ns;
     const int tid = threadIdx.x - C::kConvWarp * 32;
-    int kv = 0;
+    int kv = 0, uq = 0;
     bool ok = true;
     for (int unit = blockIdx.x; ok && unit < p.n_units; unit += gridDim.x) {
         const XaUnit u = xa_unit(p, unit);
-        const size_t sbase = ((size_t)u.b * p.kv_heads + u.kvh) * p.scale_blocks;
-        const int last = p.scale_blocks - 1;  // a block past the cache's last repeats it (its rows are not kept)
-        for (int j = u.jb; j < u.je; ++j, ++kv) {
-            const int i0 = min(2 * j, last), i1 = min(2 * j + 1, last);
-            const float ks0 = __ldg(p.k_scale + sbase + i0), ks1 = __ldg(p.k_scale + sbase + i1);
-            const float vs0 = __ldg(p.v_scale + sbase + i0), vs1 = __ldg(p.v_scale + sbase + i1);
+        if (u.je <= u.jb) continue;
+        const int qs = uq % C::kQStages;
+        ok = warp_wait(&bars[C::bQFull + qs], (uq / C::kQStages) & 1, lim);
+        if (!ok) break;
+        const int set = uq % C::kExpSets;
+        ++uq;
+#pragma unroll 1
+        for (int t = 0; t < u.nt; ++t)
+            reinterpret_cast<int8_t *>(smem + C::kOffExp)[(set * 2 + t) * 128 + tid] =
+                int8_t(xa_convert_q_row<D>(smem + C::kOffQ + (qs * 2 + t) * C::kTileBytes, tid));
+        sm100::mbar_arrive(&bars[C::bExp + set]);
+        sm100::fence_proxy_async();
+        sm100::mbar_arrive(&bars[C::bQReady + qs]);
+        for (int j = u.jb; ok && j < u.je; ++j, ++kv) {
             uint32_t w[4];
             xa_keep(p, u, j, xa_block_keys(u, j), w);
             const int cs = kv % C::kCodeStages, cpar = (kv / C::kCodeStages) & 1;
             const int s = kv % C::kStages, use = kv / C::kStages;
-            ok = !*abort_flag && sm100::mbar_wait(&bars[C::bKCFull + cs], cpar, lim) &&
-                 (use == 0 || sm100::mbar_wait(&bars[C::bKEmpty + s], (use - 1) & 1, lim));
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            xa_convert_tile<D>(smem + C::kOffKC + cs * C::kCodeBytes, smem + C::kOffK + s * C::kTileBytes, ks0, ks1, w,
-                               tid);
-            sm100::fence_proxy_async();
-            sm100::mbar_arrive(&bars[C::bKFull + s]);
-            sm100::mbar_arrive(&bars[C::bKCEmpty + cs]);
-            ok = sm100::mbar_wait(&bars[C::bVCFull + cs], cpar, lim) &&
-                 (use == 0 || sm100::mbar_wait(&bars[C::bVEmpty + s], (use - 1) & 1, lim));
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            xa_convert_tile<D>(smem + C::kOffVC + cs * C::kCodeBytes, smem + C::kOffV + s * C::kTileBytes, vs0, vs1, w,
-                               tid);
-            sm100::fence_proxy_async();
-            sm100::mbar_arrive(&bars[C::bVFull + s]);
-            sm100::mbar_arrive(&bars[C::bVCEmpty + cs]);
+#pragma unroll 1
+            for (int t = 0; t < 2; ++t) {  // keys, values
+                ok = !*abort_flag && sm100::mbar_wait(&bars[(t ? C::bVCFull : C::bKCFull) + cs], cpar, lim) &&
+                     (use == 0 || sm100::mbar_wait(&bars[(t ? C::bVEmpty : C::bKEmpty) + s], (use - 1) & 1, lim));
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                xa_convert_tile<D>(smem + (t ? C::kOffVC : C::kOffKC) + cs * C::kCodeBytes,
+                                   smem + (t ? C::kOffV : C::kOffK) + s * C::kTileBytes, w, tid);
+                sm100::fence_proxy_async();
+                sm100::mbar_arrive(&bars[(t ? C::bVFull : C::bKFull) + s]);
+                sm100::mbar_arrive(&bars[(t ? C::bVCEmpty : C::bKCEmpty) + cs]);
+            }
         }
     }
     if (!ok) {
@@ -597,10 +642,19 @@ __device__ void xa_convert(const XaParams &p, uint8_t *smem, uint64_t *bars, vol
 // ---------------------------------------------------------------------------
 // Softmax and epilogue
 // ---------------------------------------------------------------------------
-// The scores of a block's first 32 * NCH keys, unkept ones as -inf.
-template <int NCH>
+// The scores of a block's first 32 * NCH keys, unkept ones as -inf. The 8-bit
+// kernel's 128 registers at launch rule out a load of 128.
+template <int NCH, bool KV8>
 __device__ __forceinline__ void xa_load_scores(uint32_t t_s, const uint32_t (&w)[4], float (&s)[32 * NCH]) {
-    if constexpr (NCH == 4) {
+    if constexpr (NCH % 2 == 0 && KV8) {
+#pragma unroll
+        for (int c = 0; c < NCH; c += 2) {
+            uint32_t r[64];
+            sm100::tmem_ld64(t_s + 32 * c, r);
+#pragma unroll
+            for (int i = 0; i < 64; ++i) s[32 * c + i] = __uint_as_float(r[i]);
+        }
+    } else if constexpr (NCH == 4) {
         uint32_t r[128];
         sm100::tmem_ld128(t_s, r);
 #pragma unroll
@@ -639,15 +693,22 @@ __device__ __forceinline__ void xa_store_p(uint32_t t_p, const uint32_t (&pk)[16
     }
 }
 
+// A block's scales of the 8-bit cache, one for each half of its keys: f, of the
+// scores to log2 units; lv, log2 of the value scale; inv_v, its reciprocal.
+struct XaScales {
+    float f[2], lv[2], inv_v[2];
+};
+
 template <int D, bool KV8, bool F16>
 struct XaSoftmax {
     using C = XaCfg<D, KV8>;
+    static constexpr bool kF16 = KV8 || F16;  // type of P
     // A block whose maximum exceeds the reference by more than kLead moves it
     // to kBelow under the maximum: P stays within 2^8 in bf16. In f16 the
     // probabilities are kept 2^7 higher (at most 2^15), so that those 2^-24
     // below the row's largest are still normal numbers.
-    static constexpr float kLead = F16 ? 15.f : kRescaleLog2;
-    static constexpr float kBelow = F16 ? 7.f : 0.f;
+    static constexpr float kLead = kF16 ? 15.f : kRescaleLog2;
+    static constexpr float kBelow = kF16 ? 7.f : 0.f;
 
     const XaParams &p;
     uint64_t *bars;
@@ -669,21 +730,66 @@ struct XaSoftmax {
         }
     }
 
+    // Maximum of the block's scores in log2 units, value scales included.
+    template <int N>
+    __device__ __forceinline__ float scaled_max(const float (&s)[N], const XaScales &sc) {
+        if constexpr (!KV8) {
+            return row_max<N>(s) * p.scale_log2;
+        } else {
+            float m[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                float(&h)[2] = m[i >= kKv8Block];
+                h[0] = sm100::max3(h[0], s[i], s[i + 1]);
+                h[1] = sm100::max3(h[1], s[i + 2], s[i + 3]);
+            }
+            const float m0 = fmaf(fmaxf(m[0][0], m[0][1]), sc.f[0], sc.lv[0]);
+            return N > kKv8Block ? fmaxf(m0, fmaf(fmaxf(m[1][0], m[1][1]), sc.f[1], sc.lv[1])) : m0;
+        }
+    }
+    // P of the block at reference R, its row sum returned.
+    template <int N>
+    __device__ __forceinline__ float probabilities(const float (&s)[N], const XaScales &sc, uint32_t (&pk)[N / 2]) {
+        if constexpr (!KV8) {
+            return exp_block<N, F16>(s, p.scale_log2, R, pk);
+        } else {
+            float sum = 0.f;
+#pragma unroll
+            for (int h = 0; h * kKv8Block < N; ++h) {
+                const float shift = R == -INFINITY ? 0.f : sc.lv[h] - R;
+                const uint64_t c2 = sm100::pack_f32x2(sc.f[h], sc.f[h]), m2 = sm100::pack_f32x2(shift, shift);
+                uint64_t acc[2] = {0, 0};
+#pragma unroll
+                for (int i = h * kKv8Block / 2; i < N / 2 && i < (h + 1) * kKv8Block / 2; ++i) {
+                    float x0, x1;
+                    sm100::unpack_f32x2(sm100::fma_f32x2(sm100::pack_f32x2(s[2 * i], s[2 * i + 1]), c2, m2), x0, x1);
+                    const float p0 = sm100::ex2_approx(x0), p1 = sm100::ex2_approx(x1);
+                    pk[i] = sm100::pack_f16x2(p0, p1);
+                    acc[i & 1] = sm100::add_f32x2(acc[i & 1], sm100::pack_f32x2(p0, p1));
+                }
+                float a0, a1;
+                sm100::unpack_f32x2(sm100::add_f32x2(acc[0], acc[1]), a0, a1);
+                sum = fmaf(a0 + a1, sc.inv_v[h], sum);
+            }
+            return sum;
+        }
+    }
+
     // One block of at most 32 * NCH keys; false when a wait ran out.
     template <int NCH>
-    __device__ __forceinline__ bool block(const uint32_t (&w)[4], bool first, bool turns) {
+    __device__ __forceinline__ bool block(const uint32_t (&w)[4], const XaScales &sc, bool first, bool turns) {
         constexpr int kN = 32 * NCH;
         float s[kN];
-        xa_load_scores<NCH>(tS, w, s);
+        xa_load_scores<NCH, KV8>(tS, w, s);
         if (C::kSeparateP) {
             sm100::tc_fence_before();
             sm100::mbar_arrive(&bars[C::bSFree + q]);
         }
-        const float bm = row_max<kN>(s) * p.scale_log2;
+        const float bm = scaled_max<kN>(s, sc);
         if (bm > R + kLead) R = bm - kBelow;
         if (turns && !take_turn()) return false;
         uint32_t pk[kN / 2];
-        const float sum = exp_block<kN, F16>(s, p.scale_log2, R, pk);
+        const float sum = probabilities<kN>(s, sc, pk);
         if (turns) pass_turn();
         const float alpha = (R == R_prev) ? 1.f : sm100::ex2_approx(R_prev - R);
         if (C::kSeparateP && !first) {
@@ -699,45 +805,6 @@ struct XaSoftmax {
         return true;
     }
 
-    // The same in two passes over the scores in TMEM, 32 at a time, for the
-    // 8-bit kernel: its 512 threads leave 128 registers each at launch, too few
-    // to hold a row of scores.
-    template <int NCH>
-    __device__ __forceinline__ bool block_lean(const uint32_t (&w)[4], bool first, bool turns) {
-        float bm = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < NCH; ++c) {
-            float s[32];
-            xa_load_scores<1>(tS + 32 * c, {w[c], 0, 0, 0}, s);
-            bm = fmaxf(bm, row_max<32>(s));
-        }
-        bm *= p.scale_log2;
-        if (bm > R + kLead) R = bm - kBelow;
-        const float alpha = (R == R_prev) ? 1.f : sm100::ex2_approx(R_prev - R);
-        if (C::kSeparateP && !first) {
-            if (!warp_wait(&bars[C::bPFree + q], (g - 1) & 1, lim)) return false;
-            sm100::tc_fence_after();
-        }
-        if (!first && __any_sync(0xffffffffu, alpha != 1.f)) rescale(alpha);
-        if (turns && !take_turn()) return false;
-        float sum = 0.f;
-#pragma unroll
-        for (int c = 0; c < NCH; ++c) {
-            float s[32];
-            xa_load_scores<1>(tS + 32 * c, {w[c], 0, 0, 0}, s);
-            uint32_t pk[16];
-            sum += exp_block<32, F16>(s, p.scale_log2, R, pk);
-            sm100::tmem_st16(tP + 16 * c, pk);
-        }
-        if (turns) pass_turn();
-        l = l * alpha + sum;
-        sm100::tc_fence_before();
-        if (C::kSeparateP) sm100::mbar_arrive(&bars[C::bSFree + q]);
-        sm100::mbar_arrive(&bars[C::bPFull + q]);
-        R_prev = R;
-        return true;
-    }
-
     // O *= alpha.
     __device__ __forceinline__ void rescale(float alpha) {
 #pragma unroll 1
@@ -748,14 +815,6 @@ struct XaSoftmax {
             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
             sm100::tmem_st32(tO + c * 32, o);
         }
-    }
-
-    template <int NCH>
-    __device__ __forceinline__ bool run_block(const uint32_t (&w)[4], bool first, bool turns) {
-        if constexpr (KV8)
-            return block_lean<NCH>(w, first, turns);
-        else
-            return block<NCH>(w, first, turns);
     }
 
     // A warp whose 32 rows lie past the last query keeps the barriers' counts.
@@ -783,6 +842,7 @@ __device__ void xa_softmax(const XaParams &p, uint8_t *smem, uint64_t *bars, uin
                               tmem + lane_off + C::col_p(q), q, warp, (threadIdx.x & 31) == 0, 0, 0, 0.f, 0.f, 0.f};
     uint8_t *stage = smem + C::kOffO + q * C::kChunkBytes;
     int ep = 0;  // uses of the warpgroup's own barrier
+    int uq = -1;  // units with keys so far, the current one included
     auto group_sync = [&]() {
         sm100::mbar_arrive(&bars[C::bEpi + q]);
         return warp_wait(&bars[C::bEpi + q], (ep++) & 1, lim);
@@ -790,30 +850,59 @@ __device__ void xa_softmax(const XaParams &p, uint8_t *smem, uint64_t *bars, uin
     bool ok = true;
     for (int unit = blockIdx.x; ok && unit < p.n_units; unit += gridDim.x) {
         const XaUnit u = xa_unit(p, unit);
+        uq += u.je > u.jb;
         if (q >= u.nt) continue;
         const int grow = u.row0 + q * 128 + row;  // this thread's query
         const bool active = u.row0 + q * 128 + warp * 32 < p.Lq;
         const bool turns = u.nt == 2;
         st.R = st.R_prev = -INFINITY;
         st.l = 0.f;
+        XaScales sc;
+        float ks[2], vs[2], f_row = 0.f;  // the next block's scales; this row's factor
+        const size_t s0 = KV8 ? ((size_t)u.b * p.kv_heads + u.kvh) * p.scale_blocks : 0;
+        auto fetch_scales = [&](int j) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int i = min(2 * j + h, p.scale_blocks - 1);  // past the cache: its keys are not kept
+                ks[h] = __ldg(p.k_scale + s0 + i);
+                vs[h] = __ldg(p.v_scale + s0 + i);
+            }
+        };
+        if (KV8 && u.je > u.jb) fetch_scales(u.jb);
         for (int j = u.jb; j < u.je; ++j) {
             const int n = xa_block_keys(u, j);
             uint32_t w[4];
             xa_keep(p, u, j, n, w);
             ok = warp_wait(&bars[C::bSFull + q], st.g & 1, lim);
             if (!ok) break;
+            if constexpr (KV8) {
+                if (j == u.jb) {
+                    const int set = uq % C::kExpSets;
+                    ok = warp_wait(&bars[C::bExp + set], (uq / C::kExpSets) & 1, lim);
+                    if (!ok) break;
+                    const int e = reinterpret_cast<const int8_t *>(smem + C::kOffExp)[(set * 2 + q) * 128 + row];
+                    f_row = p.scale_log2 * __uint_as_float(uint32_t(127 + e) << 23);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    sc.f[h] = fmaxf(f_row * ks[h], 1.2e-38f);  // above 0: -inf times it stays -inf
+                    sc.lv[h] = __log2f(vs[h]);
+                    sc.inv_v[h] = __fdividef(1.f, vs[h]);
+                }
+                if (j + 1 < u.je) fetch_scales(j + 1);
+            }
             sm100::tc_fence_after();
             const bool first = j == u.jb;
             if (!active)
                 ok = st.idle_block(first, turns);
             else if (n > 96)
-                ok = st.template run_block<4>(w, first, turns);
+                ok = st.template block<4>(w, sc, first, turns);
             else if (n > 64)
-                ok = st.template run_block<3>(w, first, turns);
+                ok = st.template block<3>(w, sc, first, turns);
             else if (n > 32)
-                ok = st.template run_block<2>(w, first, turns);
+                ok = st.template block<2>(w, sc, first, turns);
             else
-                ok = st.template run_block<1>(w, first, turns);
+                ok = st.template block<1>(w, sc, first, turns);
             ++st.g;
             st.tb += turns;
             if (!ok) break;
@@ -897,6 +986,7 @@ __global__ void __launch_bounds__(XaCfg<D, KV8>::kThreads, 1)
     xa_fwd_kernel(const __grid_constant__ XaParams p) {
     using C = XaCfg<D, KV8>;
     extern __shared__ uint8_t smem_raw[];
+    sm100::let_next_kernel_start();
     const uint32_t raw = sm100::smem_u32(smem_raw);
     uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
@@ -907,7 +997,9 @@ __global__ void __launch_bounds__(XaCfg<D, KV8>::kThreads, 1)
         for (int s = 0; s < C::kQStages; ++s) {
             sm100::mbar_init(&bars[C::bQFull + s], 1);
             sm100::mbar_init(&bars[C::bQEmpty + s], 1);
+            sm100::mbar_init(&bars[C::bQReady + s], 128);
         }
+        for (int s = 0; KV8 && s < C::kExpSets; ++s) sm100::mbar_init(&bars[C::bExp + s], 128);
         for (int s = 0; s < C::kStages; ++s) {
             sm100::mbar_init(&bars[C::bKFull + s], KV8 ? 128 : 1);
             sm100::mbar_init(&bars[C::bKEmpty + s], 1);
@@ -986,28 +1078,50 @@ struct XaCombineParams {
 };
 
 template <int D, bool F16>
-__global__ void __launch_bounds__(256) xa_combine_kernel(const __grid_constant__ XaCombineParams p) {
-    const int r = blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (r >= p.rows) return;
+__global__ void __launch_bounds__(128) xa_combine_kernel(const __grid_constant__ XaCombineParams p) {
+    constexpr int kPer = D / 32;   // elements of O per lane
+    constexpr int kAhead = 8;      // splits whose loads are in flight together
+    const int r = blockIdx.x * 4 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
-    constexpr int kPer = D / 32;
-    float mstar = -INFINITY;
-    for (int s = lane; s < p.n_splits; s += 32) mstar = fmaxf(mstar, p.ml[((size_t)s * p.rows + r) * 2]);
+    sm100::wait_for_previous_kernel();
+    if (r >= p.rows) return;
+    static_assert(kXaMaxSplits == 64, "two splits per lane");
+    float2 ml[2];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mstar = fmaxf(mstar, __shfl_xor_sync(0xffffffffu, mstar, o));
+    for (int i = 0; i < 2; ++i)
+        ml[i] = lane + 32 * i < p.n_splits
+                    ? __ldcg(reinterpret_cast<const float2 *>(p.ml) + (size_t)(lane + 32 * i) * p.rows + r)
+                    : make_float2(-INFINITY, 0.f);
+    float m = fmaxf(ml[0].x, ml[1].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float w[2], L = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        w[i] = ml[i].x == -INFINITY ? 0.f : sm100::ex2_approx(ml[i].x - m);
+        L = fmaf(w[i], ml[i].x == -INFINITY ? 0.f : ml[i].y, L);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     float acc[kPer];
 #pragma unroll
     for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
-    float L = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < p.n_splits; ++s) {
-        const size_t pr = (size_t)s * p.rows + r;
-        const float2 ml = __ldg(reinterpret_cast<const float2 *>(p.ml) + pr);
-        if (ml.x == -INFINITY) continue;
-        const float wgt = sm100::ex2_approx(ml.x - mstar);
-        L += wgt * ml.y;
+    const float *part = p.o_part + (size_t)r * D + lane * kPer;
+    for (int s0 = 0; s0 < p.n_splits; s0 += kAhead) {
+        float o[kAhead][kPer], wgt[kAhead];
 #pragma unroll
-        for (int c = 0; c < kPer; ++c) acc[c] += wgt * p.o_part[pr * D + lane * kPer + c];
+        for (int i = 0; i < kAhead; ++i) {
+            const int s = s0 + i;
+            const bool first = s < 32;
+            wgt[i] = __shfl_sync(0xffffffffu, first ? w[0] : w[1], s & 31);
+            const bool in = s < p.n_splits && wgt[i] != 0.f;  // a split without keys wrote no O
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) o[i][c] = in ? __ldcg(part + (size_t)s * p.rows * D + c) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) acc[c] = fmaf(wgt[i], o[i][c], acc[c]);
     }
     const float inv = L > 0.f ? 1.f / L : L;
     const int bh = r / p.Lq, i = r - bh * p.Lq, b = bh / p.heads, h = bh - b * p.heads;

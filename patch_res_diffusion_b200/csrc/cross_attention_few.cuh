@@ -33,6 +33,8 @@ namespace npa {
 
 constexpr int kXaFewRows = 16;
 constexpr int kXaFewWarps = 4;
+// CTAs that run on a multiprocessor at once, by their registers.
+__host__ __device__ constexpr int xa_few_per_sm(int d, int row_tiles) { return d == 64 ? (row_tiles == 1 ? 4 : 3) : 2; }
 
 struct XfParams {
     const void *q, *k, *v;
@@ -70,6 +72,7 @@ struct XfWarp {
     static constexpr bool kF16 = KV8 || F16;                 // type of the products
     static constexpr int kStep = !KV8 && D == 128 ? 16 : 32;  // keys of a step: what the registers hold
     static constexpr int kTiles = kStep / 8, kSubs = kStep / 16;
+    static constexpr uint32_t kAll = kStep == 32 ? 0xffffffffu : 0xffffu;  // every key of a step is kept
     static constexpr int kKLoads = KV8 ? D / 64 : D / 32;    // 16-byte pieces of a key row per lane
     static constexpr int kVWords = KV8 ? D / 32 : D / 16;    // 32-bit words of a value row per lane
     static constexpr int kMTiles = D / 16;
@@ -89,34 +92,33 @@ struct XfWarp {
         return (jm >> 2) * 64 + 8 * g + 2 * (jm & 3) + e;
     }
 
-    __device__ __forceinline__ void load_k(const XfParams &p, const void *base, long long stride, int key0, int len,
-                                           int g, int t) {
+    // row: this lane's bytes of the step's key g (load_k) or 2t (load_v);
+    // stride: bytes from key to key; n: keys left from the step's first on.
+    template <bool kFull>
+    __device__ __forceinline__ void load_k(const char *row, long long stride, int n, int g) {
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-            const int key = key0 + 8 * i + g;
-            const char *row = static_cast<const char *>(base) + (long long)key * stride * (KV8 ? 1 : 2) + t * 16;
+        for (int i = 0; i < kTiles; ++i)
 #pragma unroll
             for (int j = 0; j < kKLoads; ++j)
-                kr[i][j] = key < len ? __ldg(reinterpret_cast<const uint4 *>(row + j * 64)) : make_uint4(0, 0, 0, 0);
-        }
+                kr[i][j] = kFull || 8 * i + g < n ? __ldg(reinterpret_cast<const uint4 *>(row + 8 * i * stride + j * 64))
+                                                  : make_uint4(0, 0, 0, 0);
     }
-    __device__ __forceinline__ void load_v(const XfParams &p, const void *base, long long stride, int key0, int len,
-                                           int g, int t) {
+    template <bool kFull>
+    __device__ __forceinline__ void load_v(const char *row, long long stride, int n, int t) {
 #pragma unroll
         for (int s = 0; s < kSubs; ++s)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int key = key0 + 16 * s + 2 * t + (i & 1) + (i >> 1) * 8;
-                const char *row = static_cast<const char *>(base) + (long long)key * stride * (KV8 ? 1 : 2);
-                const bool in = key < len;
+                const int key = 16 * s + (i & 1) + (i >> 1) * 8;  // past 2t
+                const bool in = kFull || key + 2 * t < n;
                 if constexpr (KV8 && D == 64) {
-                    const uint2 x = in ? __ldg(reinterpret_cast<const uint2 *>(row + g * 8)) : make_uint2(0, 0);
+                    const uint2 x = in ? __ldg(reinterpret_cast<const uint2 *>(row + key * stride)) : make_uint2(0, 0);
                     vr[s][i][0] = x.x;
                     vr[s][i][1] = x.y;
                 } else {
 #pragma unroll
                     for (int j = 0; j < kVWords / 4; ++j) {
-                        const uint4 x = in ? __ldg(reinterpret_cast<const uint4 *>(row + g * 16 + j * 128))
+                        const uint4 x = in ? __ldg(reinterpret_cast<const uint4 *>(row + key * stride + j * 128))
                                            : make_uint4(0, 0, 0, 0);
                         vr[s][i][4 * j] = x.x;
                         vr[s][i][4 * j + 1] = x.y;
@@ -158,7 +160,7 @@ struct XfWarp {
     // O^T += V^T P^T for the step, P as packed pairs [row tile][16 keys][2].
     __device__ __forceinline__ void products(const uint32_t (&pb)[NT][kSubs][2], uint32_t keep, int t) {
         // values of keys that are not kept: 0 (P is 0 there, but not 0 * NaN)
-        if (keep != (kStep == 32 ? 0xffffffffu : 0xffffu)) {
+        if (keep != kAll) {
 #pragma unroll
             for (int s = 0; s < kSubs; ++s)
 #pragma unroll
@@ -212,8 +214,9 @@ struct XfWarp {
 };
 
 template <int D, bool KV8, bool F16, int NT>
-__global__ void __launch_bounds__(32 * kXaFewWarps) xa_few_kernel(const __grid_constant__ XfParams p) {
+__global__ void __launch_bounds__(32 * kXaFewWarps, xa_few_per_sm(D, NT)) xa_few_kernel(const __grid_constant__ XfParams p) {
     using W = XfWarp<D, KV8, F16, NT>;
+    sm100::let_next_kernel_start();
     extern __shared__ float xf_smem[];  // [warps][8 NT][D] O, then [warps][8 NT][2] reference and sum
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int unit = blockIdx.x / p.n_splits, split = blockIdx.x - unit * p.n_splits;
@@ -223,27 +226,31 @@ __global__ void __launch_bounds__(32 * kXaFewWarps) xa_few_kernel(const __grid_c
     const long long steps = ((long long)len + W::kStep - 1) / W::kStep;
     const int j1 = int(steps * (split + 1) / p.n_splits);
     int j = int(steps * split / p.n_splits) + warp;
-    const void *kb, *vb;
-    if (KV8) {
-        kb = static_cast<const char *>(p.k) + b * p.ksb + kvh * p.ksh;
-        vb = static_cast<const char *>(p.v) + b * p.vsb + kvh * p.vsh;
-    } else {
-        kb = static_cast<const uint16_t *>(p.k) + b * p.ksb + kvh * p.ksh;
-        vb = static_cast<const uint16_t *>(p.v) + b * p.vsb + kvh * p.vsh;
-    }
+    // bytes from key to key (a cache's rows are contiguous), and this lane's place in the first
+    constexpr int kElem = KV8 ? 1 : 2;
+    const long long kst = KV8 ? D : p.kst * 2, vst = KV8 ? D : p.vst * 2;
+    const char *kb = static_cast<const char *>(p.k) + (b * p.ksb + kvh * p.ksh) * kElem + g * kst + t * 16;
+    const char *vb = static_cast<const char *>(p.v) + (b * p.vsb + kvh * p.vsh) * kElem + 2 * t * vst +
+                     g * (KV8 && D == 64 ? 8 : 16);
     const float *ks = p.k_scale + (size_t)unit * p.scale_blocks, *vs = p.v_scale + (size_t)unit * p.scale_blocks;
     const unsigned char *mask = p.key_mask ? p.key_mask + (size_t)b * p.Lk : nullptr;
 
     W w;
     auto load_keys = [&](int step) {
-        const int key0 = step * W::kStep;
-        w.load_k(p, kb, p.kst, key0, len, g, t);
+        const int key0 = step * W::kStep, n = len - key0;
+        if (n >= W::kStep)
+            w.template load_k<true>(kb + key0 * kst, kst, n, g);
+        else
+            w.template load_k<false>(kb + key0 * kst, kst, n, g);
         if (KV8) w.ks = __ldg(ks + key0 / kKv8Block);
-        w.mask_byte = key0 + lane < len && (W::kStep == 32 || lane < 16) && (!mask || __ldg(mask + key0 + lane) != 0);
+        if (mask) w.mask_byte = lane < min(n, W::kStep) ? __ldg(mask + key0 + lane) : 0;
     };
     auto load_values = [&](int step) {
-        const int key0 = step * W::kStep;
-        w.load_v(p, vb, p.vst, key0, len, g, t);
+        const int key0 = step * W::kStep, n = len - key0;
+        if (n >= W::kStep)
+            w.template load_v<true>(vb + key0 * vst, vst, n, t);
+        else
+            w.template load_v<false>(vb + key0 * vst, vst, n, t);
         if (KV8) w.vs = __ldg(vs + key0 / kKv8Block);
     };
     if (j < j1) {
@@ -308,10 +315,13 @@ __global__ void __launch_bounds__(32 * kXaFewWarps) xa_few_kernel(const __grid_c
         const bool more = j + kXaFewWarps < j1;
         float s[W::kTiles][4];
         w.scores(s);
-        const uint32_t keep = __ballot_sync(0xffffffffu, w.mask_byte);
+        const int left = len - j * W::kStep;
+        const uint32_t keep = mask                 ? __ballot_sync(0xffffffffu, w.mask_byte != 0)
+                              : left >= W::kStep ? W::kAll
+                                                 : (1u << left) - 1u;
         const float kscale = KV8 ? w.ks : 1.f;
         if (more) load_keys(j + kXaFewWarps);
-        if (keep != (W::kStep == 32 ? 0xffffffffu : 0xffffu)) {
+        if (keep != W::kAll) {
 #pragma unroll
             for (int i = 0; i < W::kTiles; ++i)
 #pragma unroll

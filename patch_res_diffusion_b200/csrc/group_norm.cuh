@@ -113,13 +113,6 @@ struct GnVec<T, 1> {
     static __device__ __forceinline__ Raw narrow(const float (&f)[1]) { return T(f[0]); }
 };
 
-// Waits until the kernels before this one on the stream are complete (launched
-// with programmatic serialisation, a kernel starts before that).
-__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void let_next_kernel_start() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 // Sum over kLanes neighbouring lanes.
 template <int kLanes>
 __device__ __forceinline__ float lanes_sum(float v) {
@@ -441,7 +434,7 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_stats_kernel(const __grid_co
     using Raw = typename V::Raw;
     extern __shared__ uint4 gn_smem16[];
     float2 *entry = reinterpret_cast<float2 *>(gn_smem16);
-    let_next_kernel_start();
+    sm100::let_next_kernel_start();
     const int tile = blockIdx.x, b = blockIdx.y;
     const int ty = p.by_cols(threadIdx.x), tx = threadIdx.x - ty * p.cols;
     const int r0 = tile * p.tile_rows, tokens = min(p.N - r0, p.tile_rows);
@@ -477,9 +470,9 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_stats_kernel(const __grid_co
 
 // One warp to a (batch row, group).
 __global__ void __launch_bounds__(128) gn_merge_kernel(const __grid_constant__ GnParams p, int n) {
-    let_next_kernel_start();
+    sm100::let_next_kernel_start();
     const int g = blockIdx.x * 4 + (threadIdx.x >> 5);
-    wait_for_previous_kernel();
+    sm100::wait_for_previous_kernel();
     if (g >= n) return;
     const float2 q = gn_merge_tiles<32, kGnMaxTiles / 32>(p, p.part + (size_t)g * p.tiles, 1, threadIdx.x & 31);
     if ((threadIdx.x & 31) == 0) p.mean_rstd[g] = q;
@@ -490,7 +483,7 @@ template <typename T, int kVec>
 __global__ void __launch_bounds__(kGnThreads, 3) gn_apply_kernel(const __grid_constant__ GnParams p) {
     using V = GnVec<T, kVec>;
     using Raw = typename V::Raw;
-    let_next_kernel_start();
+    sm100::let_next_kernel_start();
     const int ty = p.by_cols(threadIdx.x), tx = threadIdx.x - ty * p.cols;
     const int r0 = (gridDim.x - 1 - blockIdx.x) * p.apply_rows, tokens = min(p.N - r0, p.apply_rows);
     const int b = gridDim.y - 1 - blockIdx.y;
@@ -511,7 +504,7 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_apply_kernel(const __grid_co
         if (left >= kGnBatch) fetch(raw);
         GnAffine<T, kVec> f;
         f.weights(p, col, 0);
-        if (!waited) wait_for_previous_kernel();
+        if (!waited) sm100::wait_for_previous_kernel();
         waited = true;
         f.statistics(p, mean_rstd, col);
         auto write = [&](auto silu) {

@@ -148,7 +148,7 @@ def attend_and_check(npa, q, cache, n, kv_lens=None, key_mask=None, scale=None, 
     assert npa.npa_device_status() == npa.NPA_OK
     v = values(cache.v, cache.v_scale, n)
     ref, mag = oracle.cross_attention(f64(q), values(cache.k, cache.k_scale, n), v, keep=keep, scale=scale)
-    check_attention(f64(out), ref, mag, "bf16", n, float(np.nanmax(np.abs(v))), what)
+    check_attention(f64(out), ref, mag, "bf16", n, float(np.nanmax(np.abs(v))), what, kv8=True)
     return out
 
 
@@ -196,20 +196,26 @@ def test_attention_layouts_and_guard(npa):
     assert (buf[:, 0] == 7.0).all() and (buf[:, -1] == 7.0).all()
 
 
-def test_other_scales(npa):
-    """Scales that are no powers of two (a cache filled elsewhere): code *
-    scale is rounded to bf16 once, half a step relative, on k and on v. The
-    scores then carry an error of up to 2^-8 sum |q k| c."""
-    B, h, Lq, n, d = 1, 2, 50, 300, 64
+@pytest.mark.parametrize("Lq", [3, 50])
+def test_other_scales(npa, Lq):
+    """Scales that are no powers of two (a cache filled elsewhere) are as exact."""
+    B, h, n, d = 1, 2, 300, 64
     cache = filled(npa, 90, B, h, n, d)
     cache.k_scale.mul_(1.2345)
     cache.v_scale.mul_(0.777)
-    q = randn(91, B, h, Lq, d)
-    out = f64(npa.kv8_cross_attention(q, cache, n))
-    rnd = lambda c, s: f64(torch.from_numpy(values(c, s, n)).bfloat16())
-    k, v = rnd(cache.k, cache.k_scale), rnd(cache.v, cache.v_scale)
-    ref, mag = oracle.cross_attention(f64(q), k, v)
-    check_attention(out, ref, mag, "bf16", n, float(np.abs(v).max()))
+    attend_and_check(npa, randn(91, B, h, Lq, d), cache, n)
+
+
+@pytest.mark.parametrize("Lq", [2, 150])
+def test_sizes_of_values_and_queries(npa, Lq):
+    """Blocks whose values differ by 2^60, tiny and huge keys and queries."""
+    B, h, n, d = 1, 2, 320, 64
+    k, v = randn(95, B, h, n, d), randn(96, B, h, n, d)
+    size = torch.tensor([1.0, 2.0 ** -40, 2.0 ** 20, 1.0, 2.0 ** -8], device="cuda").repeat_interleave(64)[:, None]
+    for ks, qs in ((1.0, 1.0), (2.0 ** -60, 2.0 ** 60), (2.0 ** 70, 2.0 ** -70)):
+        cache = npa.Kv8Cache.empty(B, h, n, d)
+        npa.kv8_store(cache, (k.double() * ks).bfloat16(), (v.double() * size).bfloat16())
+        attend_and_check(npa, (randn(97, B, h, Lq, d).double() * qs).bfloat16(), cache, n, what=(ks, qs))
 
 
 def test_a_denoising_loop_in_one_graph(npa):
