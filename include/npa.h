@@ -256,11 +256,11 @@ typedef struct {
  * Lk are any sizes >= 1.
  * Arithmetic as for npa_attention_fwd; float16 inputs keep their probabilities
  * in float16 for the P.V product.
- * When the queries alone would leave multiprocessors idle, the key range is
+ * Where the queries alone would leave multiprocessors idle, the key range is
  * split over them: partial results go to `workspace` (caller-owned device
- * memory, 16-byte aligned; npa_cross_attention_workspace_size() bytes for the
- * planned split count, and a smaller or NULL workspace gives fewer or no
- * splits) and a second kernel on the same stream merges them. Calls that
+ * memory, 16-byte aligned; npa_cross_attention_workspace_size() bytes as
+ * planned, and a smaller or NULL workspace gives fewer or no splits - the same
+ * result up to rounding) and a second kernel on the same stream merges them. Calls that
  * overlap on the GPU need workspaces of their own. o and the workspace must
  * not overlap each other or an input (address ranges, gaps between strided
  * rows included). */
@@ -271,8 +271,8 @@ npa_status npa_cross_attention_fwd(const void *q, const void *k, const void *v, 
                                    float scale, void *workspace, size_t workspace_bytes, npa_stream_t stream);
 
 /* Workspace bytes npa_cross_attention_fwd and npa_kv8_cross_attention_fwd use
- * for their planned split count on the current device (0: none needed, or
- * invalid arguments). */
+ * on the current device for the split they plan (0: none, or invalid
+ * arguments; 16-bit keys of at most 128 never need any). */
 size_t npa_cross_attention_workspace_size(int B, int heads, int kv_heads, int Lq, int Lk, int d);
 
 /* Keys and values held in 8 bits: e4m3 codes (1-4-3, largest 448) with one

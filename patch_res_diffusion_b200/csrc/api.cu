@@ -697,40 +697,44 @@ bool encode_view(CUtensorMap *m, const View &v, bool f16, int rows = 128) {
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Key-range splits: the count with the smallest predicted time, in key blocks
-// of one CTA, over the launch's waves. A unit costs about two blocks beyond
-// its own, and merging the splits about four.
-int plan_xa_splits(long long base_units, long long n_blocks, int sm_count) {
-    int best = 1;
-    double best_cost = 1e300;
-    for (int s = 1; s <= npa::kXaMaxSplits && s <= n_blocks; ++s) {
-        const long long waves = (base_units * s + sm_count - 1) / sm_count;
-        if (s > 1 && waves > 1 && base_units >= sm_count) break;
-        const double cost = (double)waves * ((n_blocks + s - 1) / s + 2) + (s > 1 ? 4 : 0);
-        if (cost < best_cost - 1e-9) {
-            best_cost = cost;
-            best = s;
-        }
-    }
-    return best;
+// How xa_fwd_kernel's units are shared out: whole units in waves, and whether
+// the last wave, which does not fill the GPU, is cut into pieces of the key
+// range. In key blocks of one CTA, a unit costs about two beyond its own, and
+// cut units five more for the merge.
+struct XaPlan {
+    int grid, waves, tail_ctas, tail_blocks;
+};
+
+XaPlan plan_xa(long long units, long long n_blk, int sm_count, bool cut) {
+    XaPlan pl;
+    pl.grid = (int)std::min<long long>(units, sm_count);
+    pl.waves = (int)((units + sm_count - 1) / sm_count);
+    pl.tail_ctas = pl.tail_blocks = 0;
+    const long long whole = units / sm_count, rest = units % sm_count, blocks = rest * n_blk;
+    if (!cut || rest == 0 || blocks > (1 << 30)) return pl;
+    const long long ctas = std::min<long long>(sm_count, (blocks + 1) / 2);
+    if (ctas <= rest || (blocks + ctas - 1) / ctas + 3 + 5 >= n_blk + 2) return pl;
+    pl.waves = (int)whole;
+    pl.grid = (int)(whole ? sm_count : ctas);
+    pl.tail_ctas = (int)ctas;
+    pl.tail_blocks = (int)blocks;
+    return pl;
 }
 
-// The same for xa_few_kernel: as many CTAs as run at once, each with two steps
-// or more for every warp.
+// Key-range splits of xa_few_kernel: as many CTAs as run at once, each with two
+// steps or more for every warp.
 int plan_xf_splits(long long units, int rows, int Lk, int d, int sm_count) {
     const long long want = (long long)npa::xa_few_per_sm(d, rows > 8 ? 2 : 1) * sm_count / units;
     const long long most = ((long long)Lk + 255) / 256;
     return (int)std::max(1LL, std::min({want, most, (long long)npa::kXaMaxSplits}));
 }
 
-// The planned split count of a call, whichever kernel runs it.
-int plan_splits(int B, int heads, int kv_heads, int Lq, int Lk, int d, int sm_count) {
-    const long long rows = (long long)(heads / kv_heads) * Lq;
-    if (rows <= npa::kXaFewRows) return plan_xf_splits((long long)B * kv_heads, (int)rows, Lk, d, sm_count);
-    return plan_xa_splits((long long)B * heads * ((Lq + 255) / 256), ((long long)Lk + 127) / 128, sm_count);
+bool xa_few_rows(int heads, int kv_heads, int Lq) {
+    return (long long)(heads / kv_heads) * Lq <= npa::kXaFewRows;
 }
 
 size_t xa_split_bytes(int B, int heads, int Lq, int d) { return (size_t)B * heads * Lq * (d + 2) * sizeof(float); }
+size_t xa_tail_bytes(int ctas, int d) { return (size_t)ctas * 512 * (d + 2) * sizeof(float); }
 
 struct XaCall {
     View q, k, v, o;
@@ -796,16 +800,24 @@ npa_status launch_xs_kernel(const XaCall &c, const npa::XaParams &a, int sm_coun
                : NPA_ERR_CUDA;
 }
 
+// The kernel that merges partial results: of cut units (tail_ctas > 0), or of
+// xa_few_kernel's splits.
 npa_status launch_combine(const XaCall &c, const npa::XaParams &a, npa_stream_t stream) {
     const int d = c.q.d;
-    const long long rows = (long long)a.B * a.heads * a.Lq;
+    npa::XaParams prm = a;
+    const bool tail = a.tail_ctas > 0;
+    const int cut = a.tail_ctas ? a.tail_blocks / a.n_blk : 0;  // cut units
+    const long long rows = tail ? 256LL * cut : (long long)a.B * a.heads * a.Lq;
     npa::XaCombineParams cp{a.o_part, a.ml, const_cast<void *>(c.o.ptr), c.o.sb, c.o.sh, c.o.st, a.n_splits,
-                            (int)rows, a.heads, a.Lq};
-    void *args[1] = {&cp};
-    const void *kernel = d == 64 ? (c.f16 ? (const void *)npa::xa_combine_kernel<64, true>
-                                          : (const void *)npa::xa_combine_kernel<64, false>)
-                                 : (c.f16 ? (const void *)npa::xa_combine_kernel<128, true>
-                                          : (const void *)npa::xa_combine_kernel<128, false>);
+                            (int)rows, a.heads, a.Lq, a.n_units - cut};
+    void *tail_args[2] = {&prm, &cp}, *split_args[1] = {&cp};
+    void **args = tail ? tail_args : split_args;
+    const void *kernels[2][2][2] = {
+        {{(const void *)npa::xa_combine_kernel<64, false>, (const void *)npa::xa_combine_kernel<64, true>},
+         {(const void *)npa::xa_combine_kernel<128, false>, (const void *)npa::xa_combine_kernel<128, true>}},
+        {{(const void *)npa::xa_tail_kernel<64, false>, (const void *)npa::xa_tail_kernel<64, true>},
+         {(const void *)npa::xa_tail_kernel<128, false>, (const void *)npa::xa_tail_kernel<128, true>}}};
+    const void *kernel = kernels[tail][d == 128][c.f16];
     // it may start under the attention kernel's end, and waits there
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -881,26 +893,19 @@ npa_status launch_xa(const XaCall &c, npa_stream_t stream) {
     const double scale = c.scale > 0.f ? (double)c.scale : 1.0 / std::sqrt((double)d);
     prm.scale_log2 = (float)(1.4426950408889634 * scale);
     prm.wait_limit_ns = kWaitLimitNs;
-    const long long base = (long long)B * heads * prm.n_qpairs;
-    // as many splits as planned and as the workspace holds (one needs none)
-    int splits = plan_splits(B, heads, c.k.heads, Lq, Lk, d, sm_count);
-    const size_t per_split = xa_split_bytes(B, heads, Lq, d);
-    const size_t held = c.workspace ? c.workspace_bytes / per_split : 1;
-    if ((size_t)splits > held) splits = (int)held;
-    if (splits < 2) splits = 1;
-    prm.n_splits = splits;
-    const long long rows = (long long)B * heads * Lq;
-    if (splits > 1) {
-        prm.o_part = static_cast<float *>(c.workspace);
-        prm.ml = prm.o_part + (size_t)splits * rows * d;
-    }
-    prm.n_units = (int)(base * splits);
-    prm.by_splits = npa::FastDiv(splits);
+    const long long units = (long long)B * heads * prm.n_qpairs;
+    prm.n_units = (int)units;
     prm.by_qpairs = npa::FastDiv(prm.n_qpairs);
     prm.by_heads = npa::FastDiv(heads);
     prm.by_group = npa::FastDiv(prm.group);
+    prm.o_part = static_cast<float *>(c.workspace);
     const bool kv8 = c.k_scale != nullptr;
-    if ((long long)prm.group * Lq <= npa::kXaFewRows) {
+    if (xa_few_rows(heads, c.k.heads, Lq)) {
+        // as many splits as planned and as the workspace holds (one needs none)
+        const size_t held = c.workspace ? c.workspace_bytes / xa_split_bytes(B, heads, Lq, d) : 1;
+        prm.n_splits = plan_xf_splits((long long)B * c.k.heads, prm.group * Lq, Lk, d, sm_count);
+        if ((size_t)prm.n_splits > held) prm.n_splits = (int)std::max<size_t>(held, 1);
+        prm.ml = prm.n_splits > 1 ? prm.o_part + (size_t)prm.n_splits * B * heads * Lq * d : nullptr;
         npa_status s;
         if (kv8)
             s = d == 64 ? launch_xf_kernel<64, true, false>(c, prm, stream)
@@ -911,7 +916,7 @@ npa_status launch_xa(const XaCall &c, npa_stream_t stream) {
         else
             s = c.f16 ? launch_xf_kernel<128, false, true>(c, prm, stream)
                       : launch_xf_kernel<128, false, false>(c, prm, stream);
-        return s != NPA_OK || splits == 1 ? s : launch_combine(c, prm, stream);
+        return s != NPA_OK || prm.n_splits == 1 ? s : launch_combine(c, prm, stream);
     }
     if (!encode_view(&prm.tm_q, c.q, c.f16) || !encode_view(&prm.tm_o, c.o, c.f16)) return NPA_ERR_CUDA;
     if (!kv8 && Lk <= npa::kXaShortKeys)
@@ -920,6 +925,15 @@ npa_status launch_xa(const XaCall &c, npa_stream_t stream) {
                        : (c.f16 ? launch_xs_kernel<128, true>(c, prm, sm_count, stream)
                                 : launch_xs_kernel<128, false>(c, prm, sm_count, stream));
     if (!encode_view(&prm.tm_k, c.k, c.f16) || !encode_view(&prm.tm_v, c.v, c.f16)) return NPA_ERR_CUDA;
+    prm.n_blk = (Lk + 127) / 128;
+    prm.by_blk = npa::FastDiv(prm.n_blk);
+    XaPlan pl = plan_xa(units, prm.n_blk, sm_count, true);
+    if (pl.tail_ctas && (!c.workspace || c.workspace_bytes < xa_tail_bytes(pl.tail_ctas, d)))
+        pl = plan_xa(units, prm.n_blk, sm_count, false);
+    prm.waves = pl.waves;
+    prm.tail_ctas = pl.tail_ctas;
+    prm.tail_blocks = pl.tail_blocks;
+    prm.ml = prm.o_part + (size_t)pl.tail_ctas * 512 * d;
     const void *kernel;
     unsigned threads, smem;
     auto pick = [&](const void *k, auto cfg) {
@@ -938,11 +952,10 @@ npa_status launch_xa(const XaCall &c, npa_stream_t stream) {
         pick(c.f16 ? (const void *)npa::xa_fwd_kernel<128, false, true>
                    : (const void *)npa::xa_fwd_kernel<128, false, false>,
              npa::XaCfg<128, false>{});
-    const unsigned grid = (unsigned)(prm.n_units < sm_count ? prm.n_units : sm_count);
     void *args[1] = {&prm};
-    if (cudaLaunchKernel(kernel, dim3(grid), dim3(threads), args, smem, (cudaStream_t)stream) != cudaSuccess)
+    if (cudaLaunchKernel(kernel, dim3((unsigned)pl.grid), dim3(threads), args, smem, (cudaStream_t)stream) != cudaSuccess)
         return NPA_ERR_CUDA;
-    return splits > 1 ? launch_combine(c, prm, stream) : NPA_OK;
+    return pl.tail_ctas ? launch_combine(c, prm, stream) : NPA_OK;
 }
 
 // A cache's own arguments.
@@ -1326,8 +1339,12 @@ size_t npa_cross_attention_workspace_size(int B, int heads, int kv_heads, int Lq
     int dev = 0, sm = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return 0;
-    const int s = plan_splits(B, heads, kv_heads, Lq, Lk, d, sm);
-    return s > 1 ? (size_t)s * xa_split_bytes(B, heads, Lq, d) : 0;
+    if (xa_few_rows(heads, kv_heads, Lq)) {
+        const int s = plan_xf_splits((long long)B * kv_heads, heads / kv_heads * Lq, Lk, d, sm);
+        return s > 1 ? (size_t)s * xa_split_bytes(B, heads, Lq, d) : 0;
+    }
+    const XaPlan pl = plan_xa((long long)B * heads * ((Lq + 255) / 256), ((long long)Lk + 127) / 128, sm, true);
+    return xa_tail_bytes(pl.tail_ctas, d);
 }
 
 npa_status npa_cross_attention_fwd(const void *q, const void *k, const void *v, void *o, npa_dtype dtype, int B,

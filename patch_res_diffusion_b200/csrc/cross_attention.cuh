@@ -75,12 +75,21 @@ struct XaParams {
     int B, heads, kv_heads, group, Lq, Lk;
     int q_b, q_h, k_b, k_h, v_b, v_h;  // 1, or 0 along an axis that the tensor repeats (stride 0)
     int n_qpairs;                      // ceil(Lq / 256)
-    int n_splits, n_units;
-    FastDiv by_splits, by_qpairs, by_heads, by_group;
+    int n_units;                       // 256-row units: B * heads * n_qpairs
+    // Every CTA runs `waves` whole units (blockIdx.x, blockIdx.x + gridDim.x,
+    // ...). The units after those, fewer than there are CTAs, are cut: their
+    // tail_blocks key blocks (n_blk each) are dealt evenly to the first
+    // tail_ctas CTAs, in order, and pieces of a unit are merged by
+    // xa_tail_kernel. tail_ctas = 0: nothing is cut.
+    int waves, tail_ctas, tail_blocks, n_blk;
+    FastDiv by_blk, by_qpairs, by_heads, by_group;
     float scale_log2;
     unsigned long long wait_limit_ns;
-    float *o_part;  // n_splits > 1: [n_splits][B * heads * Lq][d] unnormalised O
-    float *ml;      // n_splits > 1: [n_splits][B * heads * Lq][2] reference, row sum
+    int n_splits;   // xa_few_kernel: key-range splits
+    // Partial results: unnormalised O [..][d], then reference and row sum
+    // [..][2]. Cut units: two slots of 256 rows per CTA (its first piece, its
+    // last); xa_few_kernel: [n_splits][B * heads * Lq].
+    float *o_part, *ml;
 };
 
 template <int D, bool KV8>
@@ -145,7 +154,10 @@ struct XaCfg {
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
     static constexpr uint32_t kTmemCols = 512;
     static constexpr bool kSeparateP = (D == 64);
-    static constexpr bool kUseTurn = (D == 64);
+    // Turns on the exponential unit: not with the 8-bit cache, where half of a
+    // block's scores are read under them (531 us with, 494 without on 2 x 10
+    // heads, 4096 queries, 12288 keys).
+    static constexpr bool kUseTurn = D == 64 && !KV8;
     __device__ static constexpr uint32_t col_s(int q) { return uint32_t(q * 128); }
     __device__ static constexpr uint32_t col_o(int q) { return uint32_t(256 + q * D); }
     __device__ static constexpr uint32_t col_p(int q) { return kSeparateP ? uint32_t(256 + 2 * D + q * 64) : col_s(q); }
@@ -160,29 +172,51 @@ struct XaUnit {
     int nt;      // query tiles (1 or 2)
     int len;     // keys of this batch row
     int jb, je;  // key blocks [jb, je)
-    int split;
+    int slot;    // a piece of a unit: where its partial result goes; -1: the whole unit
 };
 
-__device__ __forceinline__ XaUnit xa_unit(const XaParams &p, int unit) {
+// First tail block of CTA c.
+__host__ __device__ inline int xa_tail_start(int blocks, int ctas, int c) { return int((long long)blocks * c / ctas); }
+
+// The units of a CTA, in the order that all of its roles walk them.
+struct XaIter {
+    const XaParams &p;
     XaUnit u;
-    const int r = p.by_splits(unit);
-    u.split = unit - r * p.n_splits;
-    const int bh = p.by_qpairs(r);
-    u.row0 = (r - bh * p.n_qpairs) * 256;
-    u.b = p.by_heads(bh);
-    u.h = bh - u.b * p.heads;
-    u.kvh = p.by_group(u.h);
-    u.nt = p.Lq - u.row0 > 128 ? 2 : 1;
-    u.len = p.kv_lens ? min(max(__ldg(p.kv_lens + u.b), 0), p.Lk) : p.Lk;
-    const int nblk = (u.len + 127) / 128;  // < 2^24, and n_splits <= 64
-    u.jb = 0;
-    u.je = nblk;
-    if (p.n_splits > 1) {
-        u.jb = p.by_splits(nblk * u.split);
-        u.je = p.by_splits(nblk * (u.split + 1));
+    int w = 0, pos = 0, start = 0, end = 0;
+    __device__ __forceinline__ explicit XaIter(const XaParams &prm) : p(prm) {
+        if (int(blockIdx.x) < p.tail_ctas) {
+            pos = start = xa_tail_start(p.tail_blocks, p.tail_ctas, blockIdx.x);
+            end = xa_tail_start(p.tail_blocks, p.tail_ctas, blockIdx.x + 1);
+        }
     }
-    return u;
-}
+    __device__ __forceinline__ bool next() {
+        int unit, jb = 0, je = p.n_blk;
+        u.slot = -1;
+        if (w < p.waves) {
+            unit = blockIdx.x + w * gridDim.x;
+            ++w;
+            if (unit >= p.n_units) return false;
+        } else {
+            if (pos >= end) return false;
+            const int t = p.by_blk(pos);
+            unit = p.waves * gridDim.x + t;
+            jb = pos - t * p.n_blk;
+            je = min(p.n_blk, jb + end - pos);
+            if (je - jb < p.n_blk) u.slot = 2 * blockIdx.x + (pos != start);
+            pos += je - jb;
+        }
+        const int bh = p.by_qpairs(unit);
+        u.row0 = (unit - bh * p.n_qpairs) * 256;
+        u.b = p.by_heads(bh);
+        u.h = bh - u.b * p.heads;
+        u.kvh = p.by_group(u.h);
+        u.nt = p.Lq - u.row0 > 128 ? 2 : 1;
+        u.len = p.kv_lens ? min(max(__ldg(p.kv_lens + u.b), 0), p.Lk) : p.Lk;
+        u.je = min(je, (u.len + 127) / 128);
+        u.jb = min(jb, u.je);
+        return true;
+    }
+};
 
 __device__ __forceinline__ int xa_block_keys(const XaUnit &u, int j) { return min(128, u.len - j * 128); }
 
@@ -224,8 +258,8 @@ __device__ void xa_producer(const XaParams &p, uint8_t *smem, uint64_t *bars, vo
     sm100::tma_prefetch_desc(&p.tm_o);
     int nk = 0, nv = 0, uq = 0;
     bool ok = true;
-    for (int unit = blockIdx.x; ok && unit < p.n_units; unit += gridDim.x) {
-        const XaUnit u = xa_unit(p, unit);
+    for (XaIter it(p); ok && it.next();) {
+        const XaUnit &u = it.u;
         if (u.je <= u.jb) continue;
         const int qs = uq % C::kQStages, quse = uq / C::kQStages;
         if (quse > 0 && !sm100::mbar_wait(&bars[C::bQEmpty + qs], (quse - 1) & 1, lim)) {
@@ -351,8 +385,8 @@ __device__ void xa_mma_s(const XaParams &p, uint8_t *smem, uint64_t *bars, uint3
     const XaDescs<D, KV8> dd(smem);
     int kv = 0, uq = 0, g[2] = {0, 0};
     bool ok = true;
-    for (int unit = blockIdx.x; ok && unit < p.n_units; unit += gridDim.x) {
-        const XaUnit u = xa_unit(p, unit);
+    for (XaIter it(p); ok && it.next();) {
+        const XaUnit &u = it.u;
         if (u.je <= u.jb) continue;
         const int qs = uq % C::kQStages;
         ok = sm100::mbar_wait(&bars[(KV8 ? C::bQReady : C::bQFull) + qs], (uq / C::kQStages) & 1, lim);
@@ -396,8 +430,8 @@ __device__ void xa_mma_pv(const XaParams &p, uint8_t *smem, uint64_t *bars, uint
     const int bV = xa_v_bar<D, KV8>(p);
     int kv = 0, g[2] = {0, 0};
     bool ok = true;
-    for (int unit = blockIdx.x; ok && unit < p.n_units; unit += gridDim.x) {
-        const XaUnit u = xa_unit(p, unit);
+    for (XaIter it(p); ok && it.next();) {
+        const XaUnit &u = it.u;
         for (int j = u.jb; ok && j < u.je; ++j, ++kv) {
             if (*abort_flag) {
                 ok = false;
@@ -437,8 +471,8 @@ __device__ void xa_mma(const XaParams &p, uint8_t *smem, uint64_t *bars, uint32_
     const int bV = xa_v_bar<D, KV8>(p);
     int kv0 = 0, uq = 0, g[2] = {0, 0};  // kv0: ring index of the unit's first block; g: P blocks consumed
     bool ok = true;
-    for (int unit = blockIdx.x; ok && unit < p.n_units; unit += gridDim.x) {
-        const XaUnit u = xa_unit(p, unit);
+    for (XaIter it(p); ok && it.next();) {
+        const XaUnit &u = it.u;
         const int n_blk = u.je - u.jb;
         if (n_blk <= 0) continue;
         const int qs = uq % C::kQStages;
@@ -499,8 +533,8 @@ __device__ void xa_clear_unkept(const XaParams &p, uint8_t *smem, uint64_t *bars
     const int lane = threadIdx.x & 31;
     int kv = 0;
     bool ok = true;
-    for (int unit = blockIdx.x; ok && unit < p.n_units; unit += gridDim.x) {
-        const XaUnit u = xa_unit(p, unit);
+    for (XaIter it(p); ok && it.next();) {
+        const XaUnit &u = it.u;
         for (int j = u.jb; j < u.je; ++j, ++kv) {
             const int s = kv % C::kStages, n = xa_block_keys(u, j);
             uint32_t w[4];
@@ -599,8 +633,8 @@ __device__ void xa_convert(const XaParams &p, uint8_t *smem, uint64_t *bars, vol
     const int tid = threadIdx.x - C::kConvWarp * 32;
     int kv = 0, uq = 0;
     bool ok = true;
-    for (int unit = blockIdx.x; ok && unit < p.n_units; unit += gridDim.x) {
-        const XaUnit u = xa_unit(p, unit);
+    for (XaIter it(p); ok && it.next();) {
+        const XaUnit &u = it.u;
         if (u.je <= u.jb) continue;
         const int qs = uq % C::kQStages;
         ok = warp_wait(&bars[C::bQFull + qs], (uq / C::kQStages) & 1, lim);
@@ -642,18 +676,14 @@ __device__ void xa_convert(const XaParams &p, uint8_t *smem, uint64_t *bars, vol
 // ---------------------------------------------------------------------------
 // Softmax and epilogue
 // ---------------------------------------------------------------------------
-// The scores of a block's first 32 * NCH keys, unkept ones as -inf. The 8-bit
-// kernel's 128 registers at launch rule out a load of 128.
-template <int NCH, bool KV8>
+// 32 * NCH scores of a row, unkept ones as -inf.
+template <int NCH>
 __device__ __forceinline__ void xa_load_scores(uint32_t t_s, const uint32_t (&w)[4], float (&s)[32 * NCH]) {
-    if constexpr (NCH % 2 == 0 && KV8) {
+    if constexpr (NCH == 2) {
+        uint32_t r[64];
+        sm100::tmem_ld64(t_s, r);
 #pragma unroll
-        for (int c = 0; c < NCH; c += 2) {
-            uint32_t r[64];
-            sm100::tmem_ld64(t_s + 32 * c, r);
-#pragma unroll
-            for (int i = 0; i < 64; ++i) s[32 * c + i] = __uint_as_float(r[i]);
-        }
+        for (int i = 0; i < 64; ++i) s[i] = __uint_as_float(r[i]);
     } else if constexpr (NCH == 4) {
         uint32_t r[128];
         sm100::tmem_ld128(t_s, r);
@@ -682,6 +712,8 @@ template <int NCH>
 __device__ __forceinline__ void xa_store_p(uint32_t t_p, const uint32_t (&pk)[16 * NCH]) {
     if constexpr (NCH == 4) {
         sm100::tmem_st64(t_p, pk);
+    } else if constexpr (NCH == 2) {
+        sm100::tmem_st32(t_p, pk);
     } else {
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
@@ -730,79 +762,106 @@ struct XaSoftmax {
         }
     }
 
-    // Maximum of the block's scores in log2 units, value scales included.
+    // Maximum of one half's scores in log2 units, value scale included.
     template <int N>
-    __device__ __forceinline__ float scaled_max(const float (&s)[N], const XaScales &sc) {
-        if constexpr (!KV8) {
-            return row_max<N>(s) * p.scale_log2;
-        } else {
-            float m[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};
+    __device__ __forceinline__ float half_max(const float (&s)[N], const XaScales &sc, int h) {
+        float m[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < N; i += 4) {
-                float(&h)[2] = m[i >= kKv8Block];
-                h[0] = sm100::max3(h[0], s[i], s[i + 1]);
-                h[1] = sm100::max3(h[1], s[i + 2], s[i + 3]);
-            }
-            const float m0 = fmaf(fmaxf(m[0][0], m[0][1]), sc.f[0], sc.lv[0]);
-            return N > kKv8Block ? fmaxf(m0, fmaf(fmaxf(m[1][0], m[1][1]), sc.f[1], sc.lv[1])) : m0;
+        for (int i = 0; i < N; i += 4) {
+            m[0] = sm100::max3(m[0], s[i], s[i + 1]);
+            m[1] = sm100::max3(m[1], s[i + 2], s[i + 3]);
         }
+        return fmaf(fmaxf(m[0], m[1]), sc.f[h], sc.lv[h]);
     }
-    // P of the block at reference R, its row sum returned.
+    // P of one half at reference R; the row sum, without the value scale.
     template <int N>
-    __device__ __forceinline__ float probabilities(const float (&s)[N], const XaScales &sc, uint32_t (&pk)[N / 2]) {
-        if constexpr (!KV8) {
-            return exp_block<N, F16>(s, p.scale_log2, R, pk);
-        } else {
-            float sum = 0.f;
-#pragma unroll
-            for (int h = 0; h * kKv8Block < N; ++h) {
-                const float shift = R == -INFINITY ? 0.f : sc.lv[h] - R;
-                const uint64_t c2 = sm100::pack_f32x2(sc.f[h], sc.f[h]), m2 = sm100::pack_f32x2(shift, shift);
-                uint64_t acc[2] = {0, 0};
-#pragma unroll
-                for (int i = h * kKv8Block / 2; i < N / 2 && i < (h + 1) * kKv8Block / 2; ++i) {
-                    float x0, x1;
-                    sm100::unpack_f32x2(sm100::fma_f32x2(sm100::pack_f32x2(s[2 * i], s[2 * i + 1]), c2, m2), x0, x1);
-                    const float p0 = sm100::ex2_approx(x0), p1 = sm100::ex2_approx(x1);
-                    pk[i] = sm100::pack_f16x2(p0, p1);
-                    acc[i & 1] = sm100::add_f32x2(acc[i & 1], sm100::pack_f32x2(p0, p1));
-                }
-                float a0, a1;
-                sm100::unpack_f32x2(sm100::add_f32x2(acc[0], acc[1]), a0, a1);
-                sum = fmaf(a0 + a1, sc.inv_v[h], sum);
-            }
-            return sum;
-        }
+    __device__ __forceinline__ float half_exp(const float (&s)[N], const XaScales &sc, int h, uint32_t (&pk)[N / 2]) {
+        return exp_block<N, true>(s, sc.f[h], R == -INFINITY ? R : R - sc.lv[h], pk) * sc.inv_v[h];
     }
 
-    // One block of at most 32 * NCH keys; false when a wait ran out.
-    template <int NCH>
-    __device__ __forceinline__ bool block(const uint32_t (&w)[4], const XaScales &sc, bool first, bool turns) {
-        constexpr int kN = 32 * NCH;
-        float s[kN];
-        xa_load_scores<NCH, KV8>(tS, w, s);
+    // The row's scores are in registers: d = 64, the next block's may come.
+    __device__ __forceinline__ void release_scores() {
         if (C::kSeparateP) {
             sm100::tc_fence_before();
             sm100::mbar_arrive(&bars[C::bSFree + q]);
         }
-        const float bm = scaled_max<kN>(s, sc);
-        if (bm > R + kLead) R = bm - kBelow;
-        if (turns && !take_turn()) return false;
-        uint32_t pk[kN / 2];
-        const float sum = probabilities<kN>(s, sc, pk);
-        if (turns) pass_turn();
-        const float alpha = (R == R_prev) ? 1.f : sm100::ex2_approx(R_prev - R);
+    }
+
+    // PV(j-1) is done and O is at the reference R.
+    __device__ __forceinline__ bool ready_for_p(bool first, float alpha) {
         if (C::kSeparateP && !first) {
             if (!warp_wait(&bars[C::bPFree + q], (g - 1) & 1, lim)) return false;
             sm100::tc_fence_after();
         }
         if (!first && __any_sync(0xffffffffu, alpha != 1.f)) rescale(alpha);
-        l = l * alpha + sum;
-        xa_store_p<NCH>(tP, pk);
+        return true;
+    }
+
+    // A block over the 8-bit cache, half by half (each has its scales): a whole
+    // row of scores does not fit in the registers that its 512 threads leave.
+    // The second half is read twice; P of the first may overwrite its own
+    // scores (d = 128), not the second's.
+    template <int NCH>
+    __device__ __forceinline__ bool block8(const uint32_t (&w)[4], const XaScales &sc, bool first, bool turns) {
+        constexpr int kA = NCH < 2 ? NCH : 2, kB = NCH - kA;  // 32-key pieces of the halves
+        const uint32_t wb[4] = {w[2], w[3], 0, 0};
+        float bm = -INFINITY;
+        if constexpr (kB > 0) {
+            float s[32 * kB];
+            xa_load_scores<kB>(tS + 64, wb, s);
+            bm = half_max(s, sc, 1);
+        }
+        float s[32 * kA];
+        xa_load_scores<kA>(tS, w, s);
+        if (kB == 0) release_scores();
+        bm = fmaxf(bm, half_max(s, sc, 0));
+        if (bm > R + kLead) R = bm - kBelow;
+        const float alpha = (R == R_prev) ? 1.f : sm100::ex2_approx(R_prev - R);
+        if (turns && !take_turn()) return false;
+        uint32_t pk[16 * kA];
+        l = l * alpha + half_exp(s, sc, 0, pk);
+        if (!ready_for_p(first, alpha)) return false;
+        xa_store_p<kA>(tP, pk);
+        if constexpr (kB > 0) {
+            float t[32 * kB];
+            xa_load_scores<kB>(tS + 64, wb, t);
+            release_scores();
+            uint32_t pt[16 * kB];
+            l += half_exp(t, sc, 1, pt);
+            xa_store_p<kB>(tP + 32, pt);
+        }
+        if (turns) pass_turn();
         sm100::tc_fence_before();
         sm100::mbar_arrive(&bars[C::bPFull + q]);
         R_prev = R;
         return true;
+    }
+
+    // One block of at most 32 * NCH keys; false when a wait ran out.
+    template <int NCH>
+    __device__ __forceinline__ bool block(const uint32_t (&w)[4], const XaScales &sc, bool first, bool turns) {
+        if constexpr (KV8) {
+            return block8<NCH>(w, sc, first, turns);
+        } else {
+            constexpr int kN = 32 * NCH;
+            float s[kN];
+            xa_load_scores<NCH>(tS, w, s);
+            release_scores();
+            const float bm = row_max<kN>(s) * p.scale_log2;
+            if (bm > R + kLead) R = bm - kBelow;
+            if (turns && !take_turn()) return false;
+            uint32_t pk[kN / 2];
+            const float sum = exp_block<kN, F16>(s, p.scale_log2, R, pk);
+            if (turns) pass_turn();
+            const float alpha = (R == R_prev) ? 1.f : sm100::ex2_approx(R_prev - R);
+            if (!ready_for_p(first, alpha)) return false;
+            l = l * alpha + sum;
+            xa_store_p<NCH>(tP, pk);
+            sm100::tc_fence_before();
+            sm100::mbar_arrive(&bars[C::bPFull + q]);
+            R_prev = R;
+            return true;
+        }
     }
 
     // O *= alpha.
@@ -848,8 +907,8 @@ __device__ void xa_softmax(const XaParams &p, uint8_t *smem, uint64_t *bars, uin
         return warp_wait(&bars[C::bEpi + q], (ep++) & 1, lim);
     };
     bool ok = true;
-    for (int unit = blockIdx.x; ok && unit < p.n_units; unit += gridDim.x) {
-        const XaUnit u = xa_unit(p, unit);
+    for (XaIter it(p); ok && it.next();) {
+        const XaUnit &u = it.u;
         uq += u.je > u.jb;
         if (q >= u.nt) continue;
         const int grow = u.row0 + q * 128 + row;  // this thread's query
@@ -912,11 +971,9 @@ __device__ void xa_softmax(const XaParams &p, uint8_t *smem, uint64_t *bars, uin
         if (ok && any) ok = warp_wait(&bars[C::bPFree + q], (st.g - 1) & 1, lim);
         if (!ok) break;
         sm100::tc_fence_after();
-        const size_t bh = (size_t)u.b * p.heads + u.h;
-        if (p.n_splits > 1) {
-            const size_t rows = (size_t)p.B * p.heads * p.Lq;
-            const size_t prow = u.split * rows + bh * p.Lq + grow;
-            const bool valid = bound_row(grow < p.Lq, prow, rows * p.n_splits);
+        if (u.slot >= 0) {
+            const size_t prow = (size_t)u.slot * 256 + q * 128 + row;
+            const bool valid = bound_row(grow < p.Lq, prow, (size_t)p.tail_ctas * 512);
             if (valid) *reinterpret_cast<float2 *>(p.ml + prow * 2) = make_float2(any ? st.R_prev : -INFINITY, st.l);
             if (any && active) {
                 float4 *part = reinterpret_cast<float4 *>(p.o_part + prow * D);
@@ -1067,7 +1124,7 @@ __global__ void __launch_bounds__(XaCfg<D, KV8>::kThreads, 1)
     }
 }
 
-// Merges the key-range splits: one warp per query row. With m* the largest
+// Merges xa_few_kernel's key-range splits: one warp per query row. With m* the largest
 // reference, o = sum_s 2^(m_s - m*) O_s / sum_s 2^(m_s - m*) l_s; a split
 // without keys has m_s = -inf and no O.
 struct XaCombineParams {
@@ -1075,7 +1132,48 @@ struct XaCombineParams {
     void *o;
     long long sb, sh, st;  // strides of o in elements
     int n_splits, rows, heads, Lq;
+    int first_unit;  // xa_tail_kernel: the first cut unit
 };
+
+// The cut units' pieces, one warp per query row: with c0 and c1 the CTAs that
+// hold the unit's first and last block, its pieces are the slots of c0 .. c1.
+template <int D, bool F16>
+__global__ void __launch_bounds__(128) xa_tail_kernel(const __grid_constant__ XaParams p, XaCombineParams o) {
+    constexpr int kPer = D / 32;
+    const int idx = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int t = idx >> 8, r = idx & 255;
+    sm100::wait_for_previous_kernel();
+    if (t >= p.n_units - o.first_unit) return;
+    const int bh = p.by_qpairs(o.first_unit + t), row = (o.first_unit + t - bh * p.n_qpairs) * 256 + r;
+    const int b0 = t * p.n_blk;
+    auto cta_of = [&](int block) { return int(((long long)(block + 1) * p.tail_ctas - 1) / p.tail_blocks); };
+    const int c0 = cta_of(b0), c1 = cta_of(b0 + p.n_blk - 1);
+    if (row >= p.Lq || c0 == c1) return;  // no row, or the unit was not cut
+    auto slot_row = [&](int c) {
+        const int slot = 2 * c + (xa_tail_start(p.tail_blocks, p.tail_ctas, c) < b0);
+        return (size_t)slot * 256 + r;
+    };
+    float m = -INFINITY, L = 0.f, acc[kPer];
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
+    for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(p.ml + slot_row(c) * 2));
+    for (int c = c0; c <= c1; ++c) {
+        const size_t pr = slot_row(c);
+        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.ml) + pr);
+        if (ml.x == -INFINITY) continue;  // a piece without keys wrote no O
+        const float wgt = sm100::ex2_approx(ml.x - m);
+        L = fmaf(wgt, ml.y, L);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) acc[k] = fmaf(wgt, __ldcg(p.o_part + pr * D + lane * kPer + k), acc[k]);
+    }
+    const float inv = L > 0.f ? 1.f / L : L;
+    const int b = p.by_heads(bh), h = bh - b * p.heads;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(o.o) + b * o.sb + h * o.sh + row * o.st +
+                                                 lane * kPer);
+#pragma unroll
+    for (int k = 0; k < kPer; k += 2)
+        dst[k / 2] = L == 0.f ? 0u : sm100::pack_16x2<F16>(acc[k] * inv, acc[k + 1] * inv);
+}
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(128) xa_combine_kernel(const __grid_constant__ XaCombineParams p) {

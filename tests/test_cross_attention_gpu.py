@@ -81,6 +81,18 @@ def test_long_keys(npa, dtype, d):
     run_and_check(npa, q, k, v, dtype, what="units")
 
 
+@pytest.mark.parametrize("d,Lk,lens", [(64, 2500, None), (128, 1800, [1800, 700]), (64, 1290, [5, 1290])])
+def test_more_units_than_multiprocessors(npa, d, Lk, lens):
+    """Whole units in waves, then the rest cut into pieces of the key range;
+    batch rows whose keys end inside, before and after a piece."""
+    q, k, v = qkv(9, 2, 5, 5, 4000, Lk, d)
+    assert npa.npa_cross_attention_workspace_size(2, 5, 5, 4000, Lk, d) > 0
+    a = run_and_check(npa, q, k, v, "bf16", kv_lens=lens, what="cut")
+    b = npa.cross_attention(q, k, v, kv_lens=None if lens is None else torch.tensor(lens, dtype=torch.int32).cuda())
+    assert torch.equal(bits(a), bits(b))
+    run_and_check(npa, q, k, v, "bf16", kv_lens=lens, split=False, what="whole")
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_large_scores(npa, d, dtype):

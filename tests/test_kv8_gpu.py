@@ -169,6 +169,15 @@ def test_attention_long(npa, d):
     attend_and_check(npa, randn(63, 2, 4, 6000, d), cache, 600)
 
 
+@pytest.mark.parametrize("d,n,lens", [(64, 2500, None), (128, 1800, [1800, 700])])
+def test_attention_more_units_than_multiprocessors(npa, d, n, lens):
+    """Whole units in waves, then the rest cut into pieces of the key range."""
+    cache = filled(npa, 65, 2, 5, n, d)
+    q = randn(66, 2, 5, 4000, d)
+    attend_and_check(npa, q, cache, n, kv_lens=lens)
+    attend_and_check(npa, q, cache, n, kv_lens=lens, split=False)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_attention_heads_lens_masks(npa, d):
     B, n = 4, 400
