@@ -495,9 +495,10 @@ def asg_combine(eps, eps_ref, mask, w_t: float, out=None, stream=None):
 
 
 # ---------------------------------------------------------------------------
-# The steps around the self-attention. These calls are short (some run for a
-# few microseconds), so what does not change from call to call - stride
-# structures, dtype codes, workspace sizes - is looked up, not built again.
+# The steps around the self-attention. Some of these calls run for a few
+# microseconds, so what a call's shapes, strides and types decide - the checks,
+# the stride structures, the workspace's size - is worked out once for each
+# combination (the lru_cache'd functions) and looked up afterwards.
 # ---------------------------------------------------------------------------
 
 @functools.lru_cache(maxsize=None)
@@ -506,47 +507,47 @@ def _dtype_codes():
     return {torch.bfloat16: NPA_DTYPE_BF16, torch.float16: NPA_DTYPE_FP16, torch.float32: NPA_DTYPE_FP32}
 
 
-def _dtype_code(t, allowed) -> int:
-    code = _dtype_codes().get(t.dtype)
+def _dtype_code(dtype, allowed) -> int:
+    code = _dtype_codes().get(dtype)
     if code not in allowed:
-        raise ValueError(f"unsupported dtype {t.dtype}")
+        raise ValueError(f"unsupported dtype {dtype}")
     return code
 
 
-def _device_of(first, *others):
-    """The CUDA device that all the tensors (or None) are on."""
-    dev = first.device
-    if dev.type != "cuda":
-        raise ValueError(f"expected CUDA tensors, got {dev}")
+def _device_of(first, *others) -> int:
+    """The index of the CUDA device that all the tensors (or None) are on."""
+    index = first.get_device()
+    if index < 0:
+        raise ValueError(f"expected CUDA tensors, got {first.device}")
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
-    return dev
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+    return index
 
 
-def _run_on(dev, stream, body):
-    """``body()`` with ``dev`` and, when given, ``stream`` current, so that
-    outputs and workspaces come from the stream that the call runs on."""
+def _run_on(index, stream, body, *args):
+    """``body(*args, handle)`` with device ``index`` and, when given, ``stream``
+    current, so that outputs and workspaces come from the stream that the call
+    runs on; handle is that stream's."""
     import torch
-    if stream is None and dev.index == torch.cuda.current_device():
-        return body()
-    with torch.cuda.device(dev):
+    if stream is None and index == torch.cuda.current_device():
+        return body(*args, _raw_stream_of()(index))
+    with torch.cuda.device(index):
         if stream is None:
-            return body()
+            return body(*args, _raw_stream_of()(index))
         if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+            stream = torch.cuda.ExternalStream(int(stream), device=torch.device("cuda", index))
         with torch.cuda.stream(stream):
-            return body()
+            return body(*args, int(stream.cuda_stream))
 
 
-def _heads_strides(name, t, shape):
-    """Checks a [B, heads, L, d] tensor's shape and returns its (batch, head, token) strides."""
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected {tuple(shape)}, got {tuple(t.shape)}")
-    s = t.stride()
-    if s[3] != 1:
+def _heads_strides(name, shape, strides, want):
+    """Checks a [B, heads, L, d] tensor's layout; its strides for the C call."""
+    if tuple(shape) != tuple(want):
+        raise ValueError(f"{name}: expected {tuple(want)}, got {tuple(shape)}")
+    if strides[3] != 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
-    return s[:3]
+    return _strides(strides[:3])
 
 
 def _kept_keys(kv_lens, key_mask, B, Lk):
@@ -566,14 +567,35 @@ def _scale(scale) -> float:
     return float(scale)
 
 
-@functools.lru_cache(maxsize=1024)
-def _xa_workspace_size(device_index, B, heads, kv_heads, Lq, Lk, d) -> int:
-    return npa_cross_attention_workspace_size(B, heads, kv_heads, Lq, Lk, d)   # of the current device: the key's first part
+def _like_strides(shape, strides):
+    """The strides, for the C call, that torch.empty_like gives a tensor of this layout."""
+    import torch
+    like = torch.empty_like(torch.empty_strided(shape, strides, dtype=torch.uint8, device="meta"))
+    return _heads_strides("out", shape, like.stride(), shape)
+
+
+def _empty_bytes(n, like):
+    import torch
+    return torch.empty(n, dtype=torch.uint8, device=like.device) if n else None
 
 
 @functools.lru_cache(maxsize=1024)
-def _gn_workspace_size(device_index, code, B, N, C, groups) -> int:
-    return npa_group_norm_workspace_size(code, B, N, C, groups)
+def _cross_plan(index, split, q_shape, q_strides, k_shape, k_strides, v_shape, v_strides, q_dtype, k_dtype, v_dtype):
+    """(sizes, strides and a fresh output's strides for the C call, workspace bytes)."""
+    if len(q_shape) != 4 or len(k_shape) != 4:
+        raise ValueError(f"expected [B, heads, L, d], got {tuple(q_shape)} and {tuple(k_shape)}")
+    B, heads, Lq, d = q_shape
+    kv_heads, Lk = k_shape[1], k_shape[2]
+    strides = (_heads_strides("q", q_shape, q_strides, q_shape),
+               _heads_strides("k", k_shape, k_strides, (B, kv_heads, Lk, d)),
+               _heads_strides("v", v_shape, v_strides, k_shape))
+    code = _dtype_code(q_dtype, (NPA_DTYPE_BF16, NPA_DTYPE_FP16))
+    if not q_dtype == k_dtype == v_dtype:
+        raise ValueError("q, k and v must have one dtype")
+    nbytes = 0
+    if split and index >= 0:
+        nbytes = npa_cross_attention_workspace_size(B, heads, kv_heads, Lq, Lk, d)   # of the current device: `index`
+    return (code, B, heads, kv_heads, Lq, Lk, d), strides, _like_strides(q_shape, q_strides), nbytes
 
 
 def cross_attention(q, k, v, kv_lens=None, key_mask=None, scale: Optional[float] = None, out=None, split: bool = True,
@@ -584,32 +606,36 @@ def cross_attention(q, k, v, kv_lens=None, key_mask=None, scale: Optional[float]
     through ``transpose(1, 2)``). What ``kv_lens`` (int32 [B]) or ``key_mask``
     (bool or uint8 [B, Lk], true: attend) leave out does not reach the output;
     a row without keys gives zeros. ``scale`` defaults to 1/sqrt(d). With
-    ``split`` a workspace is allocated so that the key range of few queries can
-    be split across the GPU. Returns ``out`` (by default laid out like q)."""
+    ``split`` a workspace is allocated so that the key range can be split
+    across the GPU. Returns ``out`` (by default laid out like q)."""
+    index = q.get_device()
+    if index < 0:   # refused below, after the shapes' own faults
+        return _cross_attention(index, q, k, v, kv_lens, key_mask, scale, out, split, 0)
+    return _run_on(index, stream, _cross_attention, index, q, k, v, kv_lens, key_mask, scale, out, split)
+
+
+def _cross_attention(index, q, k, v, kv_lens, key_mask, scale, out, split, handle):
     import torch
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError(f"expected [B, heads, L, d], got {tuple(q.shape)} and {tuple(k.shape)}")
-    B, heads, Lq, d = q.shape
-    kv_heads, Lk = k.shape[1], k.shape[2]
-    qs = _heads_strides("q", q, q.shape)
-    ks = _heads_strides("k", k, (B, kv_heads, Lk, d))
-    vs = _heads_strides("v", v, k.shape)
-    code = _dtype_code(q, (NPA_DTYPE_BF16, NPA_DTYPE_FP16))
-    if not q.dtype == k.dtype == v.dtype or (out is not None and out.dtype != q.dtype):
-        raise ValueError("q, k, v and out must have one dtype")
+    sizes, strides, o_strides, nbytes = _cross_plan(index, split, q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(),
+                                                    q.dtype, k.dtype, v.dtype)
+    lens = mask = None
     if kv_lens is not None or key_mask is not None:
-        _kept_keys(kv_lens, key_mask, B, Lk)
-    dev = _device_of(q, k, v, kv_lens, key_mask, out)
-
-    def call():
-        o = torch.empty_like(q) if out is None else out
-        nbytes = _xa_workspace_size(dev.index, B, heads, kv_heads, Lq, Lk, d) if split else 0
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-        npa_cross_attention_fwd(q, k, v, o, code, B, heads, kv_heads, Lq, Lk, d, qs, ks, vs,
-                                _heads_strides("out", o, q.shape), kv_lens, key_mask, _scale(scale), ws, nbytes)
-        return o
-
-    return _run_on(dev, stream, call)
+        _kept_keys(kv_lens, key_mask, sizes[1], sizes[5])
+        lens, mask = _ptr(kv_lens), _ptr(key_mask)
+    _device_of(q, k, v, kv_lens, key_mask, out)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        if out.dtype != q.dtype:
+            raise ValueError("out must have q's dtype")
+        o_strides = _heads_strides("out", out.shape, out.stride(), q.shape)
+    ws = _empty_bytes(nbytes, q)
+    code = lib().npa_cross_attention_fwd(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), *sizes, *strides, o_strides, lens, mask, _scale(scale),
+        ws.data_ptr() if nbytes else None, nbytes, handle)
+    if code:
+        raise NpaError(code, "npa_cross_attention_fwd")
+    return out
 
 
 class Kv8Cache:
@@ -618,7 +644,7 @@ class Kv8Cache:
     ``k_scale``, ``v_scale`` [B, kv_heads, capacity / 64], value = code *
     scale. ``Kv8Cache.empty`` allocates one; ``kv8_store`` writes it."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "c_struct", "index")
 
     def __init__(self, k, v, k_scale, v_scale):
         import torch
@@ -634,8 +660,9 @@ class Kv8Cache:
                 raise ValueError(f"expected e4m3 or uint8 codes, got {t.dtype}")
         if not (k.is_contiguous() and v.is_contiguous() and k_scale.is_contiguous() and v_scale.is_contiguous()):
             raise ValueError("a cache's tensors must be contiguous")
-        _device_of(k, v, k_scale, v_scale)
+        self.index = _device_of(k, v, k_scale, v_scale)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.c_struct = _Kv8Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k.shape[2])
 
     @classmethod
     def empty(cls, B: int, kv_heads: int, capacity: int, d: int, device="cuda") -> "Kv8Cache":
@@ -652,58 +679,105 @@ class Kv8Cache:
         return int(self.k.shape[2])
 
 
+@functools.lru_cache(maxsize=1024)
+def _store_plan(cache_shape, k_shape, k_strides, v_shape, v_strides, k_dtype, v_dtype):
+    B, kv_heads, _, d = cache_shape
+    if len(k_shape) != 4:
+        raise ValueError(f"expected [B, heads, L, d], got {tuple(k_shape)}")
+    strides = (_heads_strides("k", k_shape, k_strides, (B, kv_heads, k_shape[2], d)),
+               _heads_strides("v", v_shape, v_strides, k_shape))
+    code = _dtype_code(k_dtype, (NPA_DTYPE_BF16, NPA_DTYPE_FP16))
+    if v_dtype != k_dtype:
+        raise ValueError("k and v must have one dtype")
+    return (code, B, kv_heads, d), k_shape[2], strides
+
+
 def kv8_store(cache: Kv8Cache, k, v, start: int = 0, starts=None, stream=None) -> None:
     """Writes bf16 or fp16 k, v [B, kv_heads, n, d] (strides as for
     ``cross_attention``) into the cache from token ``start`` on, or from
     ``starts[b]`` (int32 [B]) in batch row b."""
+    _run_on(cache.index, stream, _kv8_store, cache, k, v, start, starts)
+
+
+def _kv8_store(cache, k, v, start, starts, handle):
     import torch
-    B, kv_heads, capacity, d = cache.k.shape
-    if k.dim() != 4:
-        raise ValueError(f"expected [B, heads, L, d], got {tuple(k.shape)}")
-    n = k.shape[2]
-    ks = _heads_strides("k", k, (B, kv_heads, n, d))
-    vs = _heads_strides("v", v, k.shape)
-    code = _dtype_code(k, (NPA_DTYPE_BF16, NPA_DTYPE_FP16))
-    if v.dtype != k.dtype:
-        raise ValueError("k and v must have one dtype")
-    if starts is not None and (starts.dtype != torch.int32 or starts.shape != (B,) or not starts.is_contiguous()):
-        raise ValueError(f"starts: expected a contiguous int32 tensor of {B} positions")
-    dev = _device_of(cache.k, k, v, starts)
-    _run_on(dev, stream, lambda: npa_kv8_store(k, v, cache.k, cache.v, cache.k_scale, cache.v_scale, capacity, code, B,
-                                               kv_heads, d, start, n, starts, ks, vs))
+    sizes, n, strides = _store_plan(cache.k.shape, k.shape, k.stride(), v.shape, v.stride(), k.dtype, v.dtype)
+    if starts is not None and (starts.dtype != torch.int32 or starts.shape != sizes[1:2] or
+                               not starts.is_contiguous()):
+        raise ValueError(f"starts: expected a contiguous int32 tensor of {sizes[1]} positions")
+    _device_of(cache.k, k, v, starts)
+    code = lib().npa_kv8_store(k.data_ptr(), v.data_ptr(), cache.c_struct, *sizes, start, _ptr(starts), n, *strides, handle)
+    if code:
+        raise NpaError(code, "npa_kv8_store")
+
+
+@functools.lru_cache(maxsize=1024)
+def _kv8_plan(index, split, q_shape, q_strides, cache_shape, Lk, q_dtype):
+    B, kv_heads, capacity, d = cache_shape
+    if len(q_shape) != 4:
+        raise ValueError(f"expected [B, heads, L, d], got {tuple(q_shape)}")
+    heads, Lq = q_shape[1], q_shape[2]
+    strides = _heads_strides("q", q_shape, q_strides, (B, heads, Lq, d))
+    _dtype_code(q_dtype, (NPA_DTYPE_BF16,))
+    Lk = capacity if Lk is None else int(Lk)
+    nbytes = npa_cross_attention_workspace_size(B, heads, kv_heads, Lq, Lk, d) if split else 0   # current device: `index`
+    return (B, heads, kv_heads, Lq, Lk, d), strides, _like_strides(q_shape, q_strides), nbytes
 
 
 def kv8_cross_attention(q, cache: Kv8Cache, n_tokens: Optional[int] = None, kv_lens=None, key_mask=None,
                         scale: Optional[float] = None, out=None, split: bool = True, stream=None):
     """``cross_attention`` of bf16 q [B, heads, Lq, d] over the first
     ``n_tokens`` (default: all) tokens of an 8-bit cache."""
+    return _run_on(cache.index, stream, _kv8_cross_attention, q, cache, n_tokens, kv_lens, key_mask, scale, out, split)
+
+
+def _kv8_cross_attention(q, cache, n_tokens, kv_lens, key_mask, scale, out, split, handle):
     import torch
-    cB, kv_heads, capacity, cd = cache.k.shape
-    if q.dim() != 4:
-        raise ValueError(f"expected [B, heads, L, d], got {tuple(q.shape)}")
-    B, heads, Lq, d = q.shape
-    qs = _heads_strides("q", q, (cB, heads, Lq, cd))
-    Lk = capacity if n_tokens is None else int(n_tokens)
-    _dtype_code(q, (NPA_DTYPE_BF16,))
-    if out is not None and out.dtype != q.dtype:
-        raise ValueError("q and out must have one dtype")
+    sizes, q_strides, o_strides, nbytes = _kv8_plan(cache.index, split, q.shape, q.stride(), cache.k.shape, n_tokens, q.dtype)
+    lens = mask = None
     if kv_lens is not None or key_mask is not None:
-        _kept_keys(kv_lens, key_mask, B, Lk)
-    dev = _device_of(q, cache.k, kv_lens, key_mask, out)
-
-    def call():
-        o = torch.empty_like(q) if out is None else out
-        nbytes = _xa_workspace_size(dev.index, B, heads, kv_heads, Lq, Lk, d) if split else 0
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-        npa_kv8_cross_attention_fwd(q, cache.k, cache.v, cache.k_scale, cache.v_scale, capacity, o, B, heads,
-                                    kv_heads, Lq, Lk, d, qs, _heads_strides("out", o, q.shape), kv_lens, key_mask,
-                                    _scale(scale), ws, nbytes)
-        return o
-
-    return _run_on(dev, stream, call)
+        _kept_keys(kv_lens, key_mask, sizes[0], sizes[4])
+        lens, mask = _ptr(kv_lens), _ptr(key_mask)
+    _device_of(cache.k, q, kv_lens, key_mask, out)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        if out.dtype != q.dtype:
+            raise ValueError("out must have q's dtype")
+        o_strides = _heads_strides("out", out.shape, out.stride(), q.shape)
+    ws = _empty_bytes(nbytes, q)
+    code = lib().npa_kv8_cross_attention_fwd(
+        q.data_ptr(), cache.c_struct, out.data_ptr(), *sizes, q_strides, o_strides, lens, mask, _scale(scale),
+        ws.data_ptr() if nbytes else None, nbytes, handle)
+    if code:
+        raise NpaError(code, "npa_kv8_cross_attention_fwd")
+    return out
 
 
 _ACTIVATIONS = {None: NPA_ACT_NONE, "none": NPA_ACT_NONE, "silu": NPA_ACT_SILU}
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_plan(index, groups, act, x_shape, x_strides, x_dtype, w_shape, w_strides, w_dtype, b_shape, b_strides, b_dtype):
+    """((dtype codes and sizes), x's strides, activation, workspace bytes)."""
+    if len(x_shape) != 3:
+        raise ValueError(f"expected [B, N, C], got {tuple(x_shape)}")
+    if act not in _ACTIVATIONS:
+        raise ValueError(f"unknown activation {act!r}")
+    B, N, C = x_shape
+    code = wcode = _dtype_code(x_dtype, (NPA_DTYPE_BF16, NPA_DTYPE_FP16, NPA_DTYPE_FP32))
+    for name, shape, strides, dtype in (("weight", w_shape, w_strides, w_dtype), ("bias", b_shape, b_strides, b_dtype)):
+        if shape is None:
+            continue
+        if tuple(shape) != (C,) or (C > 1 and strides != (1,)):
+            raise ValueError(f"{name}: expected a contiguous [{C}] tensor")
+        wcode = _dtype_code(dtype, (code, NPA_DTYPE_FP32))
+    if w_dtype is not None and b_dtype is not None and w_dtype != b_dtype:
+        raise ValueError("weight and bias must have one dtype")
+    if C > 1 and x_strides[2] != 1:
+        raise ValueError("channels must be contiguous")
+    nbytes = npa_group_norm_workspace_size(code, B, N, C, groups) if index >= 0 else 0   # of the current device: `index`
+    return (code, wcode, B, N, C, groups), x_strides[:2], _ACTIVATIONS[act], nbytes
 
 
 def group_norm(x, groups: int, weight=None, bias=None, eps: float = 1e-5, act: Optional[str] = None, out=None,
@@ -713,35 +787,28 @@ def group_norm(x, groups: int, weight=None, bias=None, eps: float = 1e-5, act: O
     strides free; weight and bias [C] of x's dtype or float32. ``out=x`` works
     in place. (A channels-last [B, C, H, W] tensor is ``x.permute(0, 2, 3,
     1).flatten(1, 2)``.)"""
+    index = x.get_device()
+    if index < 0:
+        return _group_norm(index, x, groups, weight, bias, eps, act, out, 0)
+    return _run_on(index, stream, _group_norm, index, x, groups, weight, bias, eps, act, out)
+
+
+def _group_norm(index, x, groups, weight, bias, eps, act, out, handle):
     import torch
-    if x.dim() != 3:
-        raise ValueError(f"expected [B, N, C], got {tuple(x.shape)}")
-    if act not in _ACTIVATIONS:
-        raise ValueError(f"unknown activation {act!r}")
-    B, N, C = x.shape
-    code = _dtype_code(x, (NPA_DTYPE_BF16, NPA_DTYPE_FP16, NPA_DTYPE_FP32))
-    wcode = code
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is None:
-            continue
-        if t.shape != (C,) or not t.is_contiguous():
-            raise ValueError(f"{name}: expected a contiguous [{C}] tensor")
-        wcode = _dtype_code(t, (code, NPA_DTYPE_FP32))
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        raise ValueError("weight and bias must have one dtype")
-    if out is not None and (out.dtype != x.dtype or out.shape != x.shape):
+    w = (None, None, None) if weight is None else (weight.shape, weight.stride(), weight.dtype)
+    b = (None, None, None) if bias is None else (bias.shape, bias.stride(), bias.dtype)
+    sizes, xs, act_code, nbytes = _norm_plan(index, groups, act, x.shape, x.stride(), x.dtype, *w, *b)
+    _device_of(x, weight, bias, out)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif out.dtype != x.dtype or out.shape != x.shape:
         raise ValueError("out must have x's shape and dtype")
-    dev = _device_of(x, weight, bias, out)
-
-    def call():
-        y = torch.empty((B, N, C), dtype=x.dtype, device=dev) if out is None else out
-        xs, ys = x.stride(), y.stride()
-        if C > 1 and (xs[2] != 1 or ys[2] != 1):
-            raise ValueError("channels must be contiguous")
-        nbytes = _gn_workspace_size(dev.index, code, B, N, C, groups)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-        npa_group_norm_act(x, weight, bias, y, code, wcode, B, N, C, groups, xs[0], xs[1], ys[0], ys[1], float(eps),
-                           _ACTIVATIONS[act], ws, nbytes)
-        return y
-
-    return _run_on(dev, stream, call)
+    ys = out.stride()
+    if ys[2] != 1 and x.shape[2] > 1:
+        raise ValueError("channels must be contiguous")
+    ws = _empty_bytes(nbytes, x)
+    code = lib().npa_group_norm_act(x.data_ptr(), _ptr(weight), _ptr(bias), out.data_ptr(), *sizes, *xs, ys[0], ys[1],
+                                    float(eps), act_code, ws.data_ptr() if nbytes else None, nbytes, handle)
+    if code:
+        raise NpaError(code, "npa_group_norm_act")
+    return out

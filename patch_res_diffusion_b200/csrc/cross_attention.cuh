@@ -676,8 +676,8 @@ __device__ void xa_convert(const XaParams &p, uint8_t *smem, uint64_t *bars, vol
 // ---------------------------------------------------------------------------
 // Softmax and epilogue
 // ---------------------------------------------------------------------------
-// 32 * NCH scores of a row, unkept ones as -inf.
-template <int NCH>
+// 32 * NCH scores of a row, unkept ones as -inf (kMasked: there may be some).
+template <int NCH, bool kMasked = true>
 __device__ __forceinline__ void xa_load_scores(uint32_t t_s, const uint32_t (&w)[4], float (&s)[32 * NCH]) {
     if constexpr (NCH == 2) {
         uint32_t r[64];
@@ -699,7 +699,7 @@ __device__ __forceinline__ void xa_load_scores(uint32_t t_s, const uint32_t (&w)
         }
     }
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
+    for (int c = 0; kMasked && c < NCH; ++c) {
         if (w[c] != 0xffffffffu) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
@@ -801,18 +801,18 @@ struct XaSoftmax {
     // row of scores does not fit in the registers that its 512 threads leave.
     // The second half is read twice; P of the first may overwrite its own
     // scores (d = 128), not the second's.
-    template <int NCH>
+    template <int NCH, bool kMasked>
     __device__ __forceinline__ bool block8(const uint32_t (&w)[4], const XaScales &sc, bool first, bool turns) {
         constexpr int kA = NCH < 2 ? NCH : 2, kB = NCH - kA;  // 32-key pieces of the halves
         const uint32_t wb[4] = {w[2], w[3], 0, 0};
         float bm = -INFINITY;
         if constexpr (kB > 0) {
             float s[32 * kB];
-            xa_load_scores<kB>(tS + 64, wb, s);
+            xa_load_scores<kB, kMasked>(tS + 64, wb, s);
             bm = half_max(s, sc, 1);
         }
         float s[32 * kA];
-        xa_load_scores<kA>(tS, w, s);
+        xa_load_scores<kA, kMasked>(tS, w, s);
         if (kB == 0) release_scores();
         bm = fmaxf(bm, half_max(s, sc, 0));
         if (bm > R + kLead) R = bm - kBelow;
@@ -824,7 +824,7 @@ struct XaSoftmax {
         xa_store_p<kA>(tP, pk);
         if constexpr (kB > 0) {
             float t[32 * kB];
-            xa_load_scores<kB>(tS + 64, wb, t);
+            xa_load_scores<kB, kMasked>(tS + 64, wb, t);
             release_scores();
             uint32_t pt[16 * kB];
             l += half_exp(t, sc, 1, pt);
@@ -838,14 +838,14 @@ struct XaSoftmax {
     }
 
     // One block of at most 32 * NCH keys; false when a wait ran out.
-    template <int NCH>
+    template <int NCH, bool kMasked = true>
     __device__ __forceinline__ bool block(const uint32_t (&w)[4], const XaScales &sc, bool first, bool turns) {
         if constexpr (KV8) {
-            return block8<NCH>(w, sc, first, turns);
+            return block8<NCH, kMasked>(w, sc, first, turns);
         } else {
             constexpr int kN = 32 * NCH;
             float s[kN];
-            xa_load_scores<NCH>(tS, w, s);
+            xa_load_scores<NCH, kMasked>(tS, w, s);
             release_scores();
             const float bm = row_max<kN>(s) * p.scale_log2;
             if (bm > R + kLead) R = bm - kBelow;
@@ -931,7 +931,8 @@ __device__ void xa_softmax(const XaParams &p, uint8_t *smem, uint64_t *bars, uin
         for (int j = u.jb; j < u.je; ++j) {
             const int n = xa_block_keys(u, j);
             uint32_t w[4];
-            xa_keep(p, u, j, n, w);
+            const bool full = n == 128 && !p.key_mask;
+            if (!full) xa_keep(p, u, j, n, w);
             ok = warp_wait(&bars[C::bSFull + q], st.g & 1, lim);
             if (!ok) break;
             if constexpr (KV8) {
@@ -954,6 +955,8 @@ __device__ void xa_softmax(const XaParams &p, uint8_t *smem, uint64_t *bars, uin
             const bool first = j == u.jb;
             if (!active)
                 ok = st.idle_block(first, turns);
+            else if (full)
+                ok = st.template block<4, false>(w, sc, first, turns);
             else if (n > 96)
                 ok = st.template block<4>(w, sc, first, turns);
             else if (n > 64)
