@@ -699,25 +699,28 @@ bool encode_view(CUtensorMap *m, const View &v, bool f16, int rows = 128) {
 
 // How xa_fwd_kernel's units are shared out: whole units in waves, and whether
 // the last wave, which does not fill the GPU, is cut into pieces of the key
-// range. In key blocks of one CTA, a unit costs about two beyond its own, and
-// cut units five more for the merge.
+// range. In key blocks of one CTA, a unit costs about two beyond its own, a CTA's
+// two pieces six, and the merge six. (Uncut / cut: 37 / 44 us for 80 units of
+// 16 blocks, 866 / 719 us for 384 units of 128.)
 struct XaPlan {
-    int grid, waves, tail_ctas, tail_blocks;
+    int grid, waves, tail_ctas;
+    long long tail_blocks;
 };
 
 XaPlan plan_xa(long long units, long long n_blk, int sm_count, bool cut) {
     XaPlan pl;
     pl.grid = (int)std::min<long long>(units, sm_count);
     pl.waves = (int)((units + sm_count - 1) / sm_count);
-    pl.tail_ctas = pl.tail_blocks = 0;
+    pl.tail_ctas = 0;
+    pl.tail_blocks = 0;
     const long long whole = units / sm_count, rest = units % sm_count, blocks = rest * n_blk;
-    if (!cut || rest == 0 || blocks > (1 << 30)) return pl;
+    if (!cut || rest == 0 || blocks > (1 << 30) || sm_count > npa::kXaMaxTailCtas) return pl;
     const long long ctas = std::min<long long>(sm_count, (blocks + 1) / 2);
-    if (ctas <= rest || (blocks + ctas - 1) / ctas + 3 + 5 >= n_blk + 2) return pl;
+    if (ctas <= rest || (blocks + ctas - 1) / ctas + 12 >= n_blk + 2) return pl;
     pl.waves = (int)whole;
     pl.grid = (int)(whole ? sm_count : ctas);
     pl.tail_ctas = (int)ctas;
-    pl.tail_blocks = (int)blocks;
+    pl.tail_blocks = blocks;
     return pl;
 }
 
@@ -804,14 +807,37 @@ npa_status launch_xs_kernel(const XaCall &c, const npa::XaParams &a, int sm_coun
 // xa_few_kernel's splits.
 npa_status launch_combine(const XaCall &c, const npa::XaParams &a, npa_stream_t stream) {
     const int d = c.q.d;
-    npa::XaParams prm = a;
     const bool tail = a.tail_ctas > 0;
-    const int cut = a.tail_ctas ? a.tail_blocks / a.n_blk : 0;  // cut units
-    const long long rows = tail ? 256LL * cut : (long long)a.B * a.heads * a.Lq;
-    npa::XaCombineParams cp{a.o_part, a.ml, const_cast<void *>(c.o.ptr), c.o.sb, c.o.sh, c.o.st, a.n_splits,
-                            (int)rows, a.heads, a.Lq, a.n_units - cut};
-    void *tail_args[2] = {&prm, &cp}, *split_args[1] = {&cp};
-    void **args = tail ? tail_args : split_args;
+    npa::XaCombineParams cp;
+    std::memset(&cp, 0, sizeof(cp));
+    cp.o_part = a.o_part;
+    cp.ml = a.ml;
+    cp.o = const_cast<void *>(c.o.ptr);
+    cp.sb = c.o.sb;
+    cp.sh = c.o.sh;
+    cp.st = c.o.st;
+    cp.n_splits = a.n_splits;
+    cp.rows = a.B * a.heads * a.Lq;
+    cp.heads = a.heads;
+    cp.Lq = a.Lq;
+    unsigned grid = (unsigned)((cp.rows + 3) / 4);
+    if (tail) {
+        const int cut = a.tail_start[a.tail_ctas] / a.n_blk;  // cut units
+        cp.first_unit = a.n_units - cut;
+        cp.n_blk = a.n_blk;
+        cp.by_qpairs = a.by_qpairs;
+        cp.by_heads = a.by_heads;
+        cp.n_qpairs = a.n_qpairs;
+        std::memcpy(cp.tail_start, a.tail_start, sizeof(cp.tail_start));
+        for (int t = 0, cta = 0; t < cut; ++t) {
+            while (a.tail_start[cta + 1] <= t * a.n_blk) ++cta;
+            cp.first_cta[t] = (short)cta;
+            while (a.tail_start[cta + 1] < (t + 1) * a.n_blk) ++cta;
+            cp.last_cta[t] = (short)cta;
+        }
+        grid = 64u * cut;
+    }
+    void *args[1] = {&cp};
     const void *kernels[2][2][2] = {
         {{(const void *)npa::xa_combine_kernel<64, false>, (const void *)npa::xa_combine_kernel<64, true>},
          {(const void *)npa::xa_combine_kernel<128, false>, (const void *)npa::xa_combine_kernel<128, true>}},
@@ -824,7 +850,7 @@ npa_status launch_combine(const XaCall &c, const npa::XaParams &a, npa_stream_t 
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3((unsigned)((rows + 3) / 4));
+    cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(128);
     cfg.stream = (cudaStream_t)stream;
     cfg.attrs = &attr;
@@ -932,7 +958,8 @@ npa_status launch_xa(const XaCall &c, npa_stream_t stream) {
         pl = plan_xa(units, prm.n_blk, sm_count, false);
     prm.waves = pl.waves;
     prm.tail_ctas = pl.tail_ctas;
-    prm.tail_blocks = pl.tail_blocks;
+    for (int i = 0; i <= pl.tail_ctas && pl.tail_ctas; ++i)
+        prm.tail_start[i] = (int)(pl.tail_blocks * i / pl.tail_ctas);
     prm.ml = prm.o_part + (size_t)pl.tail_ctas * 512 * d;
     const void *kernel;
     unsigned threads, smem;

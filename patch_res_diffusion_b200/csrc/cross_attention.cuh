@@ -48,7 +48,8 @@
 namespace npa {
 
 constexpr int kKv8Block = 64;  // tokens of one head that share a scale of the 8-bit cache
-constexpr int kXaMaxSplits = 64;  // key-range splits at most
+constexpr int kXaMaxSplits = 64;      // xa_few_kernel's key-range splits at most
+constexpr int kXaMaxTailCtas = 160;   // CTAs that cut units are dealt to at most
 
 // n / d for 0 <= n < 2^31, d >= 1: with s = ceil(log2 d) and m = ceil(2^(31 +
 // s) / d), the product n m exceeds 2^(31 + s) n / d by less than 2^(31 + s) / d.
@@ -78,10 +79,11 @@ struct XaParams {
     int n_units;                       // 256-row units: B * heads * n_qpairs
     // Every CTA runs `waves` whole units (blockIdx.x, blockIdx.x + gridDim.x,
     // ...). The units after those, fewer than there are CTAs, are cut: their
-    // tail_blocks key blocks (n_blk each) are dealt evenly to the first
-    // tail_ctas CTAs, in order, and pieces of a unit are merged by
-    // xa_tail_kernel. tail_ctas = 0: nothing is cut.
-    int waves, tail_ctas, tail_blocks, n_blk;
+    // key blocks (n_blk each) are dealt evenly, in order, to the first
+    // tail_ctas CTAs (CTA c: tail_start[c] .. tail_start[c + 1]), and pieces of
+    // a unit are merged by xa_tail_kernel. tail_ctas = 0: nothing is cut.
+    int waves, tail_ctas, n_blk;
+    int tail_start[kXaMaxTailCtas + 1];
     FastDiv by_blk, by_qpairs, by_heads, by_group;
     float scale_log2;
     unsigned long long wait_limit_ns;
@@ -175,9 +177,6 @@ struct XaUnit {
     int slot;    // a piece of a unit: where its partial result goes; -1: the whole unit
 };
 
-// First tail block of CTA c.
-__host__ __device__ inline int xa_tail_start(int blocks, int ctas, int c) { return int((long long)blocks * c / ctas); }
-
 // The units of a CTA, in the order that all of its roles walk them.
 struct XaIter {
     const XaParams &p;
@@ -185,8 +184,8 @@ struct XaIter {
     int w = 0, pos = 0, start = 0, end = 0;
     __device__ __forceinline__ explicit XaIter(const XaParams &prm) : p(prm) {
         if (int(blockIdx.x) < p.tail_ctas) {
-            pos = start = xa_tail_start(p.tail_blocks, p.tail_ctas, blockIdx.x);
-            end = xa_tail_start(p.tail_blocks, p.tail_ctas, blockIdx.x + 1);
+            pos = start = p.tail_start[blockIdx.x];
+            end = p.tail_start[blockIdx.x + 1];
         }
     }
     __device__ __forceinline__ bool next() {
@@ -1127,97 +1126,65 @@ __global__ void __launch_bounds__(XaCfg<D, KV8>::kThreads, 1)
     }
 }
 
-// Merges xa_few_kernel's key-range splits: one warp per query row. With m* the largest
-// reference, o = sum_s 2^(m_s - m*) O_s / sum_s 2^(m_s - m*) l_s; a split
-// without keys has m_s = -inf and no O.
+// Merging partial results. With m* the largest reference of a row's pieces,
+//   o = sum_s 2^(m_s - m*) O_s / sum_s 2^(m_s - m*) l_s;
+// a piece without keys has m_s = -inf and wrote no O.
 struct XaCombineParams {
     const float *o_part, *ml;
     void *o;
     long long sb, sh, st;  // strides of o in elements
     int n_splits, rows, heads, Lq;
-    int first_unit;  // xa_tail_kernel: the first cut unit
+    // xa_tail_kernel: the first cut unit, and the CTAs that hold a cut unit's
+    // first and last block
+    int first_unit, n_blk;
+    FastDiv by_qpairs, by_heads;
+    int n_qpairs;
+    short first_cta[kXaMaxTailCtas], last_cta[kXaMaxTailCtas];
+    int tail_start[kXaMaxTailCtas];
 };
 
-// The cut units' pieces, one warp per query row: with c0 and c1 the CTAs that
-// hold the unit's first and last block, its pieces are the slots of c0 .. c1.
-template <int D, bool F16>
-__global__ void __launch_bounds__(128) xa_tail_kernel(const __grid_constant__ XaParams p, XaCombineParams o) {
-    constexpr int kPer = D / 32;
-    const int idx = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int t = idx >> 8, r = idx & 255;
-    sm100::wait_for_previous_kernel();
-    if (t >= p.n_units - o.first_unit) return;
-    const int bh = p.by_qpairs(o.first_unit + t), row = (o.first_unit + t - bh * p.n_qpairs) * 256 + r;
-    const int b0 = t * p.n_blk;
-    auto cta_of = [&](int block) { return int(((long long)(block + 1) * p.tail_ctas - 1) / p.tail_blocks); };
-    const int c0 = cta_of(b0), c1 = cta_of(b0 + p.n_blk - 1);
-    if (row >= p.Lq || c0 == c1) return;  // no row, or the unit was not cut
-    auto slot_row = [&](int c) {
-        const int slot = 2 * c + (xa_tail_start(p.tail_blocks, p.tail_ctas, c) < b0);
-        return (size_t)slot * 256 + r;
-    };
-    float m = -INFINITY, L = 0.f, acc[kPer];
-#pragma unroll
-    for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
-    for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(p.ml + slot_row(c) * 2));
-    for (int c = c0; c <= c1; ++c) {
-        const size_t pr = slot_row(c);
-        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.ml) + pr);
-        if (ml.x == -INFINITY) continue;  // a piece without keys wrote no O
-        const float wgt = sm100::ex2_approx(ml.x - m);
-        L = fmaf(wgt, ml.y, L);
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) acc[k] = fmaf(wgt, __ldcg(p.o_part + pr * D + lane * kPer + k), acc[k]);
-    }
-    const float inv = L > 0.f ? 1.f / L : L;
-    const int b = p.by_heads(bh), h = bh - b * p.heads;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(o.o) + b * o.sb + h * o.sh + row * o.st +
-                                                 lane * kPer);
-#pragma unroll
-    for (int k = 0; k < kPer; k += 2)
-        dst[k / 2] = L == 0.f ? 0u : sm100::pack_16x2<F16>(acc[k] * inv, acc[k + 1] * inv);
-}
-
-template <int D, bool F16>
-__global__ void __launch_bounds__(128) xa_combine_kernel(const __grid_constant__ XaCombineParams p) {
-    constexpr int kPer = D / 32;   // elements of O per lane
-    constexpr int kAhead = 8;      // splits whose loads are in flight together
-    const int r = blockIdx.x * 4 + (threadIdx.x >> 5);
+// One row by one warp: n <= 32 * kPerLane pieces, row_of(s) the row of piece s
+// in o_part and ml. References and sums are read together, O eight pieces at
+// a time.
+template <int D, bool F16, int kPerLane, typename RowOf>
+__device__ __forceinline__ void xa_merge_row(const XaCombineParams &p, int n, RowOf row_of, uint16_t *dst) {
+    constexpr int kPer = D / 32;  // elements of O per lane
+    constexpr int kAhead = 8;
     const int lane = threadIdx.x & 31;
-    sm100::wait_for_previous_kernel();
-    if (r >= p.rows) return;
-    static_assert(kXaMaxSplits == 64, "two splits per lane");
-    float2 ml[2];
+    float2 ml[kPerLane];
+    float m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        ml[i] = lane + 32 * i < p.n_splits
-                    ? __ldcg(reinterpret_cast<const float2 *>(p.ml) + (size_t)(lane + 32 * i) * p.rows + r)
-                    : make_float2(-INFINITY, 0.f);
-    float m = fmaxf(ml[0].x, ml[1].x);
+    for (int i = 0; i < kPerLane; ++i) {
+        ml[i] = lane + 32 * i < n ? __ldcg(reinterpret_cast<const float2 *>(p.ml) + row_of(lane + 32 * i))
+                                  : make_float2(-INFINITY, 0.f);
+        m = fmaxf(m, ml[i].x);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float w[2], L = 0.f;
+    float w[kPerLane], L = 0.f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kPerLane; ++i) {
         w[i] = ml[i].x == -INFINITY ? 0.f : sm100::ex2_approx(ml[i].x - m);
-        L = fmaf(w[i], ml[i].x == -INFINITY ? 0.f : ml[i].y, L);
+        L = ml[i].x == -INFINITY ? L : fmaf(w[i], ml[i].y, L);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     float acc[kPer];
 #pragma unroll
     for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
-    const float *part = p.o_part + (size_t)r * D + lane * kPer;
-    for (int s0 = 0; s0 < p.n_splits; s0 += kAhead) {
+    for (int s0 = 0; s0 < n; s0 += kAhead) {
         float o[kAhead][kPer], wgt[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int s = s0 + i;
-            const bool first = s < 32;
-            wgt[i] = __shfl_sync(0xffffffffu, first ? w[0] : w[1], s & 31);
-            const bool in = s < p.n_splits && wgt[i] != 0.f;  // a split without keys wrote no O
+            float mine = w[0];
 #pragma unroll
-            for (int c = 0; c < kPer; ++c) o[i][c] = in ? __ldcg(part + (size_t)s * p.rows * D + c) : 0.f;
+            for (int k = 1; k < kPerLane; ++k) mine = s >> 5 == k ? w[k] : mine;
+            wgt[i] = __shfl_sync(0xffffffffu, mine, s & 31);
+            const bool in = s < n && wgt[i] != 0.f;
+            const float *src = p.o_part + (in ? (size_t)row_of(s) * D : 0) + lane * kPer;
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) o[i][c] = in ? __ldcg(src + c) : 0.f;
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
@@ -1225,12 +1192,39 @@ __global__ void __launch_bounds__(128) xa_combine_kernel(const __grid_constant__
             for (int c = 0; c < kPer; ++c) acc[c] = fmaf(wgt[i], o[i][c], acc[c]);
     }
     const float inv = L > 0.f ? 1.f / L : L;
-    const int bh = r / p.Lq, i = r - bh * p.Lq, b = bh / p.heads, h = bh - b * p.heads;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.o) + b * p.sb + h * p.sh + i * p.st +
-                                                 lane * kPer);
 #pragma unroll
     for (int c = 0; c < kPer; c += 2)
-        dst[c / 2] = L == 0.f ? 0u : sm100::pack_16x2<F16>(acc[c] * inv, acc[c + 1] * inv);
+        reinterpret_cast<uint32_t *>(dst + lane * kPer)[c / 2] =
+            L == 0.f ? 0u : sm100::pack_16x2<F16>(acc[c] * inv, acc[c + 1] * inv);
+}
+
+// xa_few_kernel's key-range splits.
+template <int D, bool F16>
+__global__ void __launch_bounds__(128) xa_combine_kernel(const __grid_constant__ XaCombineParams p) {
+    const int r = blockIdx.x * 4 + (threadIdx.x >> 5);
+    sm100::wait_for_previous_kernel();
+    if (r >= p.rows) return;
+    const int bh = r / p.Lq, i = r - bh * p.Lq, b = bh / p.heads, h = bh - b * p.heads;
+    xa_merge_row<D, F16, kXaMaxSplits / 32>(
+        p, p.n_splits, [&](int s) { return (size_t)s * p.rows + r; },
+        static_cast<uint16_t *>(p.o) + b * p.sb + h * p.sh + i * p.st);
+}
+
+// The pieces of cut units: 64 blocks of four rows to a unit.
+template <int D, bool F16>
+__global__ void __launch_bounds__(128) xa_tail_kernel(const __grid_constant__ XaCombineParams p) {
+    const int t = blockIdx.x >> 6, r = (blockIdx.x & 63) * 4 + (threadIdx.x >> 5);
+    const int unit = p.first_unit + t, bh = p.by_qpairs(unit), row = (unit - bh * p.n_qpairs) * 256 + r;
+    const int c0 = p.first_cta[t], c1 = p.last_cta[t];
+    sm100::wait_for_previous_kernel();
+    if (row >= p.Lq || c0 == c1) return;  // no row, or the unit was not cut
+    const int b = p.by_heads(bh), h = bh - b * p.heads;
+    // a CTA's first piece is in its slot 0: of the unit's CTAs, only the first
+    // may have begun with another unit
+    const int begun = p.tail_start[c0] < t * p.n_blk;
+    xa_merge_row<D, F16, kXaMaxTailCtas / 32>(
+        p, c1 - c0 + 1, [&](int s) { return (size_t)(2 * (c0 + s) + (s == 0 ? begun : 0)) * 256 + r; },
+        static_cast<uint16_t *>(p.o) + b * p.sb + h * p.sh + row * p.st);
 }
 
 }  // namespace npa

@@ -81,7 +81,7 @@ def test_long_keys(npa, dtype, d):
     run_and_check(npa, q, k, v, dtype, what="units")
 
 
-@pytest.mark.parametrize("d,Lk,lens", [(64, 2500, None), (128, 1800, [1800, 700]), (64, 1290, [5, 1290])])
+@pytest.mark.parametrize("d,Lk,lens", [(64, 2500, None), (128, 1800, [1800, 700]), (64, 2200, [5, 2200])])
 def test_more_units_than_multiprocessors(npa, d, Lk, lens):
     """Whole units in waves, then the rest cut into pieces of the key range;
     batch rows whose keys end inside, before and after a piece."""
