@@ -305,9 +305,10 @@ npa_status npa_kv8_store(const void *k, const void *v, const npa_kv8_cache *cach
 
 /* npa_cross_attention_fwd over the first Lk tokens of an 8-bit cache (Lk <=
  * capacity); q and o are bfloat16. The codes enter the products exactly (as
- * float16, with the probabilities) and the scales in float32; scales must be
- * positive and finite, powers of two or not, and within one head the values'
- * scales less than 2^100 apart. Other arguments, results, workspace and errors as for npa_cross_attention_fwd. */
+ * float16, with the probabilities) and the scales in float32; the scales of
+ * blocks with kept keys must be positive and finite, powers of two or not, and
+ * within one head those of the values less than 2^100 apart. Other arguments,
+ * results, workspace and errors as for npa_cross_attention_fwd. */
 npa_status npa_kv8_cross_attention_fwd(const void *q, const npa_kv8_cache *cache, void *o, int B, int heads,
                                        int kv_heads, int Lq, int Lk, int d, const npa_strides *q_strides,
                                        const npa_strides *o_strides, const int32_t *kv_lens, const uint8_t *key_mask,

@@ -947,6 +947,8 @@ __device__ void xa_softmax(const XaParams &p, uint8_t *smem, uint64_t *bars, uin
                     sc.f[h] = fmaxf(f_row * ks[h], 1.2e-38f);  // above 0: -inf times it stays -inf
                     sc.lv[h] = __log2f(vs[h]);
                     sc.inv_v[h] = __fdividef(1.f, vs[h]);
+                    // none of its keys is kept: whatever its scales hold stays out
+                    if (!full && (w[2 * h] | w[2 * h + 1]) == 0u) sc.lv[h] = 0.f, sc.inv_v[h] = 1.f;
                 }
                 if (j + 1 < u.je) fetch_scales(j + 1);
             }

@@ -320,6 +320,7 @@ __global__ void __launch_bounds__(32 * kXaFewWarps, xa_few_per_sm(D, NT)) xa_few
                               : left >= W::kStep ? W::kAll
                                                  : (1u << left) - 1u;
         const float kscale = KV8 ? w.ks : 1.f;
+        if (KV8 && keep == 0u) w.vs = 0.f;  // no key of the step: its block's scale may be anything
         if (more) load_keys(j + kXaFewWarps);
         if (keep != W::kAll) {
 #pragma unroll

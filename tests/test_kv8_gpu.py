@@ -196,6 +196,25 @@ def test_attention_heads_lens_masks(npa, d):
         attend_and_check(npa, q, cache, n, key_mask=mask, kv_lens=lens, scale=0.3, split=False)
 
 
+@pytest.mark.parametrize("Lq", [1, 5, 140])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scales_of_blocks_without_kept_keys(npa, d, Lq):
+    """A block that the mask leaves out altogether was perhaps never stored:
+    its scales may hold anything, alone in a 128-key block or with its other half."""
+    B, n = 2, 500
+    cache = filled(npa, 75, B, 2, n, d)
+    mask = np.ones((B, n), dtype=bool)
+    nan, inf = float("nan"), float("inf")   # (the bound takes the largest finite value: no inf there)
+    for i, bad_k, bad_v in ((0, nan, nan), (3, inf, 0.0), (4, 0.0, nan), (5, -1.0, -1.0)):
+        mask[:, 64 * i:64 * i + 64] = False
+        cache.k_scale[:, :, i] = bad_k
+        cache.v_scale[:, :, i] = bad_v
+    mask[0, 64:100] = False
+    attend_and_check(npa, randn(76, B, 4, Lq, d), cache, n, key_mask=mask)
+    mask[1] = False
+    assert not attend_and_check(npa, randn(76, B, 4, Lq, d), cache, n, key_mask=mask)[1].any()
+
+
 def test_attention_layouts_and_guard(npa):
     B, h, Lq, n, d = 2, 3, 140, 200, 64
     cache = filled(npa, 80, B, h, n, d)
