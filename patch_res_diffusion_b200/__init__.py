@@ -40,6 +40,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 from typing import Optional
 
@@ -532,6 +533,8 @@ def _run_on(index, stream, body, *args):
     import torch
     if stream is None and index == torch.cuda.current_device():
         return body(*args, _raw_stream_of()(index))
+    if getattr(stream, "device_index", index) != index:
+        raise ValueError(f"stream of device {stream.device_index}, tensors on device {index}")
     with torch.cuda.device(index):
         if stream is None:
             return body(*args, _raw_stream_of()(index))
@@ -539,6 +542,14 @@ def _run_on(index, stream, body, *args):
             stream = torch.cuda.ExternalStream(int(stream), device=torch.device("cuda", index))
         with torch.cuda.stream(stream):
             return body(*args, int(stream.cuda_stream))
+
+
+def _int32(name, n) -> int:
+    """n as an int that the C call can take (ctypes would drop its upper bits)."""
+    n = operator.index(n)
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name}: {n} does not fit in 32 bits")
+    return n
 
 
 def _heads_strides(name, shape, strides, want):
@@ -562,9 +573,10 @@ def _kept_keys(kv_lens, key_mask, B, Lk):
 def _scale(scale) -> float:
     if scale is None:
         return 0.0
-    if not scale > 0:
-        raise ValueError(f"scale must be positive, got {scale}")
-    return float(scale)
+    scale = ctypes.c_float(scale).value   # as the C call gets it, where 0 means the default
+    if not 0 < scale < float("inf"):
+        raise ValueError(f"scale must be positive and finite in float32, got {scale}")
+    return scale
 
 
 def _like_strides(shape, strides):
@@ -584,8 +596,8 @@ def _cross_plan(index, split, q_shape, q_strides, k_shape, k_strides, v_shape, v
     """(sizes, strides and a fresh output's strides for the C call, workspace bytes)."""
     if len(q_shape) != 4 or len(k_shape) != 4:
         raise ValueError(f"expected [B, heads, L, d], got {tuple(q_shape)} and {tuple(k_shape)}")
-    B, heads, Lq, d = q_shape
-    kv_heads, Lk = k_shape[1], k_shape[2]
+    B, heads, Lq, d = (_int32("q", n) for n in q_shape)
+    kv_heads, Lk = (_int32("k", n) for n in k_shape[1:3])
     strides = (_heads_strides("q", q_shape, q_strides, q_shape),
                _heads_strides("k", k_shape, k_strides, (B, kv_heads, Lk, d)),
                _heads_strides("v", v_shape, v_strides, k_shape))
@@ -644,7 +656,7 @@ class Kv8Cache:
     ``k_scale``, ``v_scale`` [B, kv_heads, capacity / 64], value = code *
     scale. ``Kv8Cache.empty`` allocates one; ``kv8_store`` writes it."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "c_struct", "index")
+    __slots__ = ("_tensors", "index")
 
     def __init__(self, k, v, k_scale, v_scale):
         import torch
@@ -661,8 +673,17 @@ class Kv8Cache:
         if not (k.is_contiguous() and v.is_contiguous() and k_scale.is_contiguous() and v_scale.is_contiguous()):
             raise ValueError("a cache's tensors must be contiguous")
         self.index = _device_of(k, v, k_scale, v_scale)
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.c_struct = _Kv8Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k.shape[2])
+        _int32("capacity", k.shape[2])
+        self._tensors = (k, v, k_scale, v_scale)
+
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    k_scale = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
+
+    def c_struct(self):
+        k, v, k_scale, v_scale = self._tensors
+        return _Kv8Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k.shape[2])
 
     @classmethod
     def empty(cls, B: int, kv_heads: int, capacity: int, d: int, device="cuda") -> "Kv8Cache":
@@ -684,12 +705,13 @@ def _store_plan(cache_shape, k_shape, k_strides, v_shape, v_strides, k_dtype, v_
     B, kv_heads, _, d = cache_shape
     if len(k_shape) != 4:
         raise ValueError(f"expected [B, heads, L, d], got {tuple(k_shape)}")
+    n = _int32("k", k_shape[2])
     strides = (_heads_strides("k", k_shape, k_strides, (B, kv_heads, k_shape[2], d)),
                _heads_strides("v", v_shape, v_strides, k_shape))
     code = _dtype_code(k_dtype, (NPA_DTYPE_BF16, NPA_DTYPE_FP16))
     if v_dtype != k_dtype:
         raise ValueError("k and v must have one dtype")
-    return (code, B, kv_heads, d), k_shape[2], strides
+    return (code, B, kv_heads, d), n, strides
 
 
 def kv8_store(cache: Kv8Cache, k, v, start: int = 0, starts=None, stream=None) -> None:
@@ -706,7 +728,7 @@ def _kv8_store(cache, k, v, start, starts, handle):
                                not starts.is_contiguous()):
         raise ValueError(f"starts: expected a contiguous int32 tensor of {sizes[1]} positions")
     _device_of(cache.k, k, v, starts)
-    code = lib().npa_kv8_store(k.data_ptr(), v.data_ptr(), cache.c_struct, *sizes, start, _ptr(starts), n, *strides, handle)
+    code = lib().npa_kv8_store(k.data_ptr(), v.data_ptr(), cache.c_struct(), *sizes, _int32("start", start), _ptr(starts), n, *strides, handle)
     if code:
         raise NpaError(code, "npa_kv8_store")
 
@@ -716,10 +738,10 @@ def _kv8_plan(index, split, q_shape, q_strides, cache_shape, Lk, q_dtype):
     B, kv_heads, capacity, d = cache_shape
     if len(q_shape) != 4:
         raise ValueError(f"expected [B, heads, L, d], got {tuple(q_shape)}")
-    heads, Lq = q_shape[1], q_shape[2]
+    heads, Lq = (_int32("q", n) for n in q_shape[1:3])
     strides = _heads_strides("q", q_shape, q_strides, (B, heads, Lq, d))
     _dtype_code(q_dtype, (NPA_DTYPE_BF16,))
-    Lk = capacity if Lk is None else int(Lk)
+    Lk = capacity if Lk is None else _int32("n_tokens", Lk)
     nbytes = npa_cross_attention_workspace_size(B, heads, kv_heads, Lq, Lk, d) if split else 0   # current device: `index`
     return (B, heads, kv_heads, Lq, Lk, d), strides, _like_strides(q_shape, q_strides), nbytes
 
@@ -747,7 +769,7 @@ def _kv8_cross_attention(q, cache, n_tokens, kv_lens, key_mask, scale, out, spli
         o_strides = _heads_strides("out", out.shape, out.stride(), q.shape)
     ws = _empty_bytes(nbytes, q)
     code = lib().npa_kv8_cross_attention_fwd(
-        q.data_ptr(), cache.c_struct, out.data_ptr(), *sizes, q_strides, o_strides, lens, mask, _scale(scale),
+        q.data_ptr(), cache.c_struct(), out.data_ptr(), *sizes, q_strides, o_strides, lens, mask, _scale(scale),
         ws.data_ptr() if nbytes else None, nbytes, handle)
     if code:
         raise NpaError(code, "npa_kv8_cross_attention_fwd")
@@ -764,7 +786,8 @@ def _norm_plan(index, groups, act, x_shape, x_strides, x_dtype, w_shape, w_strid
         raise ValueError(f"expected [B, N, C], got {tuple(x_shape)}")
     if act not in _ACTIVATIONS:
         raise ValueError(f"unknown activation {act!r}")
-    B, N, C = x_shape
+    B, N, C = (_int32("x", n) for n in x_shape)
+    groups = _int32("groups", groups)
     code = wcode = _dtype_code(x_dtype, (NPA_DTYPE_BF16, NPA_DTYPE_FP16, NPA_DTYPE_FP32))
     for name, shape, strides, dtype in (("weight", w_shape, w_strides, w_dtype), ("bias", b_shape, b_strides, b_dtype)):
         if shape is None:

@@ -175,6 +175,49 @@ def test_helpers_refuse(L):
         npa.group_norm(t(2, 3, 64), 8, weight=torch.zeros(64, dtype=torch.float16))
 
 
+def test_helpers_refuse_numbers_that_the_c_call_would_change():
+    """ctypes drops an int's upper bits, and a float32 0 would mean the default scale."""
+    assert npa._scale(None) == 0 and npa._scale(0.125) == 0.125
+    for bad in (0, -1.0, float("nan"), float("inf"), 1e39, 1e-60):
+        with pytest.raises(ValueError):
+            npa._scale(bad)
+    assert npa._int32("n", 2 ** 31 - 1) == 2 ** 31 - 1
+    for bad in (2 ** 31, 2 ** 32 + 5, -2 ** 31 - 1):
+        with pytest.raises(ValueError):
+            npa._int32("n", bad)
+    shape, strides = (2, 4, 8, 64), (2048, 512, 64, 1)
+    for n in (2 ** 32 + 5, 2 ** 32):
+        with pytest.raises(ValueError):
+            npa._kv8_plan(0, False, shape, strides, (2, 4, 128, 64), n, torch.bfloat16)
+        with pytest.raises(ValueError):   # a head axis of stride 0
+            npa._kv8_plan(0, False, (2, n, 1, 64), (64, 0, 64, 1), (2, 4, 128, 64), None, torch.bfloat16)
+        with pytest.raises(ValueError):
+            npa._cross_plan(-1, False, shape, strides, (2, n, 8, 64), (512, 0, 64, 1), (2, n, 8, 64), (512, 0, 64, 1),
+                            *[torch.bfloat16] * 3)
+        with pytest.raises(ValueError):
+            npa._norm_plan(-1, 32 + n, None, (2, 3, 64), (192, 64, 1), torch.bfloat16, *[None] * 6)
+    with pytest.raises(TypeError):
+        npa._kv8_plan(0, False, shape, strides, (2, 4, 128, 64), 2.5, torch.bfloat16)
+
+
+def test_helpers_refuse_a_stream_of_another_device(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+
+    class Stream:
+        cuda_stream, device_index = 0, 1
+    with pytest.raises(ValueError, match="stream of device 1"):
+        npa._run_on(0, Stream(), lambda handle: None)
+
+
+def test_cache_tensors_stay(L):
+    """The tensors that were checked are the ones that a call gets."""
+    c = object.__new__(npa.Kv8Cache)
+    with pytest.raises(AttributeError):
+        c.k = torch.zeros(1)
+    with pytest.raises(AttributeError):
+        c.k_scale = torch.zeros(1)
+
+
 # ---------------------------------------------------------------------------
 # The oracle's pins
 # ---------------------------------------------------------------------------
