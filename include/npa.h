@@ -28,14 +28,19 @@
  * Around these it provides the stale-row form of PCPP that runs across
  * devices, the text-query half of joint attention (global tokens as queries),
  * the overlapping-window attention NPA is compared with, and the ASG guidance
- * combine; each declaration below cites its passage.
+ * combine; each declaration below cites its passage. Beside them stand the
+ * steps of the same transformer block that surround the self-attention: cross
+ * attention to an encoder's states (npa_cross_attention_fwd), the same over an
+ * 8-bit cache of those states (npa_kv8_store, npa_kv8_cross_attention_fwd) and
+ * the group norm (npa_group_norm_act); their types, strides and arithmetic are
+ * stated at their declarations.
  *
- * Arithmetic: bfloat16 inputs, float32 accumulation of Q.K^T and P.V on the
+ * Arithmetic of the patch-restricted forms: bfloat16 inputs, float32 accumulation of Q.K^T and P.V on the
  * tensor cores, float32 online softmax with scale 1/sqrt(d), bfloat16 output
  * rounded to nearest even. Softmax probabilities are rounded to bfloat16
  * before the P.V product.
  *
- * Layouts (all row-major, contiguous, little endian, 16-byte aligned):
+ * Their layouts (all row-major, contiguous, little endian, 16-byte aligned):
  *   q, k, v, o : bfloat16 [B, heads, H*W, d], token t = row*W + col
  *   global k, v: bfloat16 [B, heads, G, d]
  *
@@ -55,8 +60,10 @@
  * CUDA graphs: after a first call on a device (which checks the device and
  * sets kernel attributes), npa_attention_fwd, pcpp_attention_fwd,
  * pcpp_attention_fwd_stale, npa_global_query_attention_fwd,
- * npa_multidiffusion_attention_fwd and asg_guidance_combine may be captured in
- * a stream capture. The tensor maps are encoded on the host when the call is
+ * npa_multidiffusion_attention_fwd, asg_guidance_combine,
+ * npa_cross_attention_fwd, npa_kv8_store, npa_kv8_cross_attention_fwd and
+ * npa_group_norm_act may be captured in a stream capture (a first call of each
+ * of the last four sets that kernel family's attributes). The tensor maps are encoded on the host when the call is
  * captured, so the graph replays on the same buffers (their contents may
  * change between replays); npa_device_status synchronises and must not be
  * captured.
