@@ -699,27 +699,43 @@ bool encode_view(CUtensorMap *m, const View &v, bool f16, int rows = 128) {
 
 // How xa_fwd_kernel's units are shared out: whole units in waves, and whether
 // the last wave, which does not fill the GPU, is cut into pieces of the key
-// range. In key blocks of one CTA, a unit costs about two beyond its own, a CTA's
-// two pieces six, and the merge six. (Uncut / cut: 37 / 44 us for 80 units of
-// 16 blocks, 866 / 719 us for 384 units of 128.)
+// range. In key blocks of one CTA, a unit costs about two beyond its own, a
+// piece three, and the merge six. (Uncut / cut: 37 / 44 us for 80 units of 16
+// blocks, 866 / 719 us for 384 units of 128.) Cut units are dealt out either
+// evenly, where a CTA may hold the end of one unit and the beginning of the
+// next, or with the same number of CTAs to every unit, one piece each.
 struct XaPlan {
-    int grid, waves, tail_ctas;
-    long long tail_blocks;
+    int grid, waves, tail_ctas, per_unit;  // per_unit: CTAs of a cut unit, 0: dealt evenly
+    long long tail_blocks, n_blk;
+    int start(int cta) const {  // the first block of a CTA's share of the cut units
+        if (per_unit) return (int)(cta / per_unit * n_blk + cta % per_unit * n_blk / per_unit);
+        return (int)(tail_blocks * cta / tail_ctas);
+    }
 };
 
 XaPlan plan_xa(long long units, long long n_blk, int sm_count, bool cut) {
     XaPlan pl;
+    std::memset(&pl, 0, sizeof(pl));
+    pl.n_blk = n_blk;
     pl.grid = (int)std::min<long long>(units, sm_count);
     pl.waves = (int)((units + sm_count - 1) / sm_count);
-    pl.tail_ctas = 0;
-    pl.tail_blocks = 0;
     const long long whole = units / sm_count, rest = units % sm_count, blocks = rest * n_blk;
     if (!cut || rest == 0 || blocks > (1 << 30) || sm_count > npa::kXaMaxTailCtas) return pl;
-    const long long ctas = std::min<long long>(sm_count, (blocks + 1) / 2);
-    if (ctas <= rest || (blocks + ctas - 1) / ctas + 12 >= n_blk + 2) return pl;
+    long long ctas = std::min<long long>(sm_count, (blocks + 1) / 2);  // two blocks each at least
+    const long long per_unit = std::min(sm_count / rest, n_blk / 2);
+    auto share = [](long long all, long long parts) { return (all + parts - 1) / parts; };
+    long long best = n_blk + 2;
+    if (ctas > rest && share(blocks, ctas) + 12 < best) {
+        best = share(blocks, ctas) + 12;
+        pl.tail_ctas = (int)ctas;
+    }
+    if (per_unit > 1 && share(n_blk, per_unit) + 9 <= best) {
+        pl.per_unit = (int)per_unit;
+        pl.tail_ctas = (int)(per_unit * rest);
+    }
+    if (pl.tail_ctas == 0) return pl;
     pl.waves = (int)whole;
-    pl.grid = (int)(whole ? sm_count : ctas);
-    pl.tail_ctas = (int)ctas;
+    pl.grid = (int)(whole ? sm_count : pl.tail_ctas);
     pl.tail_blocks = blocks;
     return pl;
 }
@@ -959,7 +975,7 @@ npa_status launch_xa(const XaCall &c, npa_stream_t stream) {
     prm.waves = pl.waves;
     prm.tail_ctas = pl.tail_ctas;
     for (int i = 0; i <= pl.tail_ctas && pl.tail_ctas; ++i)
-        prm.tail_start[i] = (int)(pl.tail_blocks * i / pl.tail_ctas);
+        prm.tail_start[i] = pl.start(i);
     prm.ml = prm.o_part + (size_t)pl.tail_ctas * 512 * d;
     const void *kernel;
     unsigned threads, smem;

@@ -79,9 +79,9 @@ struct XaParams {
     int n_units;                       // 256-row units: B * heads * n_qpairs
     // Every CTA runs `waves` whole units (blockIdx.x, blockIdx.x + gridDim.x,
     // ...). The units after those, fewer than there are CTAs, are cut: their
-    // key blocks (n_blk each) are dealt evenly, in order, to the first
-    // tail_ctas CTAs (CTA c: tail_start[c] .. tail_start[c + 1]), and pieces of
-    // a unit are merged by xa_tail_kernel. tail_ctas = 0: nothing is cut.
+    // key blocks (n_blk each) go, in order, to the first tail_ctas CTAs (CTA
+    // c: tail_start[c] .. tail_start[c + 1]), and the pieces of a unit are
+    // merged by xa_tail_kernel. tail_ctas = 0: nothing is cut.
     int waves, tail_ctas, n_blk;
     int tail_start[kXaMaxTailCtas + 1];
     FastDiv by_blk, by_qpairs, by_heads, by_group;
