@@ -807,8 +807,8 @@ def group_norm(x, groups: int, weight=None, bias=None, eps: float = 1e-5, act: O
                stream=None):
     """Group norm with an activation (None or "silu") on a torch bf16, fp16 or
     fp32 CUDA tensor x [B, N, C], channels last and contiguous, batch and token
-    strides free; weight and bias [C] of x's dtype or float32. ``out=x`` works
-    in place. (A channels-last [B, C, H, W] tensor is ``x.permute(0, 2, 3,
+    strides free; weight and bias [C] of x's dtype or float32. ``out`` is laid
+    out like x by default; ``out=x`` works in place. (A channels-last [B, C, H, W] tensor is ``x.permute(0, 2, 3,
     1).flatten(1, 2)``.)"""
     index = x.get_device()
     if index < 0:
@@ -823,14 +823,15 @@ def _group_norm(index, x, groups, weight, bias, eps, act, out, handle):
     sizes, xs, act_code, nbytes = _norm_plan(index, groups, act, x.shape, x.stride(), x.dtype, *w, *b)
     _device_of(x, weight, bias, out)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x)
     elif out.dtype != x.dtype or out.shape != x.shape:
         raise ValueError("out must have x's shape and dtype")
     ys = out.stride()
     if ys[2] != 1 and x.shape[2] > 1:
         raise ValueError("channels must be contiguous")
     ws = _empty_bytes(nbytes, x)
-    code = lib().npa_group_norm_act(x.data_ptr(), _ptr(weight), _ptr(bias), out.data_ptr(), *sizes, *xs, ys[0], ys[1],
+    code = lib().npa_group_norm_act(x.data_ptr(), None if weight is None else weight.data_ptr(),
+                                    None if bias is None else bias.data_ptr(), out.data_ptr(), *sizes, *xs, ys[0], ys[1],
                                     float(eps), act_code, ws.data_ptr() if nbytes else None, nbytes, handle)
     if code:
         raise NpaError(code, "npa_group_norm_act")
