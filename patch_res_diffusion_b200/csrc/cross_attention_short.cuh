@@ -18,12 +18,20 @@
 // TMEM per warpgroup: S in columns 0..127; P over S's first 64; O in 64..127
 // (d = 64, over S: every row of it has been read when P V starts) or 128..255.
 // O leaves through the tile's own Q buffer, which the S product has read.
+//
+// Measured: 87 us for the size above (3.9 TB/s; the general kernel took 155, two
+// warpgroups that issue for themselves 107). No unit is busy more than 44% of
+// the time: what is left is each tile's chain (load, S, softmax, P V, store),
+// of which a multiprocessor has four under way. With 154 keys (two blocks) the
+// general kernel runs: 16 us for 2 x 10 heads x 4096 queries, d = 64.
 #pragma once
 
 #include "cross_attention.cuh"
 
 namespace npa {
 
+// Keys up to which this kernel runs: one S of the tensor memory's 128 columns.
+// Against xa_fwd_kernel: 87 / 155 us for 77 keys (2 x 10 heads x 65536 queries).
 constexpr int kXaShortKeys = 128;
 
 template <int D>
