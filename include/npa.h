@@ -264,11 +264,12 @@ typedef struct {
  * Arithmetic as for npa_attention_fwd; float16 inputs keep their probabilities
  * in float16 for the P.V product.
  * Where the queries alone would leave multiprocessors idle, the key range is
- * split over them: partial results go to `workspace` (caller-owned device
- * memory, 16-byte aligned; npa_cross_attention_workspace_size() bytes as
- * planned, and a smaller or NULL workspace gives fewer or no splits - the same
- * result up to rounding) and a second kernel on the same stream merges them. Calls that
- * overlap on the GPU need workspaces of their own. o and the workspace must
+ * split over them. Partial results are merged on chip where a few pieces are
+ * enough; else they go to `workspace` (caller-owned device memory, 16-byte
+ * aligned; npa_cross_attention_workspace_size() bytes as planned, and a smaller
+ * or NULL workspace gives fewer or no pieces - the same result up to rounding)
+ * and a second kernel on the same stream merges them. Calls that overlap on the
+ * GPU need workspaces of their own. o and the workspace must
  * not overlap each other or an input (address ranges, gaps between strided
  * rows included). */
 npa_status npa_cross_attention_fwd(const void *q, const void *k, const void *v, void *o, npa_dtype dtype, int B,

@@ -50,6 +50,8 @@ struct DeviceState {
     int l2_bytes = 0;
     bool xa_checked = false;  // the cross-attention kernels (on their first use)
     npa_status xa_status = NPA_ERR_UNSUPPORTED;
+    // clusters of xa_few_kernel that run at once: [d = 128][8-bit][two row tiles][size]
+    int xf_clusters[2][2][2][npa::kXaFewCluster + 1] = {};
     bool gn_checked = false;  // the group norm's kernels
     npa_status gn_status = NPA_ERR_UNSUPPORTED;
 };
@@ -613,8 +615,32 @@ bool prepare_xs_kernel() {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) == cudaSuccess;
 }
 
+// xa_few_kernel's dynamic shared memory.
+unsigned xf_smem(int d, int tiles) { return 8 * tiles * (npa::kXaFewWarps * (d + 2) + 2) * sizeof(float); }
+
+// How many clusters of each size run at once: out[size], of single blocks out[1].
+template <int D, bool KV8, int NT>
+bool count_xf_clusters(int (&out)[npa::kXaFewCluster + 1]) {
+    const void *kernel = (const void *)npa::xa_few_kernel<D, KV8, false, NT>;
+    for (int s = 1; s <= npa::kXaFewCluster; ++s) {
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = (unsigned)s;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg;
+        std::memset(&cfg, 0, sizeof(cfg));
+        cfg.gridDim = dim3((unsigned)s);
+        cfg.blockDim = dim3(32 * npa::kXaFewWarps);
+        cfg.dynamicSmemBytes = xf_smem(D, NT);
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&out[s], kernel, &cfg) != cudaSuccess || out[s] < 1) return false;
+    }
+    return true;
+}
+
 // ensure_ready plus the cross-attention kernels' limits, once per device.
-npa_status ensure_xa_ready(int *sm_count) {
+npa_status ensure_xa_ready(int *sm_count, const DeviceState **state = nullptr) {
     const npa_status st = ensure_ready(sm_count);
     if (st != NPA_OK) return st;
     int dev = 0;
@@ -626,10 +652,19 @@ npa_status ensure_xa_ready(int *sm_count) {
                         prepare_xa_kernel<128, false, false>() && prepare_xa_kernel<128, false, true>() &&
                         prepare_xa_kernel<64, true, false>() && prepare_xa_kernel<128, true, false>() &&
                         prepare_xs_kernel<64, false>() && prepare_xs_kernel<64, true>() &&
-                        prepare_xs_kernel<128, false>() && prepare_xs_kernel<128, true>();
+                        prepare_xs_kernel<128, false>() && prepare_xs_kernel<128, true>() &&
+                        count_xf_clusters<64, false, 1>(ds.xf_clusters[0][0][0]) &&
+                        count_xf_clusters<64, false, 2>(ds.xf_clusters[0][0][1]) &&
+                        count_xf_clusters<64, true, 1>(ds.xf_clusters[0][1][0]) &&
+                        count_xf_clusters<64, true, 2>(ds.xf_clusters[0][1][1]) &&
+                        count_xf_clusters<128, false, 1>(ds.xf_clusters[1][0][0]) &&
+                        count_xf_clusters<128, false, 2>(ds.xf_clusters[1][0][1]) &&
+                        count_xf_clusters<128, true, 1>(ds.xf_clusters[1][1][0]) &&
+                        count_xf_clusters<128, true, 2>(ds.xf_clusters[1][1][1]);
         ds.xa_status = ok ? NPA_OK : NPA_ERR_UNSUPPORTED;
         ds.xa_checked = true;
     }
+    if (state) *state = &ds;  // not written again
     return ds.xa_status;
 }
 
@@ -740,12 +775,37 @@ XaPlan plan_xa(long long units, long long n_blk, int sm_count, bool cut) {
     return pl;
 }
 
-// Key-range splits of xa_few_kernel: as many CTAs as run at once, each with two
-// steps or more for every warp.
-int plan_xf_splits(long long units, int rows, int Lk, int d, int sm_count) {
-    const long long want = (long long)npa::xa_few_per_sm(d, rows > 8 ? 2 : 1) * sm_count / units;
-    const long long most = ((long long)Lk + 255) / 256;
-    return (int)std::max(1LL, std::min({want, most, (long long)npa::kXaMaxSplits}));
+// Key-range splits of xa_few_kernel. In steps of a warp: with the splits as a
+// cluster, the longest warp's, times the waves in which the clusters run; with
+// as many blocks as run at once and a merge through the workspace, the longest
+// warp's and about four more. (Cluster / workspace, us: 12.1 / 14.9 for 2 x 20
+// heads, 16 queries, 4111 keys at d = 64, where a warp has 5 or 3 steps; 23.1 /
+// 19.6 for one query over 16384 cached keys, 16 or 10 steps.) Without room for
+// the latter in the workspace, the former.
+struct XfPlan {
+    int splits;
+    bool cluster;
+};
+
+XfPlan plan_xf(const DeviceState &ds, long long units, int rows, int Lk, int d, bool kv8, size_t held) {
+    const int tiles = rows > 8 ? 2 : 1;
+    const long long step = !kv8 && d == 128 ? 16 : 32, steps = (Lk + step - 1) / step;
+    auto longest = [&](long long splits) { return (steps + splits * npa::kXaFewWarps - 1) / (splits * npa::kXaFewWarps); };
+    XfPlan pl{1, false};
+    long long best = LLONG_MAX;
+    for (int s = 1; s <= npa::kXaFewCluster; ++s) {
+        const long long at_once = ds.xf_clusters[d == 128][kv8][tiles - 1][s];
+        const long long cost = (units + at_once - 1) / at_once * longest(s);
+        if (cost < best) {
+            best = cost;
+            pl = XfPlan{s, s > 1};
+        }
+    }
+    // a split has two steps or more for every warp
+    const long long fit = (long long)npa::xa_few_per_sm(d, tiles) * ds.sm_count / units, most = ((long long)Lk + 255) / 256;
+    const long long want = std::min({fit, most, (long long)npa::kXaMaxSplits, (long long)std::min<size_t>(held, npa::kXaMaxSplits)});
+    if (want > pl.splits && longest(want) + 4 < best) pl = XfPlan{(int)want, false};
+    return pl;
 }
 
 bool xa_few_rows(int heads, int kv_heads, int Lq) {
@@ -875,7 +935,7 @@ npa_status launch_combine(const XaCall &c, const npa::XaParams &a, npa_stream_t 
 }
 
 template <int D, bool KV8, bool F16>
-npa_status launch_xf_kernel(const XaCall &c, const npa::XaParams &a, npa_stream_t stream) {
+npa_status launch_xf_kernel(const XaCall &c, const npa::XaParams &a, bool cluster, npa_stream_t stream) {
     npa::XfParams prm;
     std::memset(&prm, 0, sizeof(prm));
     prm.q = c.q.ptr;
@@ -893,23 +953,33 @@ npa_status launch_xf_kernel(const XaCall &c, const npa::XaParams &a, npa_stream_
     prm.scale_blocks = a.scale_blocks;
     prm.B = a.B, prm.heads = a.heads, prm.kv_heads = a.kv_heads, prm.group = a.group, prm.Lq = a.Lq, prm.Lk = a.Lk;
     prm.n_splits = a.n_splits;
+    prm.cluster = cluster;
     prm.scale_log2 = a.scale_log2;
     prm.o_part = a.o_part;
     prm.ml = a.ml;
     const int tiles = a.group * a.Lq > 8 ? 2 : 1;
-    const unsigned smem = npa::kXaFewWarps * 8 * tiles * (D + 2) * sizeof(float);
     const void *kernel = tiles == 2 ? (const void *)npa::xa_few_kernel<D, KV8, F16, 2>
                                     : (const void *)npa::xa_few_kernel<D, KV8, F16, 1>;
     void *args[1] = {&prm};
-    return cudaLaunchKernel(kernel, dim3((unsigned)(a.B * a.kv_heads * a.n_splits)), dim3(32 * npa::kXaFewWarps), args,
-                            smem, (cudaStream_t)stream) == cudaSuccess
-               ? NPA_OK
-               : NPA_ERR_CUDA;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)a.n_splits;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3((unsigned)(a.B * a.kv_heads * a.n_splits));
+    cfg.blockDim = dim3(32 * npa::kXaFewWarps);
+    cfg.dynamicSmemBytes = xf_smem(D, tiles);
+    cfg.stream = (cudaStream_t)stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = cluster ? 1 : 0;
+    return cudaLaunchKernelExC(&cfg, kernel, args) == cudaSuccess ? NPA_OK : NPA_ERR_CUDA;
 }
 
 npa_status launch_xa(const XaCall &c, npa_stream_t stream) {
     int sm_count = 0;
-    const npa_status st = ensure_xa_ready(&sm_count);
+    const DeviceState *ds = nullptr;
+    const npa_status st = ensure_xa_ready(&sm_count, &ds);
     if (st != NPA_OK) return st;
     const int B = c.q.B, heads = c.q.heads, Lq = c.q.L, d = c.q.d, Lk = c.k.L;
     npa::XaParams prm;
@@ -943,22 +1013,22 @@ npa_status launch_xa(const XaCall &c, npa_stream_t stream) {
     prm.o_part = static_cast<float *>(c.workspace);
     const bool kv8 = c.k_scale != nullptr;
     if (xa_few_rows(heads, c.k.heads, Lq)) {
-        // as many splits as planned and as the workspace holds (one needs none)
-        const size_t held = c.workspace ? c.workspace_bytes / xa_split_bytes(B, heads, Lq, d) : 1;
-        prm.n_splits = plan_xf_splits((long long)B * c.k.heads, prm.group * Lq, Lk, d, sm_count);
-        if ((size_t)prm.n_splits > held) prm.n_splits = (int)std::max<size_t>(held, 1);
-        prm.ml = prm.n_splits > 1 ? prm.o_part + (size_t)prm.n_splits * B * heads * Lq * d : nullptr;
+        const size_t held = c.workspace ? c.workspace_bytes / xa_split_bytes(B, heads, Lq, d) : 0;
+        const XfPlan pl = plan_xf(*ds, (long long)B * c.k.heads, prm.group * Lq, Lk, d, kv8, held);
+        const bool cluster = pl.cluster;
+        prm.n_splits = pl.splits;
+        prm.ml = pl.splits > 1 && !cluster ? prm.o_part + (size_t)prm.n_splits * B * heads * Lq * d : nullptr;
         npa_status s;
         if (kv8)
-            s = d == 64 ? launch_xf_kernel<64, true, false>(c, prm, stream)
-                        : launch_xf_kernel<128, true, false>(c, prm, stream);
+            s = d == 64 ? launch_xf_kernel<64, true, false>(c, prm, cluster, stream)
+                        : launch_xf_kernel<128, true, false>(c, prm, cluster, stream);
         else if (d == 64)
-            s = c.f16 ? launch_xf_kernel<64, false, true>(c, prm, stream)
-                      : launch_xf_kernel<64, false, false>(c, prm, stream);
+            s = c.f16 ? launch_xf_kernel<64, false, true>(c, prm, cluster, stream)
+                      : launch_xf_kernel<64, false, false>(c, prm, cluster, stream);
         else
-            s = c.f16 ? launch_xf_kernel<128, false, true>(c, prm, stream)
-                      : launch_xf_kernel<128, false, false>(c, prm, stream);
-        return s != NPA_OK || prm.n_splits == 1 ? s : launch_combine(c, prm, stream);
+            s = c.f16 ? launch_xf_kernel<128, false, true>(c, prm, cluster, stream)
+                      : launch_xf_kernel<128, false, false>(c, prm, cluster, stream);
+        return s != NPA_OK || !prm.ml ? s : launch_combine(c, prm, stream);
     }
     if (!encode_view(&prm.tm_q, c.q, c.f16) || !encode_view(&prm.tm_o, c.o, c.f16)) return NPA_ERR_CUDA;
     if (!kv8 && Lk <= npa::kXaShortKeys)
@@ -1381,12 +1451,16 @@ npa_status asg_guidance_combine(const void *eps, const void *eps_ref, const void
 
 size_t npa_cross_attention_workspace_size(int B, int heads, int kv_heads, int Lq, int Lk, int d) {
     if (validate_xa_sizes(B, heads, kv_heads, Lq, Lk, d, 0.f, nullptr) != NPA_OK) return 0;
-    int dev = 0, sm = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
+    int sm = 0;
+    const DeviceState *ds = nullptr;
+    if (ensure_xa_ready(&sm, &ds) != NPA_OK) return 0;
     if (xa_few_rows(heads, kv_heads, Lq)) {
-        const int s = plan_xf_splits((long long)B * kv_heads, heads / kv_heads * Lq, Lk, d, sm);
-        return s > 1 ? (size_t)s * xa_split_bytes(B, heads, Lq, d) : 0;
+        int splits = 0;  // of 16-bit keys or the cache, whichever has more
+        for (const bool kv8 : {false, true}) {
+            const XfPlan pl = plan_xf(*ds, (long long)B * kv_heads, heads / kv_heads * Lq, Lk, d, kv8, SIZE_MAX);
+            if (!pl.cluster && pl.splits > splits) splits = pl.splits;
+        }
+        return splits > 1 ? (size_t)splits * xa_split_bytes(B, heads, Lq, d) : 0;
     }
     const XaPlan pl = plan_xa((long long)B * heads * ((Lq + 255) / 256), ((long long)Lk + 127) / 128, sm, true);
     return xa_tail_bytes(pl.tail_ctas, d);

@@ -23,24 +23,28 @@
 // rounded to 16 bits.
 //
 // The key range is split over CTAs and over a CTA's four warps; the warps merge
-// through shared memory, the CTAs through xa_combine_kernel. The softmax
-// reference moves lazily as in npa_fwd_kernel.cuh.
+// through shared memory, the CTAs as a cluster through each other's shared
+// memory, or, where more than eight of them pay, through a workspace and
+// xa_combine_kernel. The softmax reference moves lazily as in npa_fwd_kernel.cuh.
 //
 // Measured: 23 us for the size above (18 us of it this kernel, 4.6 TB/s, the
-// rest the merge and the launches), 20 us for 2 x 20 heads x 16 queries x 4111
-// masked 16-bit keys (42 MB, 6.5 us), 3.9 us for one query of 10 heads over 77 keys.
+// rest the merge and the launches), 15 us for 2 x 20 heads x 16 queries x 4111
+// masked 16-bit keys (42 MB, 6.5 us), 3.7 us for one query of 10 heads over 77 keys.
 #pragma once
+
+#include <cooperative_groups.h>
 
 #include "cross_attention.cuh"
 
 namespace npa {
 
 // Rows up to which this kernel runs: two 8-row tiles. Against xa_fwd_kernel
-// with its cut units (keys in L2): 16 x 4111 keys of 2 x 20 heads at d = 64 14.8
-// / 21.6 us, of 24 heads at d = 128 17.3 / 18.5; one query of 10 heads x 77 keys
+// with its cut units (keys in L2): 16 x 4111 keys of 2 x 20 heads at d = 64 12.3
+// / 21.6 us, of 24 heads at d = 128 14.7 / 18.5; one query of 10 heads x 77 keys
 // 3.3 / 6.7; one query x 16384 cached keys of 2 x 20 heads 19.8 / 66.4.
 constexpr int kXaFewRows = 16;
 constexpr int kXaFewWarps = 4;
+constexpr int kXaFewCluster = 8;  // splits that merge inside a cluster at most (the portable size)
 // CTAs that run on a multiprocessor at once, by their registers.
 __host__ __device__ constexpr int xa_few_per_sm(int d, int row_tiles) { return d == 64 ? (row_tiles == 1 ? 4 : 3) : 2; }
 
@@ -54,8 +58,9 @@ struct XfParams {
     int scale_blocks;
     int B, heads, kv_heads, group, Lq, Lk;
     int n_splits;
+    int cluster;  // the splits of a unit are one cluster and merge there
     float scale_log2;
-    float *o_part, *ml;  // n_splits > 1, as in XaParams
+    float *o_part, *ml;  // n_splits > 1 without a cluster, as in XaParams
 };
 
 template <bool F16>
@@ -225,7 +230,8 @@ template <int D, bool KV8, bool F16, int NT>
 __global__ void __launch_bounds__(32 * kXaFewWarps, xa_few_per_sm(D, NT)) xa_few_kernel(const __grid_constant__ XfParams p) {
     using W = XfWarp<D, KV8, F16, NT>;
     sm100::let_next_kernel_start();
-    extern __shared__ float xf_smem[];  // [warps][8 NT][D] O, then [warps][8 NT][2] reference and sum
+    // [warps][8 NT][D] O, then [warps][8 NT][2] reference and sum, then the block's merged [8 NT][2]
+    extern __shared__ float xf_smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int unit = blockIdx.x / p.n_splits, split = blockIdx.x - unit * p.n_splits;
     const int b = unit / p.kv_heads, kvh = unit - b * p.kv_heads;
@@ -386,6 +392,7 @@ __global__ void __launch_bounds__(32 * kXaFewWarps, xa_few_per_sm(D, NT)) xa_few
     constexpr int kRows = 8 * NT;
     float *sm_o = xf_smem + (size_t)warp * kRows * D;
     float2 *sm_ml = reinterpret_cast<float2 *>(xf_smem + kXaFewWarps * kRows * D);
+    float2 *merged_ml = sm_ml + kXaFewWarps * kRows;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         float l = w.l[n];
@@ -419,7 +426,10 @@ __global__ void __launch_bounds__(32 * kXaFewWarps, xa_few_per_sm(D, NT)) xa_few
             y = fmaf(wgt, o.y, y);
         }
         const int hd = r / p.Lq, i = r - hd * p.Lq, h = kvh * p.group + hd;
-        if (p.n_splits > 1) {
+        if (p.cluster) {  // (r, d) of the warps' results is read by this thread alone
+            *reinterpret_cast<float2 *>(xf_smem + r * D + d) = make_float2(x, y);
+            if (d == 0) merged_ml[r] = make_float2(m, L);
+        } else if (p.n_splits > 1) {
             const size_t row = ((size_t)b * p.heads + h) * p.Lq + i;
             const size_t part = (size_t)split * p.B * p.heads * p.Lq + row;
             *reinterpret_cast<float2 *>(p.o_part + part * D + d) = make_float2(x, y);
@@ -430,6 +440,37 @@ __global__ void __launch_bounds__(32 * kXaFewWarps, xa_few_per_sm(D, NT)) xa_few
             *reinterpret_cast<uint32_t *>(dst) = L == 0.f ? 0u : sm100::pack_16x2<F16>(x * inv, y * inv);
         }
     }
+    if (!p.cluster) return;
+    // the splits are the blocks of a cluster: each merges a share of the row
+    // elements from everyone's shared memory
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    for (int idx = split * 32 * kXaFewWarps + threadIdx.x; idx < rows * (D / 2); idx += p.n_splits * 32 * kXaFewWarps) {
+        const int r = idx / (D / 2), d = (idx - r * (D / 2)) * 2;
+        float2 ml[kXaFewCluster], o[kXaFewCluster];
+        float m = -INFINITY, L = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+        for (int i = 0; i < kXaFewCluster; ++i) {
+            const bool in = i < p.n_splits;
+            ml[i] = in ? *cluster.map_shared_rank(merged_ml + r, i) : make_float2(-INFINITY, 0.f);
+            o[i] = in ? *cluster.map_shared_rank(reinterpret_cast<float2 *>(xf_smem + r * D + d), i) : make_float2(0.f, 0.f);
+            m = fmaxf(m, ml[i].x);
+        }
+#pragma unroll
+        for (int i = 0; i < kXaFewCluster; ++i) {
+            if (ml[i].x == -INFINITY) continue;
+            const float wgt = sm100::ex2_approx(ml[i].x - m);
+            L = fmaf(wgt, ml[i].y, L);
+            x = fmaf(wgt, o[i].x, x);
+            y = fmaf(wgt, o[i].y, y);
+        }
+        const int hd = r / p.Lq, i = r - hd * p.Lq, h = kvh * p.group + hd;
+        const float inv = L > 0.f ? 1.f / L : L;
+        uint16_t *dst = static_cast<uint16_t *>(p.o) + b * p.osb + h * p.osh + i * p.ost + d;
+        *reinterpret_cast<uint32_t *>(dst) = L == 0.f ? 0u : sm100::pack_16x2<F16>(x * inv, y * inv);
+    }
+    cluster.sync();  // nobody's shared memory goes while it is read
 }
 
 }  // namespace npa

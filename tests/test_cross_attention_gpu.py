@@ -70,6 +70,23 @@ def test_every_tail(npa, d, Lk):
     run_and_check(npa, q, k, v, "bf16", what=Lk)
 
 
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "fp16"), (64, "fp16"), (128, "bf16")])
+def test_few_rows_split_in_every_way(npa, d, dtype):
+    """At most 16 rows: whole, split inside clusters of each size, split through
+    the workspace; pieces without keys, rows without keys, more units than run at once."""
+    for i, (B, heads, kv_heads, Lq, Lk) in enumerate(((1, 1, 1, 1, 40), (2, 2, 2, 3, 300), (1, 3, 3, 16, 600), (3, 6, 2, 5, 900),
+                                                      (4, 20, 20, 1, 1200), (2, 20, 20, 9, 1500), (3, 10, 10, 2, 2100),
+                                                      (1, 2, 1, 8, 5000), (30, 20, 20, 1, 260))):
+        lens = np.random.default_rng(i).integers(0, Lk + 1, B)
+        lens[0] = Lk
+        if B > 2:
+            lens[1:3] = 0, 1
+        mask = np.random.default_rng(i).random((B, Lk)) < 0.3
+        q, k, v = qkv(700 + i, B, heads, kv_heads, Lq, Lk, d, dtype)
+        for kw in ({}, {"kv_lens": lens.tolist()}, {"key_mask": mask, "split": False}):
+            run_and_check(npa, q, k, v, dtype, what=(i, list(kw)), **kw)
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 64), ("fp16", 64), ("bf16", 128), ("fp16", 128)])
 def test_long_keys(npa, dtype, d):
     """Many blocks: ring wrap-around, rescaling, splits; and many units of
