@@ -60,7 +60,8 @@ struct XsCfg {
     static constexpr int bP = bS + NW;           // [NW] P written (128 arrivals)
     static constexpr int bO = bP + NW;           // [NW] O written (MMA commit)
     static constexpr int bE = bO + NW;           // [NW] O staged (128 arrivals)
-    static constexpr int bDrain = bE + NW;       // [NW]
+    static constexpr int bSet = bE + NW;         // [NW] the issuer has moved to another key/value set
+    static constexpr int bDrain = bSet + NW;     // [NW]
     static constexpr int kNumBars = bDrain + NW;
     static constexpr int kMiscBytes = kNumBars * 8 + 16 + 2 * 32;  // barriers; TMEM base and abort flag; kept keys
     __host__ __device__ static constexpr int kv_stage_bytes(int rows) { return 2 * kChunks * rows * 128; }
@@ -220,8 +221,11 @@ __device__ void xs_issue(const XsParams &p, uint8_t *smem, uint8_t *kv, uint64_t
             ok = false;
             break;
         }
-        if (set != seq) advance(set);
-        if (!ok) break;
+        if (set != seq) {
+            advance(set);
+            if (!ok) break;
+            sm100::mbar_arrive(&bars[C::bSet + wg]);
+        }
         const int stage = seq % p.kv_stages;
         const int n = more ? int(kept[stage * 8 + 4]) : 0;
         const uint64_t v = v_desc + uint64_t((stage * stage_bytes) >> 4);
@@ -312,13 +316,18 @@ __device__ void xs_compute(const XsParams &p, uint8_t *smem, uint64_t *bars, con
     xs_tiles(p, &t0, &t1);
     const int bh0 = p.by_qtiles(t0);
     int seq = -1, i = 0, m = 0;  // as in xs_issue
+    int sets = 0;                // sets used so far
     bool ok = true;
     for (int t = t0 + wg; t < t1; t += C::NW, ++i) {
         const int bh = p.by_qtiles(t);
         const int row0 = (t - bh * p.n_qtiles) * 128;
-        if (seq != bh - bh0) {  // this set is not released before the tile is done; the ones between may be gone
+        if (seq != bh - bh0) {
+            // The issuer says when: it walks every set, and it is never more
+            // than this tile ahead. The set's own barrier could be a phase or
+            // more away from the one wanted, where sets between are skipped.
+            // The set is not released before the tile is done.
             seq = bh - bh0;
-            ok = warp_wait(&bars[C::bKVReady + seq % p.kv_stages], (seq / p.kv_stages) & 1, lim);
+            ok = warp_wait(&bars[C::bSet + wg], (sets++) & 1, lim);
             if (!ok) break;
         }
         const uint32_t *keep = kept + seq % p.kv_stages * 8;
@@ -436,6 +445,7 @@ __global__ void __launch_bounds__(XsCfg<D>::kThreads, 1) xa_short_kernel(const _
             sm100::mbar_init(&bars[C::bP + w], 128);
             sm100::mbar_init(&bars[C::bO + w], 1);
             sm100::mbar_init(&bars[C::bE + w], 128);
+            sm100::mbar_init(&bars[C::bSet + w], 1);
             sm100::mbar_init(&bars[C::bDrain + w], 1);
         }
         misc[1] = 0;

@@ -87,6 +87,23 @@ def test_few_rows_split_in_every_way(npa, d, dtype):
             run_and_check(npa, q, k, v, dtype, what=(i, list(kw)), **kw)
 
 
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "fp16")])
+def test_many_rows_of_one_tile(npa, d, dtype):
+    """Every tile has keys of its own (at most 128 queries a head), of another
+    length than its neighbours': a warpgroup's tiles skip key sets."""
+    B, Lk = 1400, 77
+    rng = np.random.default_rng(17)
+    lens = rng.integers(0, Lk + 1, B)
+    lens[rng.random(B) < 0.3] = 0
+    mask = rng.random((B, Lk)) < 0.5
+    mask[::3] = False
+    for heads, kv_heads, Lq, Bi in ((1, 1, 20, B), (2, 1, 17, 700), (3, 3, 128, 300), (1, 1, 130, 700)):
+        q, k, v = qkv(800 + Lq, Bi, heads, kv_heads, Lq, Lk, d, dtype)
+        run_and_check(npa, q, k, v, dtype, kv_lens=lens[:Bi].tolist(), what=(heads, Lq, "lens"))
+        run_and_check(npa, q, k, v, dtype, key_mask=mask[:Bi], what=(heads, Lq, "mask"))
+        run_and_check(npa, q, k, v, dtype, what=(heads, Lq))
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 64), ("fp16", 64), ("bf16", 128), ("fp16", 128)])
 def test_long_keys(npa, dtype, d):
     """Many blocks: ring wrap-around, rescaling, splits; and many units of
