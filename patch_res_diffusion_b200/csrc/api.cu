@@ -904,6 +904,9 @@ npa_status launch_combine(const XaCall &c, const npa::XaParams &a, npa_stream_t 
         cp.by_qpairs = a.by_qpairs;
         cp.by_heads = a.by_heads;
         cp.n_qpairs = a.n_qpairs;
+        cp.kv_lens = a.sort_rows ? a.kv_lens : nullptr;
+        cp.B = a.B;
+        cp.Lk = a.Lk;
         std::memcpy(cp.tail_start, a.tail_start, sizeof(cp.tail_start));
         for (int t = 0, cta = 0; t < cut; ++t) {
             while (a.tail_start[cta + 1] <= t * a.n_blk) ++cta;
@@ -1042,6 +1045,7 @@ npa_status launch_xa(const XaCall &c, npa_stream_t stream) {
     XaPlan pl = plan_xa(units, prm.n_blk, sm_count, true);
     if (pl.tail_ctas && (!c.workspace || c.workspace_bytes < xa_tail_bytes(pl.tail_ctas, d)))
         pl = plan_xa(units, prm.n_blk, sm_count, false);
+    prm.sort_rows = prm.kv_lens && B > 1 && B <= npa::kXaMaxSortedRows && units > sm_count;
     prm.waves = pl.waves;
     prm.tail_ctas = pl.tail_ctas;
     for (int i = 0; i <= pl.tail_ctas && pl.tail_ctas; ++i)

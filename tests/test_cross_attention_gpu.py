@@ -104,6 +104,17 @@ def test_many_rows_of_one_tile(npa, d, dtype):
         run_and_check(npa, q, k, v, dtype, what=(heads, Lq))
 
 
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "fp16")])
+def test_rows_in_the_order_of_their_lengths(npa, d, dtype):
+    """More units than multiprocessors: rows run shortest first, whole units and
+    cut ones; equal lengths, none at all, and lengths outside the tensor."""
+    for B, heads, Lq, Lk in ((2, 5, 4200, 1400), (5, 3, 3000, 700), (8, 4, 1300, 2100), (9, 4, 1300, 600)):
+        q, k, v = qkv(900 + B, B, heads, heads, Lq, Lk, d, dtype)
+        for lens in ([Lk] + [Lk // 2] * (B - 1), [Lk - 37 * i for i in range(B)], [(91 * i) % 500 for i in range(B)],
+                     [0] + [Lk + 5] * (B - 1), [-3] * B):
+            run_and_check(npa, q, k, v, dtype, kv_lens=lens, what=(B, lens))
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 64), ("fp16", 64), ("bf16", 128), ("fp16", 128)])
 def test_long_keys(npa, dtype, d):
     """Many blocks: ring wrap-around, rescaling, splits; and many units of
