@@ -1172,7 +1172,9 @@ __global__ void __launch_bounds__(XaCfg<D, KV8>::kThreads, 1)
 
 // Merging partial results. With m* the largest reference of a row's pieces,
 //   o = sum_s 2^(m_s - m*) O_s / sum_s 2^(m_s - m*) l_s;
-// a piece without keys has m_s = -inf and wrote no O.
+// a piece without keys has m_s = -inf and l_s = 0 and wrote no O. One whose
+// scores are all NaN has m_s = -inf too (a maximum passes NaN over) and l_s =
+// NaN: its sum joins as it stands, so that the row is NaN however it was split.
 struct XaCombineParams {
     const float *o_part, *ml;
     void *o;
@@ -1211,7 +1213,7 @@ __device__ __forceinline__ void xa_merge_row(const XaCombineParams &p, int n, Ro
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
         w[i] = ml[i].x == -INFINITY ? 0.f : sm100::ex2_approx(ml[i].x - m);
-        L = ml[i].x == -INFINITY ? L : fmaf(w[i], ml[i].y, L);
+        L = ml[i].x == -INFINITY ? L + ml[i].y : fmaf(w[i], ml[i].y, L);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);

@@ -418,7 +418,10 @@ __global__ void __launch_bounds__(32 * kXaFewWarps, xa_few_per_sm(D, NT)) xa_few
         }
 #pragma unroll
         for (int i = 0; i < kXaFewWarps; ++i) {
-            if (ml[i].x == -INFINITY) continue;
+            if (ml[i].x == -INFINITY) {  // no keys: 0; or scores that are all NaN: NaN
+                L += ml[i].y;
+                continue;
+            }
             const float wgt = sm100::ex2_approx(ml[i].x - m);
             const float2 o = *reinterpret_cast<const float2 *>(xf_smem + (i * kRows + r) * D + d);
             L = fmaf(wgt, ml[i].y, L);
@@ -459,7 +462,10 @@ __global__ void __launch_bounds__(32 * kXaFewWarps, xa_few_per_sm(D, NT)) xa_few
         }
 #pragma unroll
         for (int i = 0; i < kXaFewCluster; ++i) {
-            if (ml[i].x == -INFINITY) continue;
+            if (ml[i].x == -INFINITY) {  // no keys: 0; or scores that are all NaN: NaN
+                L += ml[i].y;
+                continue;
+            }
             const float wgt = sm100::ex2_approx(ml[i].x - m);
             L = fmaf(wgt, ml[i].y, L);
             x = fmaf(wgt, o[i].x, x);
