@@ -907,6 +907,7 @@ npa_status launch_combine(const XaCall &c, const npa::XaParams &a, npa_stream_t 
         cp.kv_lens = a.sort_rows ? a.kv_lens : nullptr;
         cp.B = a.B;
         cp.Lk = a.Lk;
+        cp.divided = a.k_scale != nullptr;
         std::memcpy(cp.tail_start, a.tail_start, sizeof(cp.tail_start));
         for (int t = 0, cta = 0; t < cut; ++t) {
             while (a.tail_start[cta + 1] <= t * a.n_blk) ++cta;

@@ -18,7 +18,8 @@
 //   9, 10  MMA issuers: d = 64, the S products and the P.V products; d = 128,
 //          warp 9 issues both
 //   11     16-bit keys: clears the value rows of keys that are not kept
-//          (0 * NaN would reach the sums through the product otherwise)
+//          (0 * NaN would reach the sums through the product otherwise);
+//          8-bit cache: finds how large a block's kept value codes are
 //   12-15  8-bit cache: converts code blocks to f16 tiles in shared memory
 // TMEM, the aliasing of P at d = 128, the lazily moved softmax reference and
 // the turns on the exponential unit are those of npa_fwd_kernel.cuh.
@@ -31,6 +32,19 @@
 // the row sum divides it out again. (Converting code * scale to bf16 instead
 // took 900 instructions of a converting warp per block, and more than twice
 // the time of the softmax beside it.)
+//   P' is f16: what lies 2^-31 under the reference is lost. So R has to follow
+// what blocks contribute, not their scales alone: a block of zeros, one whose
+// scale stems from a token that is not kept, or one whose scale has grown may
+// have a large scale and small codes. Warp 11 therefore finds, per 64 tokens,
+// the power of two by which the largest kept code lies under the format's top
+// (where a code of 128 or more is met, as in nearly every block's first rows,
+// that is 0 and the search ends); the converter takes it out of the value tile,
+// exactly, and the softmax adds it to the scale. Halves without a kept code
+// other than 0 count as 2^-60. A key's rounding is then at most 2^-30 of the
+// largest p |v| that some 64 tokens' largest p and largest kept |v| make.
+//   Scales are taken relative to that of the unit's first 64 tokens with values
+// (2^c), so that sums stay within float32 wherever the scales lie; between
+// blocks they may differ by 2^100.
 //
 // What differs from the self-attention kernel: every tensor is a 4D {d, L,
 // heads, B} map with the caller's strides (a projection's [B, L, heads * d]
@@ -101,7 +115,7 @@ struct XaParams {
     int sort_rows;  // batch rows in the order of their lengths
     int n_splits;   // xa_few_kernel: key-range splits
     // Partial results: unnormalised O [..][d], then reference and row sum
-    // [..][2]. Cut units: two slots of 256 rows per CTA (its first piece, its
+    // [..][2] (over the 8-bit cache O / l, its logarithm and 1). Cut units: two slots of 256 rows per CTA (its first piece, its
     // last); xa_few_kernel: [n_splits][B * heads * Lq].
     float *o_part, *ml;
 };
@@ -147,7 +161,7 @@ struct XaCfg {
     static constexpr int bKCFull = bQReady + kQStages;   // [kCodeStages] code blocks landed
     static constexpr int bKCEmpty = bKCFull + kCodeStages;
     static constexpr int bVCFull = bKCEmpty + kCodeStages;
-    static constexpr int bVCEmpty = bVCFull + kCodeStages;
+    static constexpr int bVCEmpty = bVCFull + kCodeStages;  // 128 converter arrivals and the look at the values
     static constexpr int bSFull = bVCEmpty + kCodeStages;
     static constexpr int bSFree = bSFull + 2;
     static constexpr int bPFull = bSFree + 2;
@@ -161,10 +175,19 @@ struct XaCfg {
     // unit has one tile only).
     static constexpr int kExpSets = 4;
     static constexpr int bExp = bDrain + 2;
-    static constexpr int kNumBars = bExp + (KV8 ? kExpSets : 0);
+    // [kScaleSets] 8-bit: a block's scales (XaBlockScales) are written (one
+    // arrival). The converter waits for that before it converts the block's
+    // keys, so its scores come later still and the softmax need not wait again.
+    // A set is written again when the value codes of block i + kScaleSets are
+    // there: behind the value tile of block i + kStages, and so behind the
+    // products of block i, for which the softmax has read it.
+    static constexpr int kScaleSets = kCodeStages + kStages;
+    static constexpr int bScale = bExp + (KV8 ? kExpSets : 0);
+    static constexpr int kNumBars = bScale + (KV8 ? kScaleSets : 0);
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;
     static constexpr int kOffExp = kOffMisc + 16;        // [kExpSets][2][128] 8-bit: exponent taken out of a query row
-    static constexpr int kSmemBytes = kOffExp + (KV8 ? kExpSets * 256 : 0) + 1024;
+    static constexpr int kOffScale = (kOffExp + (KV8 ? kExpSets * 256 : 0) + 15) & ~15;  // [kScaleSets] XaBlockScales
+    static constexpr int kSmemBytes = kOffScale + (KV8 ? kScaleSets * 32 : 0) + 1024;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
     static constexpr uint32_t kTmemCols = 512;
     static constexpr bool kSeparateP = (D == 64);
@@ -602,26 +625,134 @@ __device__ void xa_clear_unkept(const XaParams &p, uint8_t *smem, uint64_t *bars
 }
 
 // ---------------------------------------------------------------------------
+// 8-bit cache: how large the kept value codes are (one warp)
+// ---------------------------------------------------------------------------
+constexpr int kXaNoValues = 255;  // no kept code other than 0
+
+// The power of two by which the largest kept code of 64 tokens lies under
+// 2^8..2^9, the binade of the format's top: 0 (a code of 128 or more), 2..17 or
+// kXaNoValues. Executed by a whole warp.
+template <int D>
+__device__ __forceinline__ int xa_codes_under_top(const uint8_t *codes, uint32_t w0, uint32_t w1, int lane) {
+    if ((w0 | w1) == 0u) return kXaNoValues;
+    uint32_t top = 0;  // largest magnitudes, in the upper bytes of two halves
+#pragma unroll 1
+    for (int i = 0; i < D / 8; ++i) {
+        const int idx = lane + 32 * i, row = idx / (D / 16);
+        uint4 c = *reinterpret_cast<const uint4 *>(codes + idx * 16);
+        if (!((row < 32 ? w0 : w1) >> (row & 31) & 1u)) c = make_uint4(0, 0, 0, 0);
+        const uint32_t x[4] = {c.x, c.y, c.z, c.w};
+        uint32_t big = 0;  // codes 0x70 and above, the sign aside: 128 or more
+#pragma unroll
+        for (int k = 0; k < 4; ++k) big |= x[k] & x[k] << 1 & x[k] << 2 & 0x40404040u;
+        if (__any_sync(0xffffffffu, big != 0u)) return 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            top = __vmaxu2(top, x[k] & 0x7f007f00u);
+            top = __vmaxu2(top, (x[k] & 0x007f007fu) << 8);
+        }
+    }
+    const int a = int(__reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu)) >> 8);
+    if (a == 0) return kXaNoValues;
+    return a >= 8 ? 15 - (a >> 3) : 17 - (31 - __clz(a));  // exponent (a >> 3) - 7; subnormals a 2^-9
+}
+
+// A block's scales, for each half of its keys: k, the keys'; lv, log2 of what the
+// value tile is to be multiplied by, relative to the unit's 2^c; inv_v, 2^-lv.
+// (lg2.approx is off by 2^-22, or by 2^-17 at the ends of float32's range: below
+// a sixteenth of P's rounding.)
+struct alignas(16) XaBlockScales {
+    float k[2], lv[2], inv_v[2];
+    float c;
+    int lift;  // powers of two that the value tile's halves are multiplied by: bits 0-7, 8-15
+};
+static_assert(sizeof(XaBlockScales) == 32, "two 16-byte loads");
+constexpr float kXaNoValuesLog2 = -60.f;  // lv of 64 tokens that contribute nothing
+
+template <int D>
+__device__ void xa_block_scales(const XaParams &p, uint8_t *smem, uint64_t *bars, volatile uint32_t *abort_flag) {
+    using C = XaCfg<D, true>;
+    const uint64_t lim = p.wait_limit_ns;
+    const int lane = threadIdx.x & 31;
+    XaBlockScales *sets = reinterpret_cast<XaBlockScales *>(smem + C::kOffScale);
+    int kv = 0;
+    bool ok = true;
+    for (XaIter it(p); ok && it.next();) {
+        const XaUnit &u = it.u;
+        const size_t s0 = ((size_t)u.b * p.kv_heads + u.kvh) * p.scale_blocks;
+        float c = -INFINITY;  // log2 of the first values' scale; -inf: none yet
+        for (int j = u.jb; j < u.je; ++j, ++kv) {
+            const int cs = kv % C::kCodeStages, set = kv % C::kScaleSets;
+            const int i0 = 2 * j, i1 = min(i0 + 1, p.scale_blocks - 1);  // past the cache: its keys are not kept
+            const float ks[2] = {__ldg(p.k_scale + s0 + i0), __ldg(p.k_scale + s0 + i1)};
+            const float vs[2] = {__ldg(p.v_scale + s0 + i0), __ldg(p.v_scale + s0 + i1)};
+            uint32_t w[4];
+            xa_keep(p, u, j, xa_block_keys(u, j), w);
+            ok = !*abort_flag && sm100::mbar_wait_idle(&bars[C::bVCFull + cs], (kv / C::kCodeStages) & 1, lim);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const uint8_t *codes = smem + C::kOffVC + cs * C::kCodeBytes;
+            XaBlockScales out;
+            out.lift = 0;
+            int tops = 0;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h)
+                tops |= xa_codes_under_top<D>(codes + h * 64 * D, h ? w[2] : w[0], h ? w[3] : w[1], lane) << 8 * h;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int top = tops >> 8 * h & 255;
+                const bool some = top != kXaNoValues;  // else whatever the scale holds stays out
+                const float lv = __log2f(vs[h]) - float(top);
+                if (some && c == -INFINITY) c = lv;
+                out.k[h] = ks[h];
+                out.lv[h] = some ? lv - c : kXaNoValuesLog2;
+                out.inv_v[h] = sm100::ex2_approx(-out.lv[h]);
+                if (some) out.lift |= top << 8 * h;
+            }
+            out.c = c;
+            __syncwarp();
+            if (lane == 0) {
+                sets[set] = out;
+                sm100::mbar_arrive(&bars[C::bScale + set]);
+                sm100::mbar_arrive(&bars[C::bVCEmpty + cs]);
+            }
+        }
+    }
+    if (!ok) {
+        record_error(kErrDeviceTimeout);
+        *abort_flag = 1;
+    }
+}
+
+// ---------------------------------------------------------------------------
 // 8-bit cache (one warpgroup): code blocks to f16 tiles, values of unkept keys
 // as zeros (a NaN code would reach the sums through the product otherwise), and
 // the unit's query rows to f16.
 // ---------------------------------------------------------------------------
+// The i-th 16-code piece of converting thread tid. Eight lanes take half of an
+// even row and the other half of the odd row behind it (d = 128): 128 different
+// bytes mod 128 to read, and, as the swizzle puts even rows' pieces in even
+// places, eight different places to write.
+template <int D>
+__device__ __forceinline__ void xa_piece(int i, int tid, int &row, int &piece) {
+    const int idx = tid + 128 * i, half = idx >> 2 & 1;
+    row = D == 128 ? idx / 16 * 2 + half : idx / (D / 16);
+    piece = D == 128 ? (idx & 3) + 4 * (half ^ (idx >> 3 & 1)) : idx % (D / 16);
+}
+
 template <int D>
 __device__ __forceinline__ void xa_convert_tile(const uint8_t *codes, uint8_t *tile, const uint32_t (&w)[4], int tid) {
     using C = XaCfg<D, true>;
     constexpr int kPerRow = D / 16;  // 16-code pieces of a row
     const bool all = (w[0] & w[1] & w[2] & w[3]) == 0xffffffffu;
-    constexpr int kAhead = D == 128 ? 4 : 2;  // pieces in flight (d = 64: 470 us with 2, 476 with 4; d = 128: 173, 171)
+    // pieces in flight. d = 64 takes what keeps the code short, which the kernel's
+    // roles share a cache for: 463 us with 1, 477 with 2, 487 with 4 (2 x 10 heads x
+    // 4096 x 12288); d = 128: 4 against 2, 171 and 173 us (24 heads x 2048 x 4096).
+    constexpr int kAhead = D == 128 ? 4 : 1;
 #pragma unroll kAhead
     for (int i = 0; i < kPerRow; ++i) {
-        const int idx = tid + 128 * i;
-        // Eight lanes take half of an even row and the other half of the odd row
-        // behind it (d = 128): 128 different bytes mod 128 to read, and, as the
-        // swizzle puts even rows' pieces in even places, eight different places
-        // to write.
-        const int half = idx >> 2 & 1;
-        const int row = D == 128 ? idx / 16 * 2 + half : idx / kPerRow;
-        const int piece = D == 128 ? (idx & 3) + 4 * (half ^ (idx >> 3 & 1)) : idx % kPerRow;
+        int row, piece;
+        xa_piece<D>(i, tid, row, piece);
         uint4 c4 = *reinterpret_cast<const uint4 *>(codes + row * D + piece * 16);
         if (!all) {
             const uint32_t word = row < 64 ? (row < 32 ? w[0] : w[1]) : (row < 96 ? w[2] : w[3]);
@@ -635,6 +766,24 @@ __device__ __forceinline__ void xa_convert_tile(const uint8_t *codes, uint8_t *t
         *reinterpret_cast<uint4 *>(dst + (((p0 + 1) ^ (row & 7)) << 4)) =
             make_uint4(sm100::e4m3x2_to_f16x2(c4.z), sm100::e4m3x2_to_f16x2(c4.z >> 16), sm100::e4m3x2_to_f16x2(c4.w),
                        sm100::e4m3x2_to_f16x2(c4.w >> 16));
+    }
+}
+
+// The values that this thread has converted times 2^lift0 (the first 64 rows) or
+// 2^lift1, at most 2^17: exact.
+template <int D>
+__device__ __forceinline__ void xa_lift_tile(uint8_t *tile, int lift0, int lift1, int tid) {
+    using C = XaCfg<D, true>;
+#pragma unroll 1
+    for (int i = 0; i < D / 2; ++i) {
+        int row, piece;
+        xa_piece<D>(i >> 3, tid, row, piece);
+        const int lift = row < 64 ? lift0 : lift1, p0 = (piece & 3) * 2 + (i >> 2 & 1);
+        // in two factors, f16x2: 2^17 is past f16's largest
+        const uint32_t f0 = uint32_t(15 + (lift >> 1)) * 0x04000400u, f1 = uint32_t(15 + lift - (lift >> 1)) * 0x04000400u;
+        uint8_t *base = tile + (piece >> 2) * C::kChunkBytes + row * 128 + ((p0 ^ (row & 7)) << 4);
+        uint32_t *at = reinterpret_cast<uint32_t *>(base) + (i & 3);
+        *at = sm100::mul_f16x2(sm100::mul_f16x2(*at, f0), f1);
     }
 }
 
@@ -696,12 +845,20 @@ __device__ void xa_convert(const XaParams &p, uint8_t *smem, uint64_t *bars, vol
             const int s = kv % C::kStages, use = kv / C::kStages;
 #pragma unroll 1
             for (int t = 0; t < 2; ++t) {  // keys, values
-                ok = !*abort_flag && sm100::mbar_wait(&bars[(t ? C::bVCFull : C::bKCFull) + cs], cpar, lim) &&
+                // the block's scales come after the copy of its values
+                const int set = kv % C::kScaleSets;
+                ok = !*abort_flag &&
+                     (t || (sm100::mbar_wait(&bars[C::bScale + set], (kv / C::kScaleSets) & 1, lim) &&
+                            sm100::mbar_wait(&bars[C::bKCFull + cs], cpar, lim))) &&
                      (use == 0 || sm100::mbar_wait(&bars[(t ? C::bVEmpty : C::bKEmpty) + s], (use - 1) & 1, lim));
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                xa_convert_tile<D>(smem + (t ? C::kOffVC : C::kOffKC) + cs * C::kCodeBytes,
-                                   smem + (t ? C::kOffV : C::kOffK) + s * C::kTileBytes, w, tid);
+                uint8_t *tile = smem + (t ? C::kOffV : C::kOffK) + s * C::kTileBytes;
+                xa_convert_tile<D>(smem + (t ? C::kOffVC : C::kOffKC) + cs * C::kCodeBytes, tile, w, tid);
+                if (t) {
+                    const int lift = reinterpret_cast<const XaBlockScales *>(smem + C::kOffScale)[set].lift;
+                    if (lift) xa_lift_tile<D>(tile, lift & 255, lift >> 8, tid);
+                }
                 sm100::fence_proxy_async();
                 sm100::mbar_arrive(&bars[(t ? C::bVFull : C::bKFull) + s]);
                 sm100::mbar_arrive(&bars[(t ? C::bVCEmpty : C::bKCEmpty) + cs]);
@@ -766,8 +923,7 @@ __device__ __forceinline__ void xa_store_p(uint32_t t_p, const uint32_t (&pk)[16
     }
 }
 
-// A block's scales of the 8-bit cache, one for each half of its keys: f, of the
-// scores to log2 units; lv, log2 of the value scale; inv_v, its reciprocal.
+// The same for one row: f, of the scores to log2 units.
 struct XaScales {
     float f[2], lv[2], inv_v[2];
 };
@@ -943,6 +1099,7 @@ __device__ void xa_softmax(const XaParams &p, uint8_t *smem, uint64_t *bars, uin
     uint8_t *stage = smem + C::kOffO + q * C::kChunkBytes;
     int ep = 0;  // uses of the warpgroup's own barrier
     int uq = -1;  // units with keys so far, the current one included
+    int kv = 0;   // 8-bit cache: blocks before the current unit's, of any tile
     auto group_sync = [&]() {
         sm100::mbar_arrive(&bars[C::bEpi + q]);
         return warp_wait(&bars[C::bEpi + q], (ep++) & 1, lim);
@@ -951,6 +1108,8 @@ __device__ void xa_softmax(const XaParams &p, uint8_t *smem, uint64_t *bars, uin
     for (XaIter it(p); ok && it.next();) {
         const XaUnit &u = it.u;
         uq += u.je > u.jb;
+        const int kv0 = kv - u.jb;
+        kv += u.je - u.jb;
         if (q >= u.nt) continue;
         const int grow = u.row0 + q * 128 + row;  // this thread's query
         const bool active = u.row0 + q * 128 + warp * 32 < p.Lq;
@@ -958,17 +1117,7 @@ __device__ void xa_softmax(const XaParams &p, uint8_t *smem, uint64_t *bars, uin
         st.R = st.R_prev = -INFINITY;
         st.l = 0.f;
         XaScales sc;
-        float ks[2], vs[2], f_row = 0.f;  // the next block's scales; this row's factor
-        const size_t s0 = KV8 ? ((size_t)u.b * p.kv_heads + u.kvh) * p.scale_blocks : 0;
-        auto fetch_scales = [&](int j) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int i = min(2 * j + h, p.scale_blocks - 1);  // past the cache: its keys are not kept
-                ks[h] = __ldg(p.k_scale + s0 + i);
-                vs[h] = __ldg(p.v_scale + s0 + i);
-            }
-        };
-        if (KV8 && u.je > u.jb) fetch_scales(u.jb);
+        float f_row = 0.f, c = -INFINITY;  // 8-bit cache: this row's factor; XaBlockScales::c
         for (int j = u.jb; j < u.je; ++j) {
             const int n = xa_block_keys(u, j);
             uint32_t w[4];
@@ -984,15 +1133,13 @@ __device__ void xa_softmax(const XaParams &p, uint8_t *smem, uint64_t *bars, uin
                     const int e = reinterpret_cast<const int8_t *>(smem + C::kOffExp)[(set * 2 + q) * 128 + row];
                     f_row = p.scale_log2 * __uint_as_float(uint32_t(127 + e) << 23);
                 }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    sc.f[h] = fmaxf(f_row * ks[h], 1.2e-38f);  // above 0: -inf times it stays -inf
-                    sc.lv[h] = __log2f(vs[h]);
-                    sc.inv_v[h] = __fdividef(1.f, vs[h]);
-                    // none of its keys is kept: whatever its scales hold stays out
-                    if (!full && (w[2 * h] | w[2 * h + 1]) == 0u) sc.lv[h] = 0.f, sc.inv_v[h] = 1.f;
-                }
-                if (j + 1 < u.je) fetch_scales(j + 1);
+                const float4 *at = reinterpret_cast<const float4 *>(smem + C::kOffScale) + (kv0 + j) % C::kScaleSets * 2;
+                const float4 s0 = at[0], s1 = at[1];
+                sc.f[0] = fmaxf(f_row * s0.x, 1.2e-38f);  // above 0: -inf times it stays -inf
+                sc.f[1] = fmaxf(f_row * s0.y, 1.2e-38f);
+                sc.lv[0] = s0.z, sc.lv[1] = s0.w;
+                sc.inv_v[0] = s1.x, sc.inv_v[1] = s1.y;
+                c = s1.z;
             }
             sm100::tc_fence_after();
             const bool first = j == u.jb;
@@ -1017,21 +1164,29 @@ __device__ void xa_softmax(const XaParams &p, uint8_t *smem, uint64_t *bars, uin
         if (ok && any) ok = warp_wait(&bars[C::bPFree + q], (st.g - 1) & 1, lim);
         if (!ok) break;
         sm100::tc_fence_after();
+        // 8-bit cache: 2^c in two factors (with 1 / l it may be far from 1)
+        const float to_v = KV8 ? (c == -INFINITY ? 0.f : sm100::ex2_approx(0.5f * c)) : 1.f;
+        const float inv_l = (st.l > 0.f ? 1.f / st.l : st.l == 0.f ? 0.f : st.l) * to_v;
         if (u.slot >= 0) {
             const size_t prow = (size_t)u.slot * 256 + q * 128 + row;
             const bool valid = bound_row(grow < p.Lq, prow, (size_t)p.tail_ctas * 512);
-            if (valid) *reinterpret_cast<float2 *>(p.ml + prow * 2) = make_float2(any ? st.R_prev : -INFINITY, st.l);
+            // the 8-bit cache's pieces hold O / l, with the sum in the reference:
+            // so they lie within float32 wherever the result does
+            const bool divided = KV8 && st.l > 0.f;
+            const float ref = divided ? st.R_prev + __log2f(st.l) : st.R_prev;
+            if (valid) *reinterpret_cast<float2 *>(p.ml + prow * 2) = make_float2(any ? ref : -INFINITY, divided ? 1.f : st.l);
+            auto piece = [&](uint32_t x) { return KV8 ? __uint_as_float(x) * to_v * inv_l : __uint_as_float(x); };
             if (any && active) {
                 float4 *part = reinterpret_cast<float4 *>(p.o_part + prow * D);
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
+                for (int i = 0; i < D / 32; ++i) {
                     uint32_t o[32];
-                    sm100::tmem_ld32(st.tO + c * 32, o);
+                    sm100::tmem_ld32(st.tO + i * 32, o);
                     if (valid) {
 #pragma unroll
                         for (int v = 0; v < 8; ++v)
-                            part[c * 8 + v] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
-                                                          __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
+                            part[i * 8 + v] = make_float4(piece(o[4 * v]), piece(o[4 * v + 1]), piece(o[4 * v + 2]),
+                                                          piece(o[4 * v + 3]));
                     }
                 }
             }
@@ -1039,7 +1194,6 @@ __device__ void xa_softmax(const XaParams &p, uint8_t *smem, uint64_t *bars, uin
         }
         // O / l through shared memory, 64 columns at a time (128-byte rows,
         // the tensor map's swizzle), and out by TMA
-        const float inv_l = st.l > 0.f ? 1.f / st.l : st.l == 0.f ? 0.f : st.l;
         for (int ch = 0; ch < C::kChunks; ++ch) {
             if (row == 0) sm100::bulk_wait_read();  // the previous store has read the stage
             ok = group_sync();
@@ -1056,7 +1210,8 @@ __device__ void xa_softmax(const XaParams &p, uint8_t *smem, uint64_t *bars, uin
                         uint32_t h[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float a = __uint_as_float(o[8 * v + 2 * i]), b = __uint_as_float(o[8 * v + 2 * i + 1]);
+                            float a = __uint_as_float(o[8 * v + 2 * i]), b = __uint_as_float(o[8 * v + 2 * i + 1]);
+                            if (KV8) a *= to_v, b *= to_v;
                             h[i] = any && st.l != 0.f ? sm100::pack_16x2<F16>(a * inv_l, b * inv_l) : 0u;
                         }
                         *reinterpret_cast<uint4 *>(stage + row * 128 + (((c * 4 + v) ^ (row & 7)) << 4)) =
@@ -1114,8 +1269,9 @@ __global__ void __launch_bounds__(XaCfg<D, KV8>::kThreads, 1)
             sm100::mbar_init(&bars[C::bKCFull + s], 1);
             sm100::mbar_init(&bars[C::bKCEmpty + s], 128);
             sm100::mbar_init(&bars[C::bVCFull + s], 1);
-            sm100::mbar_init(&bars[C::bVCEmpty + s], 128);
+            sm100::mbar_init(&bars[C::bVCEmpty + s], 129);
         }
+        for (int s = 0; KV8 && s < C::kScaleSets; ++s) sm100::mbar_init(&bars[C::bScale + s], 1);
         for (int q = 0; q < 2; ++q) {
             sm100::mbar_init(&bars[C::bSFull + q], 1);
             sm100::mbar_init(&bars[C::bSFree + q], 128);
@@ -1144,9 +1300,11 @@ __global__ void __launch_bounds__(XaCfg<D, KV8>::kThreads, 1)
     } else if (warp >= C::kCtlWarp) {
         sm100::setmaxnreg_dec<C::kRegsCtl>();
         const int role = warp - C::kCtlWarp;
-        if (!KV8 && role == 3) {
-            if constexpr (!KV8)
-                if (p.kv_lens || p.key_mask) xa_clear_unkept<D>(p, smem, bars, abort_flag);
+        if (role == 3) {
+            if constexpr (KV8)
+                xa_block_scales<D>(p, smem, bars, abort_flag);
+            else if (p.kv_lens || p.key_mask)
+                xa_clear_unkept<D>(p, smem, bars, abort_flag);
         } else if ((threadIdx.x & 31) == 0) {
             if (role == 0) xa_producer<D, KV8>(p, smem, bars, abort_flag);
             if constexpr (C::kSeparateP) {
@@ -1171,7 +1329,8 @@ __global__ void __launch_bounds__(XaCfg<D, KV8>::kThreads, 1)
 }
 
 // Merging partial results. With m* the largest reference of a row's pieces,
-//   o = sum_s 2^(m_s - m*) O_s / sum_s 2^(m_s - m*) l_s;
+//   o = sum_s 2^(m_s - m*) O_s / sum_s 2^(m_s - m*) l_s
+// (cut units over the 8-bit cache: O_s / l_s, m_s + log2 l_s and 1, `divided`);
 // a piece without keys has m_s = -inf and l_s = 0 and wrote no O. One whose
 // scores are all NaN has m_s = -inf too (a maximum passes NaN over) and l_s =
 // NaN: its sum joins as it stands, so that the row is NaN however it was split.
@@ -1187,6 +1346,7 @@ struct XaCombineParams {
     int n_qpairs;
     const int *kv_lens;  // null: batch rows as they stand
     int B, Lk;
+    int divided;         // pieces hold O / l: weights are divided too, so that the sum keeps the result's range
     short first_cta[kXaMaxTailCtas], last_cta[kXaMaxTailCtas];
     int tail_start[kXaMaxTailCtas];
 };
@@ -1217,6 +1377,11 @@ __device__ __forceinline__ void xa_merge_row(const XaCombineParams &p, int n, Ro
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    const float inv = L > 0.f ? 1.f / L : L;
+    if (p.divided) {
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) w[i] *= inv;
+    }
     float acc[kPer];
 #pragma unroll
     for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
@@ -1239,11 +1404,11 @@ __device__ __forceinline__ void xa_merge_row(const XaCombineParams &p, int n, Ro
 #pragma unroll
             for (int c = 0; c < kPer; ++c) acc[c] = fmaf(wgt[i], o[i][c], acc[c]);
     }
-    const float inv = L > 0.f ? 1.f / L : L;
+    const float last = p.divided && L > 0.f ? 1.f : inv;
 #pragma unroll
     for (int c = 0; c < kPer; c += 2)
         reinterpret_cast<uint32_t *>(dst + lane * kPer)[c / 2] =
-            L == 0.f ? 0u : sm100::pack_16x2<F16>(acc[c] * inv, acc[c + 1] * inv);
+            L == 0.f ? 0u : sm100::pack_16x2<F16>(acc[c] * last, acc[c + 1] * last);
 }
 
 // xa_few_kernel's key-range splits.
