@@ -315,7 +315,11 @@ npa_status npa_kv8_store(const void *k, const void *v, const npa_kv8_cache *cach
  * capacity); q and o are bfloat16. The codes enter the products exactly (as
  * float16, with the probabilities) and the scales in float32; the scales of
  * blocks with kept keys must be positive and finite, powers of two or not, and
- * within one head those of the values less than 2^100 apart. Other arguments,
+ * within one head those of the values less than 2^100 apart. A probability is
+ * off by half a step of float16, or by 2^-30 of the largest product p |v| that
+ * some 64 tokens' largest probability and largest kept value make, whichever
+ * is more: blocks of zeros and tokens that are not kept do not count. Other
+ * arguments,
  * results, workspace and errors as for npa_cross_attention_fwd. */
 npa_status npa_kv8_cross_attention_fwd(const void *q, const npa_kv8_cache *cache, void *o, int B, int heads,
                                        int kv_heads, int Lq, int Lk, int d, const npa_strides *q_strides,

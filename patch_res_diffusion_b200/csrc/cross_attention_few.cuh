@@ -20,7 +20,10 @@
 // multiplies in f16: q is scaled by a power of two per row to be exact there,
 // the block's k scale joins the softmax scale and its v scale is applied when a
 // step's product is added to O in float32. Powers of two or not, no scale is
-// rounded to 16 bits.
+// rounded to 16 bits. P is taken at the step's own largest score, and what that
+// lies under the row's reference is applied in float32 too: a block's values may
+// be as large as its probabilities are small, which f16 P at one reference for
+// all keys would lose below 2^-31.
 //
 // The key range is split over CTAs and over a CTA's four warps; the warps merge
 // through shared memory, the CTAs as a cluster through each other's shared
@@ -89,7 +92,13 @@ struct XfWarp {
     static constexpr int kKLoads = KV8 ? D / 64 : D / 32;    // 16-byte pieces of a key row per lane
     static constexpr int kVWords = KV8 ? D / 32 : D / 16;    // 32-bit words of a value row per lane
     static constexpr int kMTiles = D / 16;
-    static constexpr float kLead = kF16 ? 15.f : kRescaleLog2, kBelow = kF16 ? 7.f : 0.f;
+    // The reference moves to kBelow under a step's maximum that exceeds it by more
+    // than kLead. P of a step reaches 2^15 in f16, 2^7 at its own maximum with an
+    // 8-bit cache (where nothing but float32 sums is at the reference, and it
+    // stays above the largest score: O overflows only where sum p |v| does).
+    static constexpr float kLead = KV8 ? 0.f : kF16 ? 15.f : kRescaleLog2;
+    static constexpr float kBelow = KV8 ? -4.f : kF16 ? 7.f : 0.f;
+    static constexpr float kTop = 7.f;  // 8-bit: log2 of P at a step's maximum
 
     uint32_t q[D / 16][NT][2];  // [k step][row tile]: a0, a2 (and a1, a3)
     uint4 kr[kTiles][kKLoads];
@@ -170,8 +179,10 @@ struct XfWarp {
         }
     }
 
-    // O^T += V^T P^T for the step, P as packed pairs [row tile][16 keys][2].
-    __device__ __forceinline__ void products(const uint32_t (&pb)[NT][kSubs][2], uint32_t keep, int t) {
+    // O^T += V^T P^T for the step, P as packed pairs [row tile][16 keys][2]; to_R
+    // (8-bit): from P's reference to O's, of this lane's two rows of each tile.
+    __device__ __forceinline__ void products(const uint32_t (&pb)[NT][kSubs][2], const float (&to_R)[NT][2], uint32_t keep,
+                                             int t) {
         // values of keys that are not kept: 0 (P is 0 there, but not 0 * NaN)
         if (keep != kAll) {
 #pragma unroll
@@ -208,7 +219,8 @@ struct XfWarp {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) o[n][2 * jw + e][c] = fmaf(vs, acc[e][n][c], o[n][2 * jw + e][c]);
+                        for (int c = 0; c < 4; ++c)
+                            o[n][2 * jw + e][c] = fmaf(vs, acc[e][n][c] * to_R[n][c & 1], o[n][2 * jw + e][c]);
             }
         } else {
 #pragma unroll
@@ -345,7 +357,7 @@ __global__ void __launch_bounds__(32 * kXaFewWarps, xa_few_per_sm(D, NT)) xa_few
         }
         uint32_t pb[NT][W::kSubs][2];
         bool moved = false;
-        float alpha[NT];
+        float alpha[NT], to_R[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float mx = -INFINITY;
@@ -359,7 +371,7 @@ __global__ void __launch_bounds__(32 * kXaFewWarps, xa_few_per_sm(D, NT)) xa_few
             if (bm > w.R[n] + W::kLead) w.R[n] = bm - W::kBelow;
             alpha[n] = w.R[n] == before ? 1.f : sm100::ex2_approx(before - w.R[n]);
             moved = moved || w.R[n] != before;
-            const float neg = w.R[n] == -INFINITY ? 0.f : -w.R[n];
+            const float ref = KV8 ? bm - W::kTop : w.R[n], neg = ref == -INFINITY ? 0.f : -ref;
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < W::kTiles; ++i) {
@@ -367,6 +379,13 @@ __global__ void __launch_bounds__(32 * kXaFewWarps, xa_few_per_sm(D, NT)) xa_few
                 const float p1 = sm100::ex2_approx(fmaf(s[i][2 * n + 1], f, neg));
                 sum += p0 + p1;
                 pb[n][i >> 1][i & 1] = sm100::pack_16x2<W::kF16>(p0, p1);
+            }
+            if constexpr (KV8) {
+                // 0 where every score is -inf, or NaN, which stays
+                const float x = ref == -INFINITY ? 0.f : sm100::ex2_approx(ref - w.R[n]);
+                to_R[n][0] = __shfl_sync(0xffffffffu, x, 8 * t);
+                to_R[n][1] = __shfl_sync(0xffffffffu, x, 8 * t + 4);
+                sum *= x;
             }
             w.l[n] = fmaf(w.l[n], alpha[n], sum);
         }
@@ -384,7 +403,7 @@ __global__ void __launch_bounds__(32 * kXaFewWarps, xa_few_per_sm(D, NT)) xa_few
                 }
             }
         }
-        w.products(pb, keep, t);
+        w.products(pb, to_R, keep, t);
         if (more) load_values(j + kXaFewWarps);
     }
 

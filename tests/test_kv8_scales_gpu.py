@@ -153,6 +153,17 @@ def test_many_rows(npa, case, Lq, n, split, d):
     case(npa, Lq, n, split, d)
 
 
+# at most 16 rows: whole, split in a cluster, split through the workspace
+FEW = [(1, 384, True), (8, 1536, True), (3, 12000, True), (2, 333, False)]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Lq,n,split", FEW)
+@pytest.mark.parametrize("case", CASES)
+def test_few_rows(npa, case, Lq, n, split, d):
+    case(npa, Lq, n, split, d)
+
+
 def test_checked_build(npa):
     npa.use_bounds_checking(True)
     try:
