@@ -304,6 +304,10 @@ struct GnAffine {
             bias[k] = fmaf(-s.x, a[k], bias[k]);
         }
     }
+    static __device__ __forceinline__ float pair(const float (&u)[kVec], int i) {
+        if constexpr (kVec > 1) return u[2 * i] * u[2 * i + 1];
+        return u[0];
+    }
     template <bool kSilu>
     __device__ __forceinline__ typename GnVec<T, kVec>::Raw apply(typename GnVec<T, kVec>::Raw raw) const {
         float f[kVec];
@@ -312,18 +316,41 @@ struct GnAffine {
         for (int k = 0; k < kVec; ++k) f[k] = fmaf(f[k], a[k], bias[k]);
         if constexpr (kSilu) {
             // z / (1 + e^-z), two to a reciprocal: 1 / u = v / (u v). The power
-            // is kept below 2^63 so that u v is finite; z < -43 then gives
-            // z 2^-63, below 5e-18 in size.
-            float u[kVec];
+            // is kept below 2^63 so that u v is finite; where that would show,
+            // z e^z is the same to 2^-62 (and -0 for the largest -z).
+            constexpr int kPairs = (kVec + 1) / 2;
+            float u[kVec], uv[kPairs], most = 0.f;
 #pragma unroll
             for (int k = 0; k < kVec; ++k) u[k] = 1.f + sm100::ex2_approx(fminf(-1.4426950408889634f * f[k], 63.f));
 #pragma unroll
-            for (int k = 0; k + 1 < kVec; k += 2) {
-                const float r = rcp_approx(u[k] * u[k + 1]);
-                f[k] *= r * u[k + 1];
-                f[k + 1] *= r * u[k];
+            for (int i = 0; i < kPairs; ++i) {
+                uv[i] = pair(u, i);
+                most = fmaxf(most, uv[i]);
             }
-            if (kVec % 2) f[kVec - 1] *= rcp_approx(u[kVec - 1]);
+            if (most > 0x1p60f) {  // rare
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) {
+                    if (f[k] < -43.f) {
+                        // in two factors: ex2.approx has no results below 2^-126
+                        const float h = sm100::ex2_approx(0.5f * 1.4426950408889634f * f[k]);
+                        f[k] *= h;
+                        f[k] *= h;
+                        u[k] = 1.f;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kPairs; ++i) uv[i] = pair(u, i);
+            }
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) {
+                const float r = rcp_approx(uv[i]);
+                if constexpr (kVec > 1) {
+                    f[2 * i] *= r * u[2 * i + 1];
+                    f[2 * i + 1] *= r * u[2 * i];
+                } else {
+                    f[0] *= r;
+                }
+            }
         }
         return GnVec<T, kVec>::narrow(f);
     }
