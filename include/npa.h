@@ -278,9 +278,15 @@ npa_status npa_cross_attention_fwd(const void *q, const void *k, const void *v, 
                                    const npa_strides *o_strides, const int32_t *kv_lens, const uint8_t *key_mask,
                                    float scale, void *workspace, size_t workspace_bytes, npa_stream_t stream);
 
+/* Whether the current device runs this library: NPA_OK; NPA_ERR_UNSUPPORTED,
+ * which stays; or NPA_ERR_CUDA when the device could not be asked, which is
+ * tried again at the next call of anything. The workspace sizes below are 0 in
+ * the last two cases too, so a 0 is worth keeping only behind an NPA_OK here. */
+npa_status npa_device_ready(void);
+
 /* Workspace bytes npa_cross_attention_fwd and npa_kv8_cross_attention_fwd use
- * on the current device for the split they plan (0: none, or invalid
- * arguments; 16-bit keys of at most 128 never need any). */
+ * on the current device for the split they plan (0: none, invalid arguments, or
+ * a device that is not ready; 16-bit keys of at most 128 never need any). */
 size_t npa_cross_attention_workspace_size(int B, int heads, int kv_heads, int Lq, int Lk, int d);
 
 /* Keys and values held in 8 bits: e4m3 codes (1-4-3, largest 448) with one
@@ -348,7 +354,8 @@ npa_status npa_group_norm_act(const void *x, const void *weight, const void *bia
                               npa_activation act, void *workspace, size_t workspace_bytes, npa_stream_t stream);
 
 /* Workspace bytes of npa_group_norm_act on the current device, whatever the
- * alignment of x and y (0: none needed, or invalid arguments). */
+ * alignment of x and y (0: none needed, invalid arguments, or a device that is
+ * not ready). */
 size_t npa_group_norm_workspace_size(npa_dtype dtype, int B, int N, int C, int groups);
 
 /* Workspace bytes npa_global_query_attention_fwd uses for its full split

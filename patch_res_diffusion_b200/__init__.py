@@ -56,7 +56,7 @@ __all__ = [
     "DEBUG_ONLY_SYMBOLS", "NPA_ERR_DEVICE_BOUNDS", "use_bounds_checking", "npa_debug_withhold_arrival_once",
     "NPA_DTYPE_BF16", "NPA_DTYPE_FP16", "NPA_DTYPE_FP32", "NPA_ACT_NONE", "NPA_ACT_SILU", "KV8_BLOCK", "Kv8Cache",
     "npa_cross_attention_fwd", "npa_cross_attention_workspace_size", "npa_kv8_store", "npa_kv8_cross_attention_fwd",
-    "npa_group_norm_act", "npa_group_norm_workspace_size", "cross_attention", "kv8_store", "kv8_cross_attention",
+    "npa_group_norm_act", "npa_group_norm_workspace_size", "npa_device_ready", "cross_attention", "kv8_store", "kv8_cross_attention",
     "group_norm",
 ]
 
@@ -85,7 +85,7 @@ EXPORTED_SYMBOLS = (
     "npa_global_query_attention_fwd_noalloc", "npa_multidiffusion_attention_fwd",
     "npa_multidiffusion_workspace_size", "npa_multidiffusion_useful_flops", "asg_guidance_combine",
     "npa_cross_attention_fwd", "npa_cross_attention_workspace_size", "npa_kv8_store", "npa_kv8_cross_attention_fwd",
-    "npa_group_norm_act", "npa_group_norm_workspace_size",
+    "npa_group_norm_act", "npa_group_norm_workspace_size", "npa_device_ready",
 )
 # exported by the bounds-checking build only
 DEBUG_ONLY_SYMBOLS = ("npa_debug_withhold_arrival_once",)
@@ -161,6 +161,8 @@ def _load(path: str) -> ctypes.CDLL:
         st, kv8, f = ctypes.POINTER(_Strides), ctypes.POINTER(_Kv8Cache), ctypes.c_float
         L.npa_cross_attention_fwd.argtypes = [vp] * 4 + [i] * 7 + [st] * 4 + [vp, vp, f, vp, ctypes.c_size_t, vp]
         L.npa_cross_attention_fwd.restype = i
+        L.npa_device_ready.argtypes = []
+        L.npa_device_ready.restype = i
         L.npa_cross_attention_workspace_size.argtypes = [i] * 6
         L.npa_cross_attention_workspace_size.restype = ctypes.c_size_t
         L.npa_kv8_store.argtypes = [vp, vp, kv8] + [i] * 5 + [vp, i, st, st, vp]
@@ -323,6 +325,11 @@ def npa_cross_attention_fwd(q, k, v, o, dtype: int, B: int, heads: int, kv_heads
                                          _strides(o_strides), _ptr(kv_lens), _ptr(key_mask), scale, _ptr(workspace),
                                          int(workspace_bytes), _stream(stream)),
            "npa_cross_attention_fwd")
+
+
+def npa_device_ready() -> None:
+    """C ``npa_device_ready``: raises unless the current device runs this library."""
+    _check(lib().npa_device_ready(), "npa_device_ready")
 
 
 def npa_cross_attention_workspace_size(B, heads, kv_heads, Lq, Lk, d) -> int:
@@ -591,6 +598,15 @@ def _empty_bytes(n, like):
     return torch.empty(n, dtype=torch.uint8, device=like.device) if n else None
 
 
+def _planned_bytes(size, *args) -> int:
+    """A workspace size on the current device that may be kept: the 0 of a
+    device that could not be asked raises instead."""
+    nbytes = size(*args)
+    if not nbytes:
+        npa_device_ready()
+    return nbytes
+
+
 @functools.lru_cache(maxsize=1024)
 def _cross_plan(index, split, q_shape, q_strides, k_shape, k_strides, v_shape, v_strides, q_dtype, k_dtype, v_dtype):
     """(sizes, strides and a fresh output's strides for the C call, workspace bytes)."""
@@ -606,7 +622,7 @@ def _cross_plan(index, split, q_shape, q_strides, k_shape, k_strides, v_shape, v
         raise ValueError("q, k and v must have one dtype")
     nbytes = 0
     if split and index >= 0:
-        nbytes = npa_cross_attention_workspace_size(B, heads, kv_heads, Lq, Lk, d)   # of the current device: `index`
+        nbytes = _planned_bytes(npa_cross_attention_workspace_size, B, heads, kv_heads, Lq, Lk, d)   # on `index`
     return (code, B, heads, kv_heads, Lq, Lk, d), strides, _like_strides(q_shape, q_strides), nbytes
 
 
@@ -742,7 +758,7 @@ def _kv8_plan(index, split, q_shape, q_strides, cache_shape, Lk, q_dtype):
     strides = _heads_strides("q", q_shape, q_strides, (B, heads, Lq, d))
     _dtype_code(q_dtype, (NPA_DTYPE_BF16,))
     Lk = capacity if Lk is None else _int32("n_tokens", Lk)
-    nbytes = npa_cross_attention_workspace_size(B, heads, kv_heads, Lq, Lk, d) if split else 0   # current device: `index`
+    nbytes = _planned_bytes(npa_cross_attention_workspace_size, B, heads, kv_heads, Lq, Lk, d) if split else 0   # on `index`
     return (B, heads, kv_heads, Lq, Lk, d), strides, _like_strides(q_shape, q_strides), nbytes
 
 
@@ -799,7 +815,7 @@ def _norm_plan(index, groups, act, x_shape, x_strides, x_dtype, w_shape, w_strid
         raise ValueError("weight and bias must have one dtype")
     if C > 1 and x_strides[2] != 1:
         raise ValueError("channels must be contiguous")
-    nbytes = npa_group_norm_workspace_size(code, B, N, C, groups) if index >= 0 else 0   # of the current device: `index`
+    nbytes = _planned_bytes(npa_group_norm_workspace_size, code, B, N, C, groups) if index >= 0 else 0   # on `index`
     return (code, wcode, B, N, C, groups), x_strides[:2], _ACTIVATIONS[act], nbytes
 
 

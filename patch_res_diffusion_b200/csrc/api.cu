@@ -10,6 +10,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "npa.h"
@@ -57,17 +58,31 @@ struct DeviceState {
 };
 DeviceState g_dev[kMaxDevices];
 
-// Sets an attention kernel's shared-memory limit and checks that it was
-// compiled with the register count its warp roles redistribute: the softmax
-// warpgroups' setmaxnreg.inc draws on the registers the block was launched
-// with, and would never complete if the launch held fewer.
-template <int D, bool GQ, bool MD = false>
-bool prepare_kernel() {
-    using C = npa::KCfg<D, 2, 128>;
-    void (*kernel)(FwdParams) = npa::npa_fwd_kernel<D, 2, 128, GQ, MD>;
+// Sets a kernel's shared-memory limit and checks that it was compiled with the
+// register count its warp roles redistribute (0: none): the softmax warpgroups'
+// setmaxnreg.inc draws on the registers the block was launched with, and would
+// never complete if the launch held fewer. NPA_ERR_UNSUPPORTED is for good;
+// NPA_ERR_CUDA, a call that failed, is asked again next time.
+npa_status prepare(const void *kernel, int registers, int smem_bytes) {
     cudaFuncAttributes attr;
-    if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess || attr.numRegs != (int)C::kRegsLaunch) return false;
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) == cudaSuccess;
+    if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess) return NPA_ERR_CUDA;
+    if (registers && attr.numRegs != registers) return NPA_ERR_UNSUPPORTED;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes) == cudaSuccess
+               ? NPA_OK
+               : NPA_ERR_CUDA;
+}
+
+template <int D, bool GQ, bool MD = false>
+npa_status prepare_kernel() {
+    using C = npa::KCfg<D, 2, 128>;
+    return prepare((const void *)npa::npa_fwd_kernel<D, 2, 128, GQ, MD>, (int)C::kRegsLaunch, C::kSmemBytes);
+}
+
+// The first status that is not NPA_OK.
+npa_status first_fault(std::initializer_list<npa_status> all) {
+    for (const npa_status s : all)
+        if (s != NPA_OK) return s;
+    return NPA_OK;
 }
 
 // Resolves the tensor-map encoder and checks (once per device) that the
@@ -95,15 +110,13 @@ npa_status ensure_ready(int *sm_count = nullptr, int *l2_bytes = nullptr) {
         if (cudaDeviceGetAttribute(&ds.sm_count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
             ds.sm_count < 1 || cudaDeviceGetAttribute(&ds.l2_bytes, cudaDevAttrL2CacheSize, dev) != cudaSuccess)
             return NPA_ERR_CUDA;
-        if (major != 10 || minor != 0) {
-            ds.status = NPA_ERR_UNSUPPORTED;
-        } else if (!prepare_kernel<64, false>() || !prepare_kernel<128, false>() ||
-                   !prepare_kernel<64, false, true>() || !prepare_kernel<128, false, true>() ||
-                   !prepare_kernel<64, true>() || !prepare_kernel<128, true>()) {
-            ds.status = NPA_ERR_UNSUPPORTED;  // a kernel's compiled shape does not match its launch plan
-        } else {
-            ds.status = NPA_OK;
-        }
+        const npa_status st = major != 10 || minor != 0
+                                  ? NPA_ERR_UNSUPPORTED
+                                  : first_fault({prepare_kernel<64, false>(), prepare_kernel<128, false>(),
+                                                 prepare_kernel<64, false, true>(), prepare_kernel<128, false, true>(),
+                                                 prepare_kernel<64, true>(), prepare_kernel<128, true>()});
+        if (st == NPA_ERR_CUDA) return st;
+        ds.status = st;
         ds.checked = true;
     }
     if (sm_count) *sm_count = ds.sm_count;
@@ -595,24 +608,17 @@ double useful_flops(int B, int heads, int d, const Geo &g, int G) {
 // Cross attention, 16-bit keys or the 8-bit cache
 // ---------------------------------------------------------------------------
 template <int D, bool KV8, bool F16>
-bool prepare_xa_kernel() {
+npa_status prepare_xa_kernel() {
     using C = npa::XaCfg<D, KV8>;
-    void (*kernel)(npa::XaParams) = npa::xa_fwd_kernel<D, KV8, F16>;
-    cudaFuncAttributes attr;
-    if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess || attr.numRegs != (int)C::kRegsLaunch) return false;
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) == cudaSuccess;
+    return prepare((const void *)npa::xa_fwd_kernel<D, KV8, F16>, (int)C::kRegsLaunch, C::kSmemBytes);
 }
 
 constexpr int kMaxSmem = 227 * 1024;
 
 template <int D, bool F16>
-bool prepare_xs_kernel() {
+npa_status prepare_xs_kernel() {
     using C = npa::XsCfg<D>;
-    void (*kernel)(npa::XsParams) = npa::xa_short_kernel<D, F16>;
-    cudaFuncAttributes attr;
-    if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess) return false;
-    if (C::kSplitRegs && attr.numRegs != (int)C::kRegsLaunch) return false;
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) == cudaSuccess;
+    return prepare((const void *)npa::xa_short_kernel<D, F16>, C::kSplitRegs ? (int)C::kRegsLaunch : 0, kMaxSmem);
 }
 
 // xa_few_kernel's dynamic shared memory.
@@ -620,7 +626,7 @@ unsigned xf_smem(int d, int tiles) { return 8 * tiles * (npa::kXaFewWarps * (d +
 
 // How many clusters of each size run at once: out[size], of single blocks out[1].
 template <int D, bool KV8, int NT>
-bool count_xf_clusters(int (&out)[npa::kXaFewCluster + 1]) {
+npa_status count_xf_clusters(int (&out)[npa::kXaFewCluster + 1]) {
     const void *kernel = (const void *)npa::xa_few_kernel<D, KV8, false, NT>;
     for (int s = 1; s <= npa::kXaFewCluster; ++s) {
         cudaLaunchAttribute attr;
@@ -634,9 +640,10 @@ bool count_xf_clusters(int (&out)[npa::kXaFewCluster + 1]) {
         cfg.dynamicSmemBytes = xf_smem(D, NT);
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&out[s], kernel, &cfg) != cudaSuccess || out[s] < 1) return false;
+        if (cudaOccupancyMaxActiveClusters(&out[s], kernel, &cfg) != cudaSuccess) return NPA_ERR_CUDA;
+        if (out[s] < 1) return NPA_ERR_UNSUPPORTED;
     }
-    return true;
+    return NPA_OK;
 }
 
 // ensure_ready plus the cross-attention kernels' limits, once per device.
@@ -648,20 +655,21 @@ npa_status ensure_xa_ready(int *sm_count, const DeviceState **state = nullptr) {
     std::lock_guard<std::mutex> lock(g_mu);
     DeviceState &ds = g_dev[dev];
     if (!ds.xa_checked) {
-        const bool ok = prepare_xa_kernel<64, false, false>() && prepare_xa_kernel<64, false, true>() &&
-                        prepare_xa_kernel<128, false, false>() && prepare_xa_kernel<128, false, true>() &&
-                        prepare_xa_kernel<64, true, false>() && prepare_xa_kernel<128, true, false>() &&
-                        prepare_xs_kernel<64, false>() && prepare_xs_kernel<64, true>() &&
-                        prepare_xs_kernel<128, false>() && prepare_xs_kernel<128, true>() &&
-                        count_xf_clusters<64, false, 1>(ds.xf_clusters[0][0][0]) &&
-                        count_xf_clusters<64, false, 2>(ds.xf_clusters[0][0][1]) &&
-                        count_xf_clusters<64, true, 1>(ds.xf_clusters[0][1][0]) &&
-                        count_xf_clusters<64, true, 2>(ds.xf_clusters[0][1][1]) &&
-                        count_xf_clusters<128, false, 1>(ds.xf_clusters[1][0][0]) &&
-                        count_xf_clusters<128, false, 2>(ds.xf_clusters[1][0][1]) &&
-                        count_xf_clusters<128, true, 1>(ds.xf_clusters[1][1][0]) &&
-                        count_xf_clusters<128, true, 2>(ds.xf_clusters[1][1][1]);
-        ds.xa_status = ok ? NPA_OK : NPA_ERR_UNSUPPORTED;
+        const npa_status xa = first_fault(
+            {prepare_xa_kernel<64, false, false>(), prepare_xa_kernel<64, false, true>(),
+             prepare_xa_kernel<128, false, false>(), prepare_xa_kernel<128, false, true>(),
+             prepare_xa_kernel<64, true, false>(), prepare_xa_kernel<128, true, false>(), prepare_xs_kernel<64, false>(),
+             prepare_xs_kernel<64, true>(), prepare_xs_kernel<128, false>(), prepare_xs_kernel<128, true>(),
+             count_xf_clusters<64, false, 1>(ds.xf_clusters[0][0][0]),
+             count_xf_clusters<64, false, 2>(ds.xf_clusters[0][0][1]),
+             count_xf_clusters<64, true, 1>(ds.xf_clusters[0][1][0]),
+             count_xf_clusters<64, true, 2>(ds.xf_clusters[0][1][1]),
+             count_xf_clusters<128, false, 1>(ds.xf_clusters[1][0][0]),
+             count_xf_clusters<128, false, 2>(ds.xf_clusters[1][0][1]),
+             count_xf_clusters<128, true, 1>(ds.xf_clusters[1][1][0]),
+             count_xf_clusters<128, true, 2>(ds.xf_clusters[1][1][1])});
+        if (xa == NPA_ERR_CUDA) return xa;
+        ds.xa_status = xa;
         ds.xa_checked = true;
     }
     if (state) *state = &ds;  // not written again
@@ -1195,10 +1203,8 @@ bool gn_vectors(int C, npa_dtype dtype, const void *x, const void *y, const int6
 }
 
 template <typename T>
-bool prepare_gn_kernel() {
-    constexpr int kVec = 16 / sizeof(T);
-    return cudaFuncSetAttribute(npa::gn_cluster_kernel<T, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)kGnSlabBytes) == cudaSuccess;
+npa_status prepare_gn_kernel() {
+    return prepare((const void *)npa::gn_cluster_kernel<T, 16 / sizeof(T)>, 0, (int)kGnSlabBytes);
 }
 
 // ensure_ready plus the group norm kernels' shared memory, once per device.
@@ -1210,8 +1216,10 @@ npa_status ensure_gn_ready(int *sm_count) {
     std::lock_guard<std::mutex> lock(g_mu);
     DeviceState &ds = g_dev[dev];
     if (!ds.gn_checked) {
-        const bool ok = prepare_gn_kernel<__nv_bfloat16>() && prepare_gn_kernel<__half>() && prepare_gn_kernel<float>();
-        ds.gn_status = ok ? NPA_OK : NPA_ERR_CUDA;
+        const npa_status gn =
+            first_fault({prepare_gn_kernel<__nv_bfloat16>(), prepare_gn_kernel<__half>(), prepare_gn_kernel<float>()});
+        if (gn == NPA_ERR_CUDA) return gn;
+        ds.gn_status = gn;
         ds.gn_checked = true;
     }
     return ds.gn_status;
@@ -1452,6 +1460,12 @@ npa_status asg_guidance_combine(const void *eps, const void *eps_ref, const void
     const cudaError_t e =
         cudaLaunchKernel((const void *)npa::asg_combine_kernel, dim3(grid), dim3(256), args, 0, (cudaStream_t)stream);
     return e == cudaSuccess ? NPA_OK : NPA_ERR_CUDA;
+}
+
+npa_status npa_device_ready(void) {
+    int sm = 0;
+    const npa_status st = ensure_xa_ready(&sm);
+    return st != NPA_OK ? st : ensure_gn_ready(&sm);
 }
 
 size_t npa_cross_attention_workspace_size(int B, int heads, int kv_heads, int Lq, int Lk, int d) {
