@@ -506,7 +506,9 @@ def asg_combine(eps, eps_ref, mask, w_t: float, out=None, stream=None):
 # The steps around the self-attention. Some of these calls run for a few
 # microseconds, so what a call's shapes, strides and types decide - the checks,
 # the stride structures, the workspace's size - is worked out once for each
-# combination (the lru_cache'd functions) and looked up afterwards.
+# combination (the lru_cache'd functions) and looked up afterwards. What is
+# looked up by is made of plain numbers and types: a tensor given for a number
+# hashes by its identity, whatever it holds by then.
 # ---------------------------------------------------------------------------
 
 @functools.lru_cache(maxsize=None)
@@ -644,7 +646,7 @@ def cross_attention(q, k, v, kv_lens=None, key_mask=None, scale: Optional[float]
 
 def _cross_attention(index, q, k, v, kv_lens, key_mask, scale, out, split, handle):
     import torch
-    sizes, strides, o_strides, nbytes = _cross_plan(index, split, q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(),
+    sizes, strides, o_strides, nbytes = _cross_plan(index, bool(split), q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(),
                                                     q.dtype, k.dtype, v.dtype)
     lens = mask = None
     if kv_lens is not None or key_mask is not None:
@@ -771,7 +773,9 @@ def kv8_cross_attention(q, cache: Kv8Cache, n_tokens: Optional[int] = None, kv_l
 
 def _kv8_cross_attention(q, cache, n_tokens, kv_lens, key_mask, scale, out, split, handle):
     import torch
-    sizes, q_strides, o_strides, nbytes = _kv8_plan(cache.index, split, q.shape, q.stride(), cache.k.shape, n_tokens, q.dtype)
+    n_tokens = None if n_tokens is None else operator.index(n_tokens)   # a tensor would be looked up by its identity
+    sizes, q_strides, o_strides, nbytes = _kv8_plan(cache.index, bool(split), q.shape, q.stride(), cache.k.shape, n_tokens,
+                                                    q.dtype)
     lens = mask = None
     if kv_lens is not None or key_mask is not None:
         _kept_keys(kv_lens, key_mask, sizes[0], sizes[4])
@@ -836,7 +840,7 @@ def _group_norm(index, x, groups, weight, bias, eps, act, out, handle):
     import torch
     w = (None, None, None) if weight is None else (weight.shape, weight.stride(), weight.dtype)
     b = (None, None, None) if bias is None else (bias.shape, bias.stride(), bias.dtype)
-    sizes, xs, act_code, nbytes = _norm_plan(index, groups, act, x.shape, x.stride(), x.dtype, *w, *b)
+    sizes, xs, act_code, nbytes = _norm_plan(index, operator.index(groups), act, x.shape, x.stride(), x.dtype, *w, *b)
     _device_of(x, weight, bias, out)
     if out is None:
         out = torch.empty_like(x)

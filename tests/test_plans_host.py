@@ -59,3 +59,15 @@ def test_device_ready_on_this_machine():
             npa.npa_device_ready()
         with pytest.raises(npa.NpaError):
             npa.npa_device_ready()
+
+
+def test_groups_are_looked_up_as_a_number(monkeypatch):
+    seen = []
+    monkeypatch.setattr(npa, "_norm_plan", lambda index, groups, *rest: seen.append(groups) or (None, None, None, 0))
+    x = torch.zeros(1, 3, 64)
+    for g in (8, torch.tensor(8)):
+        with pytest.raises(ValueError):      # not on a GPU
+            npa.group_norm(x, g)
+    assert [type(g) for g in seen] == [int, int]
+    with pytest.raises(TypeError):
+        npa.group_norm(x, 8.0)
