@@ -309,8 +309,11 @@ typedef struct {
  * tokens; 1 when that is 0), and code = x / s rounded to the nearest e4m3
  * number, ties to even; infinities become +-448, NaN stays NaN. When the first
  * written token lies inside a block, the block's earlier tokens keep their
- * values: its scale is the larger of the old one and the new tokens', and if
- * it grows, the earlier codes are rounded again at it. Codes of tokens after
+ * values: its scale is the larger of the old one and the new tokens' (2^-126
+ * here where their amax is 0, so that zeros change nothing), and if it grows,
+ * the earlier codes are rounded again at it. An old scale that is no power of
+ * two stays one, and x times its rounded reciprocal is what is rounded then.
+ * Codes of tokens after
  * the last written one are left as they were (in a block whose scale is set
  * anew they then stand for other values). */
 npa_status npa_kv8_store(const void *k, const void *v, const npa_kv8_cache *cache, npa_dtype dtype, int B,

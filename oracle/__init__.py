@@ -438,7 +438,7 @@ def kv8_store(codes, scale, x, start: int, block: int = 64) -> None:
             amax = float(np.max(np.abs(piece[np.isfinite(piece)]), initial=0.0))
             if a > t0:
                 old = scale[h, blk]
-                s = max(old, kv8_scale(amax)) if amax > 0 else old
+                s = max(old, kv8_scale(amax) if amax > 0 else 2.0 ** -126)
                 if s != old:
                     codes[h, t0:a] = e4m3_round(codes[h, t0:a] * old / s)
             else:

@@ -9,7 +9,8 @@
 //
 // A block that starts inside (the first one, when `start` is not a multiple of
 // 64) keeps its earlier tokens: its scale is the larger of the old one and the
-// new tokens', and when it grows the earlier codes are rounded again at it.
+// new tokens' (of tokens without a finite number other than 0, the old one), and
+// when it grows the earlier codes are rounded again at it.
 // Codes past the last written token are left as they were.
 //
 // One block of 128 threads per (batch, head, 64 tokens, k or v): every element
@@ -124,7 +125,8 @@ __global__ void __launch_bounds__(128) kv8_store_kernel(const __grid_constant__ 
     amax = fmaxf(fmaxf(warp_max[0], warp_max[1]), fmaxf(warp_max[2], warp_max[3]));
     const float old = old_scale;
     float s = amax > 0.f ? kv8_scale(amax) : inside ? old : 1.f;
-    if (inside) s = fmaxf(s, old);
+    // a scale that nobody has set yet may be 0: 1 / s has to be finite
+    if (inside) s = fmaxf(fmaxf(s, old), 0x1p-126f);
     const float inv = 1.f / s;
     if (threadIdx.x == 0) *scale = s;
 #pragma unroll
