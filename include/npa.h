@@ -402,9 +402,10 @@ npa_status npa_selftest_wait_timeout(uint32_t limit_us, npa_stream_t stream);
 
 /* Bounds-checking build (libnpa_b200_debug.so, compiled with
  * NPA_DEBUG_BOUNDS; the pages have no counterpart, this is a debugging aid
- * standing in for a memory checker). Every kernel checks each TMA box origin
- * against its tensor's extent and each output row against the output's row
- * count; a failed check records NPA_ERR_DEVICE_BOUNDS in the status word,
+ * standing in for a memory checker). The kernels check each TMA box origin, or
+ * first key of a step, against its tensor's extent and each output row against
+ * the output's row count (the combines of partial results and of the guidance
+ * do so in every build); a failed check records NPA_ERR_DEVICE_BOUNDS in the status word,
  * clamps the load into the tensor or skips the store, and the kernel carries
  * on. The normal library has no checks and does not export the function
  * below.

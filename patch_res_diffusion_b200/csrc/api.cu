@@ -1582,6 +1582,7 @@ npa_status npa_kv8_store(const void *k, const void *v, const npa_kv8_cache *cach
     prm.n = n_tokens;
     prm.capacity = cache->capacity;
     prm.heads = kv_heads;
+    prm.rows = B * kv_heads;
     // blocks touched: counted from the first one's start, or, with starts on
     // the device, one more than the tokens alone need
     const long long span = starts ? (long long)n_tokens + npa::kKv8Block - 1 : start % npa::kKv8Block + (long long)n_tokens;

@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(32 * kXaFewWarps, xa_few_per_sm(D, NT)) xa_few
 
     W w;
     auto load_keys = [&](int step) {
-        const int key0 = step * W::kStep, n = len - key0;
+        const int key0 = bound_coord(step * W::kStep, p.Lk), n = len - key0;
         if (n >= W::kStep)
             w.template load_k<true>(kb + key0 * kst, kst, n, g);
         else
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(32 * kXaFewWarps, xa_few_per_sm(D, NT)) xa_few
         if (mask) w.mask_byte = lane < min(n, W::kStep) ? __ldg(mask + key0 + lane) : 0;
     };
     auto load_values = [&](int step) {
-        const int key0 = step * W::kStep, n = len - key0;
+        const int key0 = bound_coord(step * W::kStep, p.Lk), n = len - key0;
         if (n >= W::kStep)
             w.template load_v<true>(vb + key0 * vst, vst, n, t);
         else
@@ -454,9 +454,11 @@ __global__ void __launch_bounds__(32 * kXaFewWarps, xa_few_per_sm(D, NT)) xa_few
         } else if (p.n_splits > 1) {
             const size_t row = ((size_t)b * p.heads + h) * p.Lq + i;
             const size_t part = (size_t)split * p.B * p.heads * p.Lq + row;
+            if (!bound_row(true, part, (size_t)p.n_splits * p.B * p.heads * p.Lq)) continue;
             *reinterpret_cast<float2 *>(p.o_part + part * D + d) = make_float2(x, y);
             if (d == 0) *reinterpret_cast<float2 *>(p.ml + part * 2) = make_float2(m, L);
         } else {
+            if (!bound_row(true, ((size_t)b * p.heads + h) * p.Lq + i, (size_t)p.B * p.heads * p.Lq)) continue;
             const float inv = L > 0.f ? 1.f / L : L;
             uint16_t *dst = static_cast<uint16_t *>(p.o) + b * p.osb + h * p.osh + i * p.ost + d;
             *reinterpret_cast<uint32_t *>(dst) = L == 0.f ? 0u : sm100::pack_16x2<F16>(x * inv, y * inv);
@@ -491,6 +493,7 @@ __global__ void __launch_bounds__(32 * kXaFewWarps, xa_few_per_sm(D, NT)) xa_few
             y = fmaf(wgt, o[i].y, y);
         }
         const int hd = r / p.Lq, i = r - hd * p.Lq, h = kvh * p.group + hd;
+        if (!bound_row(true, ((size_t)b * p.heads + h) * p.Lq + i, (size_t)p.B * p.heads * p.Lq)) continue;
         const float inv = L > 0.f ? 1.f / L : L;
         uint16_t *dst = static_cast<uint16_t *>(p.o) + b * p.osb + h * p.osh + i * p.ost + d;
         *reinterpret_cast<uint32_t *>(dst) = L == 0.f ? 0u : sm100::pack_16x2<F16>(x * inv, y * inv);

@@ -439,14 +439,15 @@ __global__ void __launch_bounds__(kGnThreads) gn_cluster_kernel(const __grid_con
         if (lane == 0) mean_rstd[g] = q;
     });
     __syncthreads();
-    if (ty >= p.rows) return;
+    if (ty >= p.rows || !bound_row(true, c0 + tx * kVec + kVec - 1, (size_t)p.G * p.cpg)) return;
     f.statistics(p, mean_rstd, tx);
     T *dst = static_cast<T *>(p.y) + b * p.ysb + c0 + tx * kVec + (long long)(r0 + ty) * p.yst;
     const long long step = (long long)p.rows * p.yst;
     auto write = [&](auto silu) {
 #pragma unroll 4
         for (int k = 0; k < mine; ++k, dst += step, slab += threads)
-            *reinterpret_cast<Raw *>(dst) = f.template apply<decltype(silu)::value>(*slab);
+            if (bound_row(true, (size_t)r0 + ty + (size_t)k * p.rows, p.N))
+                *reinterpret_cast<Raw *>(dst) = f.template apply<decltype(silu)::value>(*slab);
     };
     if (p.silu)
         write(std::true_type{});
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_stats_kernel(const __grid_co
     }
     float2 *out = p.part + (size_t)b * p.G * p.tiles + tile;
     gn_groups_of_block(p, entry, tokens, [&](int g, int lane, float2 q) {
-        if (lane == 0) out[(size_t)g * p.tiles] = q;
+        if (bound_row(lane == 0, (size_t)g * p.tiles + tile, (size_t)p.G * p.tiles)) out[(size_t)g * p.tiles] = q;
     });
 }
 
@@ -526,6 +527,10 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_apply_kernel(const __grid_co
         const T *at = src;
         T *dst = out;
         int left = (tokens - ty + p.rows - 1) / p.rows;
+        // its last token and channel lie in the tensor
+        if (!bound_row(left > 0, (size_t)r0 + ty + (size_t)(left - 1) * p.rows, p.N) ||
+            !bound_row(true, (size_t)col * kVec + kVec - 1, (size_t)p.G * p.cpg))
+            left = 0;
         Raw raw[kGnBatch], next[kGnBatch];  // the next batch is on its way while one is written
         auto fetch = [&](Raw(&to)[kGnBatch]) {
 #pragma unroll

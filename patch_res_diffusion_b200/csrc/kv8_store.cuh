@@ -34,6 +34,7 @@ struct Kv8StoreParams {
     long long sb[2], sh[2], st[2];
     const int *starts;        // [B] or null: first token of each batch row (else start)
     int start, n, capacity, heads, n_blocks;
+    int rows;                 // batch rows times heads
 };
 
 // The smallest power of two s (at least 2^-126) with amax / s <= 448 = 1.75 * 2^8.
@@ -90,6 +91,8 @@ __global__ void __launch_bounds__(128) kv8_store_kernel(const __grid_constant__ 
     const long long blk = lo / kKv8Block + (rest - bh * p.n_blocks);
     const long long t0 = blk * kKv8Block;
     if (t0 >= hi) return;  // uniform over the block
+    // (uniform too) the block's tokens and its scale lie in the cache
+    if (!bound_row(true, (size_t)bh * p.capacity + t0 + kKv8Block - 1, (size_t)p.rows * p.capacity)) return;
     const uint16_t *x = static_cast<const uint16_t *>(p.x[t]) + b * p.sb[t] + h * p.sh[t];
     unsigned char *codes = p.codes[t] + ((size_t)bh * p.capacity + t0) * D;
     float *scale = p.scale[t] + (size_t)bh * (p.capacity / kKv8Block) + blk;
