@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -1015,7 +1016,8 @@ npa_status launch_xa(const XaCall &c, npa_stream_t stream) {
     prm.v_h = c.v.sh != 0;
     prm.n_qpairs = (Lq + 255) / 256;
     const double scale = c.scale > 0.f ? (double)c.scale : 1.0 / std::sqrt((double)d);
-    prm.scale_log2 = (float)(1.4426950408889634 * scale);
+    // (a scale near float32's largest: finite, so that scores of 0 stay 0)
+    prm.scale_log2 = (float)std::min(1.4426950408889634 * scale, (double)FLT_MAX);
     prm.wait_limit_ns = kWaitLimitNs;
     const long long units = (long long)B * heads * prm.n_qpairs;
     prm.n_units = (int)units;

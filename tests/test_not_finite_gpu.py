@@ -138,3 +138,24 @@ def test_cache(npa, way, d):
     bad[0, 0, Lk - 1, 9] = float("nan")
     out = run(q, k, bad)
     assert torch.isnan(out[0, :group, :, 9]).all()
+
+
+@pytest.mark.parametrize("scale", [3.4e38, 2.4e38, 1e-38, 1e-44])
+@pytest.mark.parametrize("way", ["one step", "cluster", "workspace", "at most 128 keys", "whole units", "cut units"])
+def test_scales_at_the_ends_of_float32(npa, way, scale):
+    """Scores that are all 0, or negligible, give the mean of the kept values."""
+    q, k, v, split = inputs(way, 64, "bf16", 45)
+    mask = torch.ones(q.shape[0], k.shape[2], dtype=torch.bool, device="cuda")
+    mask[:, 1::3] = False
+    if scale > 1:
+        q.zero_()
+    out = f64(npa.cross_attention(q, k, v, key_mask=mask, scale=scale, split=split))
+    keep = mask.cpu().numpy()
+    ref, mag = oracle.cross_attention(f64(q), f64(k), f64(v), keep=keep, scale=0.0)
+    assert (np.abs(out - ref) <= attention_bound(ref, mag, "bf16", k.shape[2], 6.0)).all()
+    cache = npa.Kv8Cache.empty(q.shape[0], k.shape[1], k.shape[2], 64)
+    npa.kv8_store(cache, k, v)
+    out = f64(npa.kv8_cross_attention(q, cache, k.shape[2], key_mask=mask, scale=scale, split=split))
+    vc = (f64(cache.v.float()) * np.repeat(f64(cache.v_scale), 64, axis=2)[..., None])[:, :, :k.shape[2]]
+    ref, mag = oracle.cross_attention(f64(q), f64(k), vc, keep=keep, scale=0.0)
+    assert (np.abs(out - ref) <= attention_bound(ref, mag, "bf16", k.shape[2], 6.0, True)).all()
