@@ -686,8 +686,6 @@ __device__ void xa_block_scales(const XaParams &p, uint8_t *smem, uint64_t *bars
             const int i0 = 2 * j, i1 = min(i0 + 1, p.scale_blocks - 1);  // past the cache: its keys are not kept
             const float ks[2] = {__ldg(p.k_scale + s0 + i0), __ldg(p.k_scale + s0 + i1)};
             const float vs[2] = {__ldg(p.v_scale + s0 + i0), __ldg(p.v_scale + s0 + i1)};
-            uint32_t w[4];
-            xa_keep(p, u, j, xa_block_keys(u, j), w);
             ok = !*abort_flag && sm100::mbar_wait_idle(&bars[C::bVCFull + cs], (kv / C::kCodeStages) & 1, lim);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -696,8 +694,17 @@ __device__ void xa_block_scales(const XaParams &p, uint8_t *smem, uint64_t *bars
             out.lift = 0;
             int tops = 0;
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h)
-                tops |= xa_codes_under_top<D>(codes + h * 64 * D, h ? w[2] : w[0], h ? w[3] : w[1], lane) << 8 * h;
+            for (int h = 0; h < 2; ++h) {
+                const int key = j * 128 + h * 64 + lane;  // this lane's first, the second 32 on
+                bool k0 = key < u.len, k1 = key + 32 < u.len;
+                if (p.key_mask) {
+                    const unsigned char *m = p.key_mask + (size_t)u.b * p.Lk + key;
+                    k0 = k0 && __ldg(m) != 0;
+                    k1 = k1 && __ldg(m + 32) != 0;
+                }
+                const uint32_t w0 = __ballot_sync(0xffffffffu, k0), w1 = __ballot_sync(0xffffffffu, k1);
+                tops |= xa_codes_under_top<D>(codes + h * 64 * D, w0, w1, lane) << 8 * h;
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int top = tops >> 8 * h & 255;
