@@ -259,7 +259,8 @@ typedef struct {
  * strides above; kv_lens: int32 [B] (device; values outside 0..Lk are
  * clamped) or NULL; key_mask: one byte per key, [B, Lk] contiguous (device) or
  * NULL. What k and v hold at keys that are not kept does not reach o, NaN and
- * infinities included. scale > 0, or 0 for 1/sqrt(d). d is 64 or 128; Lq and
+ * infinities included; NaN in a query or in a kept key or value shows in every
+ * output that the formula takes it to, however the call is split. scale > 0, or 0 for 1/sqrt(d). d is 64 or 128; Lq and
  * Lk are any sizes >= 1.
  * Arithmetic as for npa_attention_fwd; float16 inputs keep their probabilities
  * in float16 for the P.V product.
@@ -322,14 +323,15 @@ npa_status npa_kv8_store(const void *k, const void *v, const npa_kv8_cache *cach
 
 /* npa_cross_attention_fwd over the first Lk tokens of an 8-bit cache (Lk <=
  * capacity); q and o are bfloat16. The codes enter the products exactly (as
- * float16, with the probabilities) and the scales in float32; the scales of
+ * float16, with the probabilities) and the scales in float32; a query row is
+ * scaled by a power of two into float16, where elements below 2^-14 of its
+ * largest are off by up to 2^-25 of that. The scales of
  * blocks with kept keys must be positive and finite, powers of two or not, and
  * within one head those of the values less than 2^100 apart. A probability is
  * off by half a step of float16, or by 2^-30 of the largest product p |v| that
  * some 64 tokens' largest probability and largest kept value make, whichever
  * is more: blocks of zeros and tokens that are not kept do not count. Other
- * arguments,
- * results, workspace and errors as for npa_cross_attention_fwd. */
+ * arguments, results, workspace and errors as for npa_cross_attention_fwd. */
 npa_status npa_kv8_cross_attention_fwd(const void *q, const npa_kv8_cache *cache, void *o, int B, int heads,
                                        int kv_heads, int Lq, int Lk, int d, const npa_strides *q_strides,
                                        const npa_strides *o_strides, const int32_t *kv_lens, const uint8_t *key_mask,
@@ -344,7 +346,8 @@ typedef enum { NPA_ACT_NONE = 0, NPA_ACT_SILU = 1 } npa_activation;
  * [B, N, C], C contiguous, batch and token strides in elements (token strides
  * >= C; y's elements must not coincide); bfloat16, float16 or float32.
  * weight, bias: [C], of x's type or float32 (`weight_dtype`), or NULL for 1
- * and 0. groups divides C; C <= 4096. Statistics and arithmetic in float32.
+ * and 0. groups divides C; C <= 4096, B <= 65535. Statistics and arithmetic in
+ * float32.
  * y may be x itself (same strides) but must not otherwise overlap an input.
  * `workspace`: caller-owned device memory, 16-byte aligned, at least
  * npa_group_norm_workspace_size() bytes (0 for small tensors: NULL will do),

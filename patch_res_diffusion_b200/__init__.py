@@ -635,7 +635,8 @@ def cross_attention(q, k, v, kv_lens=None, key_mask=None, scale: Optional[float]
     with the last axis contiguous (a projection's ``[B, L, heads, d]`` seen
     through ``transpose(1, 2)``). What ``kv_lens`` (int32 [B]) or ``key_mask``
     (bool or uint8 [B, Lk], true: attend) leave out does not reach the output;
-    a row without keys gives zeros. ``scale`` defaults to 1/sqrt(d). With
+    a row without keys gives zeros. Forward only: the result carries no
+    gradient. ``scale`` defaults to 1/sqrt(d). With
     ``split`` a workspace is allocated so that the key range can be split
     across the GPU. Returns ``out`` (by default laid out like q)."""
     index = q.get_device()

@@ -787,10 +787,10 @@ XaPlan plan_xa(long long units, long long n_blk, int sm_count, bool cut) {
 // Key-range splits of xa_few_kernel. In steps of a warp: with the splits as a
 // cluster, the longest warp's, times the waves in which the clusters run; with
 // as many blocks as run at once and a merge through the workspace, the longest
-// warp's and about four more. (Cluster / workspace, us: 12.1 / 14.9 for 2 x 20
-// heads, 16 queries, 4111 keys at d = 64, where a warp has 5 or 3 steps; 23.1 /
-// 19.6 for one query over 16384 cached keys, 16 or 10 steps.) Without room for
-// the latter in the workspace, the former.
+// warp's and about four more. (Cluster / workspace, us, keys in L2: 12.0 / 14.9
+// for 2 x 20 heads, 16 queries, 4111 keys at d = 64, where a warp has 5 or 3 steps;
+// 22.5 / 19.2 for one query over 16384 cached keys, 16 or 10 steps. No third size
+// was compared.) Without room for the latter in the workspace, the former.
 struct XfPlan {
     int splits;
     bool cluster;

@@ -54,12 +54,15 @@
 // Lq; and Q is double buffered at d = 64, so that a short context (one block
 // per unit) streams queries and outputs at memory speed.
 //
-// Measured, bf16: 24 heads x 4096 x 16384 at d = 128 679 us (1,215 TFLOP/s; 754
-// in a longer run, under the power cap), tensor and exponential units 59% busy
-// each; 2 x 10 heads x 4096 x 9216 at d = 64 299 us (646 TFLOP/s),
-// exponential unit 66%; over the 8-bit cache 2 x 10 heads x 4096 x 12288
-// at d = 64 470 us (549 TFLOP/s), bound by the exponential unit (53%) and
-// by issue slots (47%): half of a block's scores are read twice.
+// Measured, bf16: 24 heads x 4096 x 16384 at d = 128 679 us (1,215 TFLOP/s; 745
+// to 754 in a longer run, under the power cap), tensor and exponential units 59%
+// busy each; 2 x 10 heads x 4096 x 9216 at d = 64 299 us (646 TFLOP/s),
+// exponential unit 66%; over the 8-bit cache 2 x 10 heads x 4096 x 12288 at d =
+// 64 464 us (555 TFLOP/s), exponential unit 52%, issue slots 47%, and 24 heads x
+// 2048 x 4096 at d = 128 169 us (610 TFLOP/s), no unit above 31%. No unit is
+// full: a tile's steps (S, softmax, P V) follow one another, two tiles fill a
+// multiprocessor's gaps in part, and half of a cached block's scores are read
+// twice.
 //
 // Tried and slower: dealing a one-tile piece's blocks to both warpgroups in
 // turn (77 queries of 24 heads x 4608 cached keys: 36 us instead of 29; the

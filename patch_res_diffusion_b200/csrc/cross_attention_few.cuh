@@ -30,9 +30,10 @@
 // memory, or, where more than eight of them pay, through a workspace and
 // xa_combine_kernel. The softmax reference moves lazily as in npa_fwd_kernel.cuh.
 //
-// Measured: 23 us for the size above (18 us of it this kernel, 4.6 TB/s, the
-// rest the merge and the launches), 15 us for 2 x 20 heads x 16 queries x 4111
-// masked 16-bit keys (42 MB, 6.5 us), 3.7 us for one query of 10 heads over 77 keys.
+// Measured with keys and values in DRAM, then in L2: 22.5 and 19.2 us for the size
+// above (17 to 18 us of it this kernel, the rest the merge and the launches), 14.8
+// and 12.6 us for 2 x 20 heads x 16 queries x 4111 masked 16-bit keys (42 MB, 6.5
+// us; 14.1 and 12.0 without a mask), 3.4 us for one query of 10 heads over 77 keys.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -42,9 +43,9 @@
 namespace npa {
 
 // Rows up to which this kernel runs: two 8-row tiles. Against xa_fwd_kernel
-// with its cut units (keys in L2): 16 x 4111 keys of 2 x 20 heads at d = 64 12.3
-// / 21.6 us, of 24 heads at d = 128 14.7 / 18.5; one query of 10 heads x 77 keys
-// 3.3 / 6.7; one query x 16384 cached keys of 2 x 20 heads 19.8 / 66.4.
+// with its cut units (keys in L2): 16 x 4111 keys of 2 x 20 heads at d = 64 12.0
+// / 21.6 us, of 24 heads at d = 128 14.5 / 18.5; one query of 10 heads x 77 keys
+// 3.3 / 6.7; one query x 16384 cached keys of 2 x 20 heads 19.2 / 66.4.
 constexpr int kXaFewRows = 16;
 constexpr int kXaFewWarps = 4;
 constexpr int kXaFewCluster = 8;  // splits that merge inside a cluster at most (the portable size)

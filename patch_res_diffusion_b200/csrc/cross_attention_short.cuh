@@ -22,8 +22,9 @@
 // Measured: 87 us for the size above (3.9 TB/s; the general kernel took 155, two
 // warpgroups that issue for themselves 107). No unit is busy more than 44% of
 // the time: what is left is each tile's chain (load, S, softmax, P V, store),
-// of which a multiprocessor has four under way. With 154 keys (two blocks) the
-// general kernel runs: 16 us for 2 x 10 heads x 4096 queries, d = 64.
+// of which a multiprocessor has four under way (S of a fifth would fit in the
+// tensor memory for 77 keys, its P beside O would not). With 154 keys (two
+// blocks) the general kernel runs: 17 us for 2 x 10 heads x 4096 queries, d = 64.
 #pragma once
 
 #include "cross_attention.cuh"

@@ -16,8 +16,10 @@
 //    tokens before it waits for that one. Cutting x into items that stay in L2
 //    between the passes was slower: 258 us instead of 182 for [2, 262144, 320]
 //    bf16, whose items of 42 MB leave each launch too little to do.
-//    180 us for that size: 64 for the statistics (5.4 TB/s), 110 for the rest
+//    179 us for that size: 64 for the statistics (5.4 TB/s), 110 for the rest
 //    (6.1 TB/s), where one pass that cannot be had would take 102.
+//    26 us for [2, 16384, 320] in float32 (84 MB, 12.8 us; both passes from L2),
+//    36 us for [2, 16384, 321] in bf16, one element to a load (42 MB).
 //    The cluster form takes 11 us for [2, 1024, 1280] in float16.
 //
 // Nothing is accumulated with atomics: results do not depend on the order in
@@ -48,7 +50,7 @@ namespace npa {
 
 constexpr int kGnThreads = 256;        // threads of a block at most
 constexpr int kGnMaxChannels = 4096;   // the block's statistics are kept in shared memory
-constexpr int kGnMaxTiles = 512;       // token tiles of an item at most
+constexpr int kGnMaxTiles = 512;       // token tiles of a batch row at most
 constexpr int kGnMaxCluster = 8;       // the portable cluster size
 constexpr int kGnBatch = 4;            // tokens that a thread takes at a time
 constexpr int kGnLanes = 8;            // lanes that merge one group's channels
