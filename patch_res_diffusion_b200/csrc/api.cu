@@ -1056,7 +1056,8 @@ npa_status launch_xa(const XaCall &c, npa_stream_t stream) {
     XaPlan pl = plan_xa(units, prm.n_blk, sm_count, true);
     if (pl.tail_ctas && (!c.workspace || c.workspace_bytes < xa_tail_bytes(pl.tail_ctas, d)))
         pl = plan_xa(units, prm.n_blk, sm_count, false);
-    prm.sort_rows = prm.kv_lens && B > 1 && B <= npa::kXaMaxSortedRows && units > sm_count;
+    prm.sort_rows = prm.kv_lens && B > 1 && B <= npa::kXaMaxSortedRows && units > sm_count &&
+                    prm.n_blk >= npa::xa_min_sorted_blocks(d);
     prm.waves = pl.waves;
     prm.tail_ctas = pl.tail_ctas;
     for (int i = 0; i <= pl.tail_ctas && pl.tail_ctas; ++i)

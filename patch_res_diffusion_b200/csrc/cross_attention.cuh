@@ -219,10 +219,14 @@ struct XaUnit {
 // have the same). Units run in this order: a CTA's whole units are then alike,
 // and the longest are those that are cut. (Lengths 12288 and 6144 in that order,
 // 2 x 10 heads x 4096 queries over the 8-bit cache: 460 us as the rows stand, 358
-// so. For short units the look at the lengths costs more than it gives: two
-// blocks, 2 x 10 heads x 4096 queries, 16.4 us as they stand, 18.1 sorted.)
+// so.) For short units the look at the lengths costs more than it gives. As they
+// stand / sorted, us, 4096 queries, all and half of the keys kept:
+//   blocks                          2          8          12         16         32
+//   d = 64, 2 x 10 heads        17 / 19    43 / 44    60 / 54    75 / 66  133 / 111
+//   the same over the cache     22 / 24    54 / 56    75 / 68    93 / 84  166 / 142
+//   d = 128, 2 x 12 heads       23 / 25    52 / 53    70 / 72    89 / 92  184 / 172
 constexpr int kXaMaxSortedRows = 8;
-constexpr int kXaMinSortedBlocks = 8;
+__host__ __device__ constexpr int xa_min_sorted_blocks(int d) { return d == 64 ? 12 : 32; }
 __device__ __forceinline__ int xa_row_of_rank(const int *kv_lens, int B, int Lk, int rank) {
     int row = 0;
     for (int b = 0; b < B; ++b) {
@@ -269,7 +273,7 @@ struct XaIter {
         u.b = p.by_heads(bh);
         u.h = bh - u.b * p.heads;
         u.kvh = p.by_group(u.h);
-        if (p.sort_rows && p.n_blk >= kXaMinSortedBlocks) u.b = xa_row_of_rank(p.kv_lens, p.B, p.Lk, u.b);
+        if (p.sort_rows) u.b = xa_row_of_rank(p.kv_lens, p.B, p.Lk, u.b);
         u.nt = p.Lq - u.row0 > 128 ? 2 : 1;
         u.len = p.kv_lens ? min(max(__ldg(p.kv_lens + u.b), 0), p.Lk) : p.Lk;
         u.je = min(je, (u.len + 127) / 128);
@@ -1442,7 +1446,7 @@ __global__ void __launch_bounds__(128) xa_tail_kernel(const __grid_constant__ Xa
     sm100::wait_for_previous_kernel();
     if (row >= p.Lq || c0 == c1) return;  // no row, or the unit was not cut
     const int rank = p.by_heads(bh), h = bh - rank * p.heads;
-    const int b = p.kv_lens && p.n_blk >= kXaMinSortedBlocks ? xa_row_of_rank(p.kv_lens, p.B, p.Lk, rank) : rank;
+    const int b = p.kv_lens ? xa_row_of_rank(p.kv_lens, p.B, p.Lk, rank) : rank;
     // a CTA's first piece is in its slot 0: of the unit's CTAs, only the first
     // may have begun with another unit
     const int begun = p.tail_start[c0] < t * p.n_blk;
