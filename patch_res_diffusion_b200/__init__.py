@@ -56,8 +56,8 @@ __all__ = [
     "DEBUG_ONLY_SYMBOLS", "NPA_ERR_DEVICE_BOUNDS", "use_bounds_checking", "npa_debug_withhold_arrival_once",
     "NPA_DTYPE_BF16", "NPA_DTYPE_FP16", "NPA_DTYPE_FP32", "NPA_ACT_NONE", "NPA_ACT_SILU", "KV8_BLOCK", "Kv8Cache",
     "npa_cross_attention_fwd", "npa_cross_attention_workspace_size", "npa_kv8_store", "npa_kv8_cross_attention_fwd",
-    "npa_group_norm_act", "npa_group_norm_workspace_size", "npa_device_ready", "cross_attention", "kv8_store", "kv8_cross_attention",
-    "group_norm",
+    "npa_group_norm_act", "npa_group_norm_workspace_size", "npa_device_ready", "cross_attention", "kv8_store",
+    "kv8_cross_attention", "group_norm",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnpa_b200.so")
@@ -647,8 +647,8 @@ def cross_attention(q, k, v, kv_lens=None, key_mask=None, scale: Optional[float]
 
 def _cross_attention(index, q, k, v, kv_lens, key_mask, scale, out, split, handle):
     import torch
-    sizes, strides, o_strides, nbytes = _cross_plan(index, bool(split), q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(),
-                                                    q.dtype, k.dtype, v.dtype)
+    sizes, strides, o_strides, nbytes = _cross_plan(index, bool(split), q.shape, q.stride(), k.shape, k.stride(), v.shape,
+                                                    v.stride(), q.dtype, k.dtype, v.dtype)
     lens = mask = None
     if kv_lens is not None or key_mask is not None:
         _kept_keys(kv_lens, key_mask, sizes[1], sizes[5])

@@ -40,7 +40,7 @@
 // (where a code of 128 or more is met, as in nearly every block's first rows,
 // that is 0 and the search ends); the converter takes it out of the value tile,
 // exactly, and the softmax adds it to the scale. Halves without a kept code
-// other than 0 count as 2^-60. A key's rounding is then at most 2^-30 of the
+// other than 0 count as 2^-80. A key's rounding is then at most 2^-30 of the
 // largest p |v| that some 64 tokens' largest p and largest kept |v| make.
 //   Scales are taken relative to that of the unit's first 64 tokens with values
 // (2^c), so that sums stay within float32 wherever the scales lie; between
@@ -118,8 +118,9 @@ struct XaParams {
     int sort_rows;  // batch rows in the order of their lengths
     int n_splits;   // xa_few_kernel: key-range splits
     // Partial results: unnormalised O [..][d], then reference and row sum
-    // [..][2] (over the 8-bit cache O / l, its logarithm and 1). Cut units: two slots of 256 rows per CTA (its first piece, its
-    // last); xa_few_kernel: [n_splits][B * heads * Lq].
+    // [..][2] (cut units over the 8-bit cache: O / l, reference plus log2 l, 1).
+    // Cut units: two slots of 256 rows per CTA (its first piece, its last);
+    // xa_few_kernel: [n_splits][B * heads * Lq].
     float *o_part, *ml;
 };
 
@@ -674,7 +675,10 @@ struct alignas(16) XaBlockScales {
     int lift;  // powers of two that the value tile's halves are multiplied by: bits 0-7, 8-15
 };
 static_assert(sizeof(XaBlockScales) == 32, "two 16-byte loads");
-constexpr float kXaNoValuesLog2 = -60.f;  // lv of 64 tokens that contribute nothing
+// lv of 64 tokens that contribute nothing: R follows them only where values have
+// less than 2^-80 of their probability, and a row sum over them alone stays below
+// 2^(80 + 15) times the number of keys.
+constexpr float kXaNoValuesLog2 = -80.f;
 
 template <int D>
 __device__ void xa_block_scales(const XaParams &p, uint8_t *smem, uint64_t *bars, volatile uint32_t *abort_flag) {

@@ -143,7 +143,20 @@ def scales_of_others(npa, Lq, n, split, d):
     attend_and_check(npa, q, cache, n, split=split, what="largest")
 
 
-CASES = [zero_blocks, unkept_sizes, grown_scales, far_apart, scales_of_others]
+def zeros_take_the_weight(npa, Lq, n, split, d):
+    """Nearly all of the probability on values of 0; what is left still counts."""
+    q, k, v = randn(16, 1, 2, Lq, d), randn(17, 1, 2, n, d), randn(18, 1, 2, n, d)
+    q[..., 0] = 8.0 * d ** 0.5
+    for zeros in (0, -(-n // 64) - 1):
+        x = v.clone()
+        x[:, :, 64 * zeros:64 * zeros + 64] = 0
+        for gap in (20.0, 50.0, 70.0, 95.0):
+            k[..., 0] = 0
+            k[:, :, 64 * zeros:64 * zeros + 64, 0] = gap / 8.0 * 0.6931
+            attend_and_check(npa, q, stored(npa, k, x), n, split=split, what=(zeros, gap))
+
+
+CASES = [zero_blocks, unkept_sizes, grown_scales, far_apart, scales_of_others, zeros_take_the_weight]
 
 
 @pytest.mark.parametrize("d", [64, 128])
