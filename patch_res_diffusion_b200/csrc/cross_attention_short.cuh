@@ -20,7 +20,7 @@
 // O leaves through the tile's own Q buffer, which the S product has read.
 //
 // Measured: 87 us for the size above (3.9 TB/s; the general kernel took 155, two
-// warpgroups that issue for themselves 107). No unit is busy more than 44% of
+// warpgroups that issue for themselves 107). No unit is busy more than 45% of
 // the time: what is left is each tile's chain (load, S, softmax, P V, store),
 // of which a multiprocessor has four under way (S of a fifth would fit in the
 // tensor memory for 77 keys, its P beside O would not). With 154 keys (two

@@ -16,7 +16,7 @@
 // One block of 128 threads per (batch, head, 64 tokens, k or v): every element
 // is read once, held in registers over the block-wide maximum, and written
 // once as 8 codes per store. 26 us for 2 x 10 heads x 16384 tokens x 64 (126 MB,
-// 4.8 TB/s, where a copy has 6.6: stores of 8 bytes a thread, issue slots 62%
+// 4.8 TB/s, where a copy has 6.6: stores of 8 bytes a thread, issue slots 60%
 // busy); one token appended takes 3.5 us, a launch.
 #pragma once
 
