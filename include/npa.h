@@ -329,9 +329,10 @@ npa_status npa_kv8_store(const void *k, const void *v, const npa_kv8_cache *cach
  * blocks with kept keys must be positive and finite, powers of two or not, and
  * within one head those of the values less than 2^100 apart. A probability is
  * off by half a step of float16, or by 2^-30 of the largest product p |v| that
- * some 64 tokens' largest probability and largest kept value make, whichever
- * is more: blocks of zeros and tokens that are not kept do not count. Other
- * arguments, results, workspace and errors as for npa_cross_attention_fwd. */
+ * some 64 tokens' largest probability and largest kept value make, or by 2^-109
+ * of the largest kept value, whichever is most: blocks of zeros and tokens that
+ * are not kept do not count. Other arguments, results, workspace and errors as
+ * for npa_cross_attention_fwd. */
 npa_status npa_kv8_cross_attention_fwd(const void *q, const npa_kv8_cache *cache, void *o, int B, int heads,
                                        int kv_heads, int Lq, int Lk, int d, const npa_strides *q_strides,
                                        const npa_strides *o_strides, const int32_t *kv_lens, const uint8_t *key_mask,

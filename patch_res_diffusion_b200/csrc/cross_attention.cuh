@@ -676,8 +676,9 @@ struct alignas(16) XaBlockScales {
 };
 static_assert(sizeof(XaBlockScales) == 32, "two 16-byte loads");
 // lv of 64 tokens that contribute nothing: R follows them only where values have
-// less than 2^-80 of their probability, and a row sum over them alone stays below
-// 2^(80 + 15) times the number of keys.
+// less than 2^-80 of their probability (a rounding is then 2^-25 2^-87 of the
+// unit's first values' scale, below 2^-109 of the largest value), and a row sum
+// over them alone stays below 2^(80 + 15) times the number of keys.
 constexpr float kXaNoValuesLog2 = -80.f;
 
 template <int D>
